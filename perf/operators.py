@@ -181,7 +181,9 @@ def _own(s):
     if s["op"] == "product":
         return iqq.gemm_i8(s["a_codes"], s["a_scales"], s["w_codes"], s["w_scales"], bias=s["bias_data"],
                            dtype=DTYPES[s["y"]])
-    cache = iqq.Kv8Cache(s["k_codes"], s["v_codes"], s["k_scales"], s["v_scales"])
+    if "cache" not in s:  # the handle that a program keeps for its cache's tensors
+        s["cache"] = iqq.Kv8Cache(s["k_codes"], s["v_codes"], s["k_scales"], s["v_scales"])
+    cache = s["cache"]
     if s["op"] == "append":
         iqq.iqq_kv8_append(cache, s["k_new"], s["v_new"], s["tables"], s["lens"], s["cu"])
         k, v = iqq.kv8_gather(cache, s["tables"], s["lens"], s["back"], s["total_back"], dtype=DTYPES[s["dtype"]])
