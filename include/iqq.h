@@ -427,6 +427,61 @@ iqq_status iqq_weighted_rmse(const float* x, const void* blocks, const float* qw
                              int64_t n_per_row, int64_t rows_per_qw, double* d_acc,
                              void* stream);
 
+/*
+ * Element types of the entry points that take a dtype argument.
+ */
+#define IQQ_F32 0
+#define IQQ_BF16 1
+#define IQQ_F16 2
+
+/*
+ * iqq_quantize_i8_rows -- 8-bit integer rows with one binary32 scale each: a scale for each
+ * token when the rows are activations, for each output channel when they are weights (the
+ * operands of iqq_gemm_i8).  Per row: amax = max|x|, d = fl32(amax / 127) (0 when amax <
+ * 2^-119), q = x / d rounded to the nearest integer, ties to even, exactly (the quotient is
+ * not rounded before; 0 when d = 0), so |q| <= 127.
+ *
+ *  dtype      IQQ_F32, IQQ_BF16 or IQQ_F16: the type of x.
+ *  x          nrows rows of n values, ldx values apart (ldx >= n; ignored for one row),
+ *             aligned to its type.  Rows on 16-byte boundaries are read 16 bytes at a time.
+ *  codes      int8 rows of n codes, ldc bytes apart (ldc >= n, ldc % 16 == 0; ignored for one
+ *             row), 16-byte aligned.  Bytes between a row's n codes and the next row are left
+ *             as they are.
+ *  scales     nrows binary32 scales, 4-byte aligned.
+ *  d_flags    optional; receives IQQ_FLAG_NONFINITE_INPUT.  A row that holds NaN or Inf gets
+ *             d = NaN and codes 0, so every product with it is NaN; other rows are exact.
+ * n == 0 with nrows > 0 is empty input: nothing is written.
+ */
+iqq_status iqq_quantize_i8_rows(int dtype, const void* x, int64_t ldx, int8_t* codes, int64_t ldc,
+                                float* scales, int64_t nrows, int64_t n, uint32_t* d_flags, void* stream);
+
+/*
+ * iqq_gemm_i8 -- y[t][r] = a_scales[t] * w_scales[r] * sum_j a[t][j] * w[r][j] (+ bias[r]):
+ * the matrix product of int8 rows with a scale for each token and each output channel.  The
+ * sum of the integer products is exact (32 bits hold it for k <= IQQ_GEMM_I8_MAX_K with any
+ * int8 codes, -128 included); it is converted to binary32, multiplied by a_scales[t], then by
+ * w_scales[r], then the bias is added, each step rounded to binary32, and the result is
+ * rounded once to the type of y.  The value of an output does not depend on n_tok, n_out or
+ * how the work is split.
+ *
+ *  a          int8 codes of n_tok tokens, rows lda bytes apart (lda >= k, lda % 16 == 0;
+ *             ignored for one row), 16-byte aligned.  Bytes behind a row's k codes are not used.
+ *  a_scales   n_tok binary32 scales.
+ *  w          int8 codes of n_out output channels, rows ldw bytes apart, as for a.
+ *  w_scales   n_out binary32 scales.
+ *  bias       optional, n_out binary32 values.
+ *  y_dtype    IQQ_F32, IQQ_BF16 or IQQ_F16: the type of y.
+ *  y          [n_tok] rows of n_out values, ldy values apart (ldy >= n_out; ignored for one
+ *             row), aligned to its type; must not overlap an input.  Values between the rows
+ *             are left as they are.
+ *  k          0 .. IQQ_GEMM_I8_MAX_K; k == 0 is the empty sum.
+ *  d_flags    optional; receives IQQ_FLAG_WAIT_TIMEOUT.
+ */
+#define IQQ_GEMM_I8_MAX_K 131071
+iqq_status iqq_gemm_i8(const int8_t* a, int64_t lda, const float* a_scales, const int8_t* w, int64_t ldw,
+                       const float* w_scales, const float* bias, int y_dtype, void* y, int64_t ldy,
+                       int64_t n_tok, int64_t n_out, int64_t k, uint32_t* d_flags, void* stream);
+
 /* Static description of a status code (never NULL). */
 const char* iqq_status_string(iqq_status status);
 

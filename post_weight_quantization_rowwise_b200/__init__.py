@@ -67,6 +67,8 @@ def _load():
                                      ctypes.c_size_t, _vp, _vp],
         "iqq_dequant_rmse_qx_bf16": [ctypes.c_int, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp],
         "iqq_dequant_rmse_q4_0_batch": [_vp, _i64, _vp, _vp],
+        "iqq_quantize_i8_rows": [ctypes.c_int, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp],
+        "iqq_gemm_i8": [_vp, _i64, _vp, _vp, _i64, _vp, _vp, ctypes.c_int, _vp, _i64, _i64, _i64, _i64, _vp, _vp],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -600,6 +602,135 @@ def iqq_weighted_rmse_qx(bits, x, blocks, qw, acc, rows_per_qw: int = 0, stream=
 
 
 # ----------------------------------------------------------------------------
+# 8-bit integer rows and their product
+# ----------------------------------------------------------------------------
+
+_DTYPES = {}  # torch dtype -> IQQ_F32, IQQ_BF16, IQQ_F16; filled on first use
+
+
+def _dtype_code(name, dtype) -> int:
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {dtype}")
+    return code
+
+
+def _launch(fn, x, stream, *args) -> None:
+    """Calls fn(*args, stream) on the device of x (made the current one for the call when it is
+    not) and checks the status; stream None is the current stream of that device."""
+    import torch
+    dev = x.device
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the data on {dev}")
+    call = getattr(_lib, fn)
+    if torch.cuda.current_device() == dev.index:
+        status = call(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = call(*args, stream.cuda_stream)
+    if status != 0:
+        raise IQQError(fn, status)
+
+
+def _empty(shape, dtype, device, stream):
+    """torch.empty for the output of a call on `stream`: allocated on that stream, so its
+    memory is reused only after what the stream has been given by then."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _need_rows(name, t, dtype=None) -> None:
+    """A CUDA matrix whose rows are contiguous (they may be further apart than their length)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with contiguous rows")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _need_vector(name, t, count, dtype, device) -> None:
+    if t is None:
+        return
+    if t.dtype != dtype or t.device != device or not t.is_contiguous() or t.numel() < count:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {count} values on {device}")
+
+
+def iqq_quantize_i8_rows(x, codes, scales, flags=None, stream=None):
+    """int8 codes and float32 scales (one a row) of x [nrows, n] float32, bfloat16 or float16.
+    The rows of x may be any distance apart; codes int8 [nrows, n] with rows a multiple of 16
+    bytes apart."""
+    import torch
+    _need_rows("x", x)
+    _need_rows("codes", codes, torch.int8)
+    code = _dtype_code("x", x.dtype)
+    nrows, n = x.shape
+    if codes.shape != x.shape:
+        raise ValueError(f"codes must be {tuple(x.shape)}, got {tuple(codes.shape)}")
+    _same_device(x, codes=codes)
+    _need_vector("scales", scales, nrows, torch.float32, x.device)
+    _need_vector("flags", flags, 1, torch.int32, x.device)
+    _launch("iqq_quantize_i8_rows", x, stream, code, x.data_ptr(), x.stride(0), codes.data_ptr(), codes.stride(0),
+            scales.data_ptr(), nrows, n, _at(flags))
+    return codes, scales
+
+
+def quantize_i8_rows(x, flags=None, stream=None):
+    """Allocates and returns (codes, scales) of x: int8 [nrows, n], rows padded to a multiple of
+    16 bytes in memory, and float32 [nrows]."""
+    import torch
+    nrows, n = _shape2(x)
+    codes = _empty((nrows, (n + 15) // 16 * 16), torch.int8, x.device, stream)
+    if codes.shape[1] != n:
+        codes = codes[:, :n]
+    scales = _empty((nrows,), torch.float32, x.device, stream)
+    return iqq_quantize_i8_rows(x, codes, scales, flags, stream)
+
+
+def iqq_gemm_i8(a_codes, a_scales, w_codes, w_scales, y, bias=None, flags=None, stream=None):
+    """y [n_tok, n_out] (float32, bfloat16 or float16) = a_codes [n_tok, k] @ w_codes [n_out, k].T,
+    scaled by a_scales [n_tok] and w_scales [n_out], plus bias [n_out] (float32)."""
+    import torch
+    _need_rows("a_codes", a_codes, torch.int8)
+    _need_rows("w_codes", w_codes, torch.int8)
+    _need_rows("y", y)
+    code = _dtype_code("y", y.dtype)
+    n_tok, k = a_codes.shape
+    n_out = w_codes.shape[0]
+    if w_codes.shape[1] != k or y.shape[0] != n_tok or y.shape[1] != n_out:
+        raise ValueError(f"a_codes {tuple(a_codes.shape)}, w_codes {tuple(w_codes.shape)} and y {tuple(y.shape)} "
+                         "do not fit")
+    _same_device(a_codes, w_codes=w_codes, y=y)
+    _need_vector("a_scales", a_scales, n_tok, torch.float32, a_codes.device)
+    _need_vector("w_scales", w_scales, n_out, torch.float32, a_codes.device)
+    _need_vector("bias", bias, n_out, torch.float32, a_codes.device)
+    _need_vector("flags", flags, 1, torch.int32, a_codes.device)
+    _launch("iqq_gemm_i8", a_codes, stream, a_codes.data_ptr(), a_codes.stride(0), a_scales.data_ptr(),
+            w_codes.data_ptr(), w_codes.stride(0), w_scales.data_ptr(), _at(bias), code, y.data_ptr(), y.stride(0),
+            n_tok, n_out, k, _at(flags))
+    return y
+
+
+def gemm_i8(a_codes, a_scales, w_codes, w_scales, bias=None, dtype=None, flags=None, stream=None):
+    """Allocates and returns y [n_tok, n_out] of iqq_gemm_i8 (dtype None: float32)."""
+    import torch
+    y = _empty((a_codes.shape[0], w_codes.shape[0]), dtype or torch.float32, a_codes.device, stream)
+    return iqq_gemm_i8(a_codes, a_scales, w_codes, w_scales, y, bias, flags, stream)
+
+
+# ----------------------------------------------------------------------------
 # conveniences
 # ----------------------------------------------------------------------------
 
@@ -732,4 +863,5 @@ def weighted_rmse(x, blocks, qw=None, rows_per_qw: int = 0, stream=None):
 
 
 __all__ = [n for n in dir() if n.startswith(("iqq_", "quantize", "dequant", "weighted", "Q", "FLAG",
-                                             "q4", "q8", "version", "status", "IQQError", "LIB", "Dequant"))]
+                                             "q4", "q8", "version", "status", "IQQError", "LIB", "Dequant",
+                                             "gemm_i8"))]
