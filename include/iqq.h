@@ -61,6 +61,8 @@ typedef enum {
 #define IQQ_FLAG_SCALE_OVERFLOW 4u  /* a finite Q4_0 scale rounded to +-Inf in fp16 */
 #define IQQ_FLAG_WAIT_TIMEOUT 8u    /* a staged copy did not arrive within the bounded
                                        wait (about 2 s); the results are unspecified  */
+#define IQQ_FLAG_BAD_INDEX 16u      /* a span, length or page number of a paged call is out of
+                                       range; what it names is left out (see the entry) */
 
 /* Block formats. */
 #define IQQ_Q4_0_BLOCK_VALUES 32
@@ -481,6 +483,113 @@ iqq_status iqq_quantize_i8_rows(int dtype, const void* x, int64_t ldx, int8_t* c
 iqq_status iqq_gemm_i8(const int8_t* a, int64_t lda, const float* a_scales, const int8_t* w, int64_t ldw,
                        const float* w_scales, const float* bias, int y_dtype, void* y, int64_t ldy,
                        int64_t n_tok, int64_t n_out, int64_t k, uint32_t* d_flags, void* stream);
+
+/*
+ * The paged 8-bit key/value cache: int8 codes with one binary32 scale for each page (a block
+ * of page_size tokens) and head, for keys and values apart; the value of a code is scale * q.
+ *
+ *  k_codes, v_codes    int8 [n_pages][n_kv_heads][page_size][head_dim], 16-byte aligned: a
+ *                      page's tokens of one head are one contiguous tile.
+ *  k_scales, v_scales  binary32 [n_pages][n_kv_heads], 4-byte aligned.
+ *  page_size           16, 32, 64 or 128.
+ *  head_dim            64 or 128.
+ */
+typedef struct iqq_kv8_cache {
+    int8_t* k_codes;
+    int8_t* v_codes;
+    float* k_scales;
+    float* v_scales;
+    int64_t n_pages;
+    int64_t n_kv_heads;
+    int64_t page_size;
+    int64_t head_dim;
+} iqq_kv8_cache;
+
+/*
+ * The sequences of a call, in device memory (4-byte aligned int32 arrays):
+ *  block_tables  [n_seqs] rows of table_width page numbers, table_stride apart (>= width):
+ *                token j of sequence b lies in page block_tables[b][j / page_size].
+ *  seq_lens      [n_seqs] tokens of each sequence in the cache, those of this call included.
+ *  cu_tokens     [n_seqs + 1] running counts: rows cu[b] .. cu[b+1]-1 of the call's packed
+ *                tensors (n_tokens rows) are the LAST n_b = cu[b+1] - cu[b] tokens of sequence
+ *                b, at positions seq_lens[b] - n_b and up.  n_b may be 0.
+ * Rows before cu[0] and behind cu[n_seqs] belong to no sequence: their outputs are left as
+ * they are (a batch padded at its end), so cu[0] is normally 0.
+ * The arrays are checked on the device: a span outside 0 .. n_tokens or of negative length, a
+ * length that is negative or beyond table_width * page_size, and a page number that is used
+ * and not in 0 .. n_pages-1 raise IQQ_FLAG_BAD_INDEX, and no memory is touched through them.
+ */
+typedef struct iqq_kv8_seqs {
+    const int32_t* block_tables;
+    int64_t table_stride;
+    int64_t table_width;
+    const int32_t* seq_lens;
+    const int32_t* cu_tokens;
+    int64_t n_seqs;
+} iqq_kv8_seqs;
+
+/*
+ * iqq_kv8_append -- quantizes new keys and values into the cache.  For every (page, head) that
+ * the new tokens reach: d_old is the scale it has, or 0 when the page's first token is among
+ * the new ones (the page is new: its old contents and scale are not used);
+ * d = max(d_old, fl32(amax / 127)) over the new values (amax < 2^-119 counts as 0); the codes
+ * of the tokens already in the page become rint(q * d_old / d) when d > d_old, at most half a
+ * step of d off each time the scale grows; the new codes are rint(x / d).  Both quotients are
+ * rounded exactly, ties to even, as in iqq_quantize_i8_rows.  Codes of tokens behind the
+ * sequence's last are left as they are.
+ *
+ *  dtype       IQQ_F32, IQQ_BF16 or IQQ_F16: the type of k and v.
+ *  k, v        [n_tokens][n_kv_heads][head_dim]: strides in values between tokens and between
+ *              heads, the head_dim values contiguous; 16-byte aligned, strides multiples of 16
+ *              bytes.
+ *  d_flags     optional; IQQ_FLAG_BAD_INDEX (a token without a place, seq_lens[b] < n_b among
+ *              them, is not stored) and IQQ_FLAG_NONFINITE_INPUT: a (page, head) that receives
+ *              NaN or Inf gets the scale NaN, which stays until the page is used anew.
+ * A page that two sequences of one call both write gets unspecified codes and scale.
+ */
+iqq_status iqq_kv8_append(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int dtype, const void* k,
+                          int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                          int64_t v_head_stride, int64_t n_tokens, uint32_t* d_flags, void* stream);
+
+/*
+ * iqq_kv8_gather -- reads cached tokens back: row cu[b] + i of k_out and v_out
+ * [n_tokens][n_kv_heads][head_dim] (contiguous, 16-byte aligned, of the given dtype) holds
+ * fl32(scale * q) of token seq_lens[b] - n_b + i of sequence b, rounded to the type.  With
+ * cu the running sums of seq_lens it is the whole cache.  A row whose token has no place
+ * (IQQ_FLAG_BAD_INDEX) is set to 0.
+ */
+iqq_status iqq_kv8_gather(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int dtype, void* k_out, void* v_out,
+                          int64_t n_tokens, uint32_t* d_flags, void* stream);
+
+/*
+ * iqq_kv8_attention -- causal attention of the call's tokens over the cached ones (append
+ * first, then attend).  For the i-th of the n_b tokens of sequence b and head h, which reads
+ * the key/value head h / (n_heads / n_kv_heads):
+ *     out = sum_j p_j v_j,  p = softmax_j(scale * q . k_j),  j <= seq_lens[b] - n_b + i,
+ * where k_j and v_j are the cache's values (scale * code).  One token a sequence is a decoding
+ * step; many are a prompt's chunk or drafted tokens.  A row that sees no token (n_b >
+ * seq_lens[b]) gives out = 0 and lse = -Inf.
+ *
+ *  dtype       IQQ_BF16 or IQQ_F16: the type of q and out.
+ *  q           [n_tokens][n_heads][head_dim], strides as for k of iqq_kv8_append.
+ *  out         [n_tokens][n_heads][head_dim] contiguous, 16-byte aligned.
+ *  lse         optional binary32 [n_tokens][n_heads]: log of the sum of exp(scale * q . k_j).
+ *  scale       finite; head_dim^-1/2 as a rule.
+ *  workspace   device memory of at least iqq_kv8_attention_workspace_bytes(...) bytes, 16-byte
+ *              aligned; may be NULL when that is 0.  Overwritten: one call at a time, and two
+ *              captured graphs that may run at the same time need one each.
+ *  d_flags     optional; IQQ_FLAG_BAD_INDEX (a page without a place, and tokens beyond
+ *              table_width * page_size, are not attended to; the rows of a bad span are left as
+ *              they are), IQQ_FLAG_WAIT_TIMEOUT.
+ * Scores and sums are binary32.  A narrower view of the block tables (table_width) bounds the
+ * lengths that the launch is laid out for.
+ */
+size_t iqq_kv8_attention_workspace_bytes(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int64_t n_heads,
+                                         int64_t n_tokens);
+iqq_status iqq_kv8_attention(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int dtype, const void* q,
+                             int64_t q_token_stride, int64_t q_head_stride, int64_t n_heads, int64_t n_tokens,
+                             void* out, float* lse, float scale, void* workspace, size_t workspace_bytes,
+                             uint32_t* d_flags, void* stream);
 
 /* Static description of a status code (never NULL). */
 const char* iqq_status_string(iqq_status status);

@@ -30,6 +30,8 @@ Q8_K128_BLOCK_BYTES = 140
 FLAG_NONFINITE_INPUT = 1
 FLAG_NEG_QW = 2
 FLAG_SCALE_OVERFLOW = 4
+FLAG_WAIT_TIMEOUT = 8
+FLAG_BAD_INDEX = 16
 
 STATUS = {0: "IQQ_OK", 1: "IQQ_ERR_NULL", 2: "IQQ_ERR_SHAPE", 3: "IQQ_ERR_ALIGN",
           4: "IQQ_ERR_CUDA", 5: "IQQ_ERR_ARG"}
@@ -68,6 +70,10 @@ def _load():
         "iqq_dequant_rmse_qx_bf16": [ctypes.c_int, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp],
         "iqq_dequant_rmse_q4_0_batch": [_vp, _i64, _vp, _vp],
         "iqq_quantize_i8_rows": [ctypes.c_int, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp],
+        "iqq_kv8_append": [_vp, _vp, ctypes.c_int, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _vp],
+        "iqq_kv8_gather": [_vp, _vp, ctypes.c_int, _vp, _vp, _i64, _vp, _vp],
+        "iqq_kv8_attention": [_vp, _vp, ctypes.c_int, _vp, _i64, _i64, _i64, _i64, _vp, _vp, ctypes.c_float, _vp,
+                              ctypes.c_size_t, _vp, _vp],
         "iqq_gemm_i8": [_vp, _i64, _vp, _vp, _i64, _vp, _vp, ctypes.c_int, _vp, _i64, _i64, _i64, _i64, _vp, _vp],
     }
     for name, args in sigs.items():
@@ -82,6 +88,8 @@ def _load():
     lib.iqq_version.restype = ctypes.c_char_p
     lib.iqq_quantize_qx_0_w_workspace_bytes.restype = ctypes.c_size_t
     lib.iqq_quantize_qx_0_w_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64]
+    lib.iqq_kv8_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.iqq_kv8_attention_workspace_bytes.argtypes = [_vp, _vp, _i64, _i64]
     return lib
 
 
@@ -731,6 +739,165 @@ def gemm_i8(a_codes, a_scales, w_codes, w_scales, bias=None, dtype=None, flags=N
 
 
 # ----------------------------------------------------------------------------
+# the paged 8-bit key/value cache
+# ----------------------------------------------------------------------------
+
+class _Kv8CacheStruct(ctypes.Structure):
+    """iqq_kv8_cache."""
+    _fields_ = [("k_codes", _vp), ("v_codes", _vp), ("k_scales", _vp), ("v_scales", _vp), ("n_pages", _i64),
+                ("n_kv_heads", _i64), ("page_size", _i64), ("head_dim", _i64)]
+
+
+class _Kv8SeqsStruct(ctypes.Structure):
+    """iqq_kv8_seqs."""
+    _fields_ = [("block_tables", _vp), ("table_stride", _i64), ("table_width", _i64), ("seq_lens", _vp),
+                ("cu_tokens", _vp), ("n_seqs", _i64)]
+
+
+class Kv8Cache:
+    """A paged key/value cache in int8: k_codes and v_codes int8 [n_pages, n_kv_heads, page_size,
+    head_dim], k_scales and v_scales float32 [n_pages, n_kv_heads], contiguous CUDA tensors of one
+    device.  The object holds the tensors; it copies nothing."""
+
+    def __init__(self, k_codes, v_codes, k_scales, v_scales):
+        import torch
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be [n_pages, n_kv_heads, page_size, head_dim]")
+        for name, t, dtype, shape in (("k_codes", k_codes, torch.int8, k_codes.shape),
+                                      ("v_codes", v_codes, torch.int8, k_codes.shape),
+                                      ("k_scales", k_scales, torch.float32, k_codes.shape[:2]),
+                                      ("v_scales", v_scales, torch.float32, k_codes.shape[:2])):
+            _need_cuda(name, t, dtype)
+            if t.shape != shape or t.device != k_codes.device:
+                raise ValueError(f"{name} must be {tuple(shape)} on {k_codes.device}, got {tuple(t.shape)} on {t.device}")
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.device = k_codes.device
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = map(int, k_codes.shape)
+        if self.page_size not in (16, 32, 64, 128) or self.head_dim not in (64, 128):
+            raise ValueError("page_size must be 16, 32, 64 or 128 and head_dim 64 or 128")
+        self._struct = _Kv8CacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
+                                       v_scales.data_ptr(), self.n_pages, self.n_kv_heads, self.page_size,
+                                       self.head_dim)
+        self._ref = ctypes.byref(self._struct)
+
+
+def kv8_cache(n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, device="cuda"):
+    """A Kv8Cache of newly allocated tensors (codes 0, scales 0)."""
+    import torch
+    shape = (n_pages, n_kv_heads, page_size, head_dim)
+    return Kv8Cache(torch.zeros(shape, dtype=torch.int8, device=device),
+                    torch.zeros(shape, dtype=torch.int8, device=device),
+                    torch.zeros(shape[:2], dtype=torch.float32, device=device),
+                    torch.zeros(shape[:2], dtype=torch.float32, device=device))
+
+
+def _kv8_seqs(cache, block_tables, seq_lens, cu_tokens):
+    """iqq_kv8_seqs of block_tables int32 [n_seqs, width] (rows any distance apart), seq_lens int32
+    [n_seqs] and cu_tokens int32 [n_seqs + 1], on the cache's device."""
+    import torch
+    n_seqs = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    if (block_tables.dim() != 2 or block_tables.shape[0] != n_seqs or block_tables.dtype != torch.int32
+            or block_tables.device != cache.device or (block_tables.shape[1] > 1 and block_tables.stride(1) != 1)):
+        raise ValueError(f"block_tables must be int32 [n_seqs, width] with contiguous rows on {cache.device}")
+    _need_vector("seq_lens", seq_lens, n_seqs, torch.int32, cache.device)
+    _need_vector("cu_tokens", cu_tokens, n_seqs + 1, torch.int32, cache.device)
+    return _Kv8SeqsStruct(block_tables.data_ptr(), block_tables.stride(0), block_tables.shape[1],
+                          seq_lens.data_ptr(), cu_tokens.data_ptr(), n_seqs)
+
+
+def _need_heads(name, t, cache, heads) -> None:
+    """[n_tokens, heads, head_dim] with contiguous heads, on the cache's device."""
+    if t.dim() != 3 or t.device != cache.device or t.shape[2] != cache.head_dim or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [n_tokens, heads, {cache.head_dim}] with contiguous heads on {cache.device}")
+    if heads is not None and t.shape[1] != heads:
+        raise ValueError(f"{name} must have {heads} heads, got {t.shape[1]}")
+
+
+def iqq_kv8_append(cache, k, v, block_tables, seq_lens, cu_tokens, flags=None, stream=None):
+    """Quantizes k and v [n_tokens, n_kv_heads, head_dim] (float32, bfloat16 or float16; tokens and
+    heads any multiple of 16 bytes apart) into the cache, as the last cu_tokens[b+1] - cu_tokens[b]
+    of the seq_lens[b] tokens of each sequence."""
+    import torch
+    _need_heads("k", k, cache, cache.n_kv_heads)
+    _need_heads("v", v, cache, cache.n_kv_heads)
+    code = _dtype_code("k", k.dtype)
+    if v.dtype != k.dtype or v.shape[0] != k.shape[0]:
+        raise ValueError("k and v must have the same type and number of tokens")
+    _need_vector("flags", flags, 1, torch.int32, cache.device)
+    seqs = _kv8_seqs(cache, block_tables, seq_lens, cu_tokens)
+    _launch("iqq_kv8_append", k, stream, cache._ref, ctypes.byref(seqs), code, k.data_ptr(), k.stride(0), k.stride(1),
+            v.data_ptr(), v.stride(0), v.stride(1), k.shape[0], _at(flags))
+
+
+def iqq_kv8_gather(cache, block_tables, seq_lens, cu_tokens, k_out, v_out, flags=None, stream=None):
+    """The values of the last cu_tokens[b+1] - cu_tokens[b] cached tokens of each sequence, into
+    k_out and v_out [n_tokens, n_kv_heads, head_dim] (contiguous; float32, bfloat16 or float16)."""
+    import torch
+    _need_heads("k_out", k_out, cache, cache.n_kv_heads)
+    code = _dtype_code("k_out", k_out.dtype)
+    if v_out.dtype != k_out.dtype or v_out.shape != k_out.shape or v_out.device != k_out.device:
+        raise ValueError("k_out and v_out must have the same type, shape and device")
+    if not k_out.is_contiguous() or not v_out.is_contiguous():
+        raise ValueError("k_out and v_out must be contiguous")
+    _need_vector("flags", flags, 1, torch.int32, cache.device)
+    seqs = _kv8_seqs(cache, block_tables, seq_lens, cu_tokens)
+    _launch("iqq_kv8_gather", k_out, stream, cache._ref, ctypes.byref(seqs), code, k_out.data_ptr(), v_out.data_ptr(),
+            k_out.shape[0], _at(flags))
+    return k_out, v_out
+
+
+def kv8_gather(cache, block_tables, seq_lens, cu_tokens, n_tokens: int, dtype=None, flags=None, stream=None):
+    """Allocates and returns (k, v) of iqq_kv8_gather; n_tokens is cu_tokens' last value (rows that
+    belong to no sequence are unspecified); dtype None: float32."""
+    import torch
+    shape = (n_tokens, cache.n_kv_heads, cache.head_dim)
+    k = _empty(shape, dtype or torch.float32, cache.device, stream)
+    v = _empty(shape, dtype or torch.float32, cache.device, stream)
+    return iqq_kv8_gather(cache, block_tables, seq_lens, cu_tokens, k, v, flags, stream)
+
+
+def kv8_attention_workspace_bytes(cache, n_seqs: int, table_width: int, n_heads: int, n_tokens: int) -> int:
+    """Device workspace iqq_kv8_attention needs (0: none)."""
+    seqs = _Kv8SeqsStruct(None, table_width, table_width, None, None, n_seqs)
+    return int(_lib.iqq_kv8_attention_workspace_bytes(cache._ref, ctypes.byref(seqs), n_heads, n_tokens))
+
+
+def iqq_kv8_attention(cache, q, block_tables, seq_lens, cu_tokens, out, lse=None, scale=None, workspace=None,
+                      flags=None, stream=None):
+    """Causal attention of q [n_tokens, n_heads, head_dim] (bfloat16 or float16), the last
+    cu_tokens[b+1] - cu_tokens[b] tokens of each sequence, over the cache, into out (contiguous,
+    like q) and lse (optional float32 [n_tokens, n_heads]).  scale None: head_dim ** -0.5.
+    workspace: uint8, kv8_attention_workspace_bytes; one for each call that may run at a time."""
+    import torch
+    _need_heads("q", q, cache, None)
+    code = _dtype_code("q", q.dtype)
+    if out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or not out.is_contiguous():
+        raise ValueError("out must be contiguous, of q's shape, type and device")
+    n_tokens, n_heads = q.shape[0], q.shape[1]
+    _need_vector("lse", lse, n_tokens * n_heads, torch.float32, cache.device)
+    _need_vector("flags", flags, 1, torch.int32, cache.device)
+    _need_vector("workspace", workspace, 0, torch.uint8, cache.device)
+    seqs = _kv8_seqs(cache, block_tables, seq_lens, cu_tokens)
+    _launch("iqq_kv8_attention", q, stream, cache._ref, ctypes.byref(seqs), code, q.data_ptr(), q.stride(0),
+            q.stride(1), n_heads, n_tokens, out.data_ptr(), _at(lse),
+            cache.head_dim ** -0.5 if scale is None else scale, _at(workspace),
+            0 if workspace is None else workspace.numel(), _at(flags))
+    return out
+
+
+def kv8_attention(cache, q, block_tables, seq_lens, cu_tokens, lse=None, scale=None, flags=None, stream=None):
+    """iqq_kv8_attention with the output (returned) and the workspace allocated here; rows of the
+    output that belong to no sequence are unspecified."""
+    import torch
+    if q.dim() != 3 or block_tables.dim() != 2:
+        raise ValueError("q must be [n_tokens, n_heads, head_dim] and block_tables [n_seqs, width]")
+    out = _empty(q.shape, q.dtype, q.device, stream)
+    need = kv8_attention_workspace_bytes(cache, block_tables.shape[0], block_tables.shape[1], q.shape[1], q.shape[0])
+    workspace = _empty((need,), torch.uint8, q.device, stream) if need else None
+    return iqq_kv8_attention(cache, q, block_tables, seq_lens, cu_tokens, out, lse, scale, workspace, flags, stream)
+
+
+# ----------------------------------------------------------------------------
 # conveniences
 # ----------------------------------------------------------------------------
 
@@ -864,4 +1031,4 @@ def weighted_rmse(x, blocks, qw=None, rows_per_qw: int = 0, stream=None):
 
 __all__ = [n for n in dir() if n.startswith(("iqq_", "quantize", "dequant", "weighted", "Q", "FLAG",
                                              "q4", "q8", "version", "status", "IQQError", "LIB", "Dequant",
-                                             "gemm_i8"))]
+                                             "gemm_i8", "kv8", "Kv8"))]

@@ -1,0 +1,396 @@
+"""The paged int8 key/value cache against plain forms in 64 bits.
+
+Append: scales and codes are exact by definition (correctly rounded quotients), so they are
+compared for equality, page after page.  Gather: fl(scale * code), rounded to the type once.
+
+Attention, with u = eps/2 of the output's type: the scores' dot products round in binary32
+(about head_dim + 4 roundings of terms that sum to S = sum |q k| scale, so a weight is off by
+the factor exp(+-2 (D+8) 2^-24 S)), the weights are rounded to the output's type or finer
+before they meet the values (a factor 1 +- u each), sums are binary32 and the result is rounded
+once (u).  Hence with V = sum_j p_j |v_j|
+    |out - o| <= V (u + 2 (D + 8) 2^-24 max S + (n_keys + 64) 2^-24) + u |o| (1 + u) + step.
+"""
+import math
+import random
+
+import pytest
+import torch
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
+
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+STEP = {BF16: 2.0 ** -133, F16: 2.0 ** -24}
+
+
+@pytest.fixture(scope="module")
+def iqq():
+    import post_weight_quantization_rowwise_b200 as m
+    return m
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _cu(new):
+    return _i32([sum(new[:b]) for b in range(len(new) + 1)])
+
+
+class Case:
+    """A cache of random codes and scales whose sequences hold lens tokens, pages in random order."""
+
+    def __init__(self, iqq, lens, kv, dim, page, seed, spare=3):
+        self.g = torch.Generator(device="cuda").manual_seed(seed)
+        counts = [-(-m // page) for m in lens]
+        order = list(range(sum(counts) + spare))
+        random.Random(seed).shuffle(order)
+        width = max(counts + [1]) + 1
+        rows, at = [], 0
+        for c in counts:
+            rows.append(order[at:at + c] + [0] * (width - c))
+            at += c
+        self.spare = order[at:]
+        self.tables = _i32(rows).reshape(len(lens), width)
+        self.lens, self.kv, self.dim, self.page = lens, kv, dim, page
+        shape = (len(order), kv, page, dim)
+        k, v = (torch.randint(-127, 128, shape, generator=self.g, device="cuda").to(torch.int8) for _ in range(2))
+        ks, vs = (torch.rand(shape[:2], generator=self.g, device="cuda") * 0.02 + 0.002 for _ in range(2))
+        self.cache = iqq.Kv8Cache(k, v, ks, vs)
+
+    def randn(self, *shape, dtype=F32):
+        return torch.randn(*shape, generator=self.g, device="cuda").to(dtype)
+
+    def values(self, b, which, head):
+        codes, scales = ((self.cache.k_codes, self.cache.k_scales), (self.cache.v_codes, self.cache.v_scales))[which]
+        cells = self.tables[b, :-(-self.lens[b] // self.page)].long()
+        return (codes[cells, head].double() * scales[cells, head].double()[:, None, None]).flatten(0, 1)[:self.lens[b]]
+
+
+def _append64(codes, scales, x, table, start, n, page):
+    """The definition for one sequence, in place, on the CPU, in 64 bits."""
+    if n == 0:
+        return
+    for p in range(start // page, -(-(start + n) // page)):
+        lo, hi = max(start, p * page), min(start + n, (p + 1) * page)
+        cell = table[p]
+        new = x[lo - start:hi - start].double()
+        amax = new.abs().amax((0, 2))
+        held = scales[cell].double() * (lo > p * page)
+        need = torch.where(amax < 2.0 ** -119, 0.0, (amax / 127).float().double())
+        d = torch.maximum(held, need)
+        safe = torch.where(d > 0, d, 1.0)[:, None, None]
+        old = codes[cell, :, :lo - p * page].double()
+        again = torch.round(old * held[:, None, None] / safe)
+        codes[cell, :, :lo - p * page] = torch.where((d > held)[:, None, None], again, old).to(torch.int8)
+        fresh = torch.where(d[:, None, None] > 0, torch.round(new.transpose(0, 1) / safe), 0.0)
+        codes[cell, :, lo - p * page:hi - p * page] = fresh.to(torch.int8)
+        scales[cell] = d.float()
+
+
+def _append_and_check(iqq, c, old, new, dtype, k=None, v=None, flags=None):
+    total = sum(new)
+    k = c.randn(total, c.kv, c.dim, dtype=dtype) if k is None else k
+    v = c.randn(total, c.kv, c.dim, dtype=dtype) * 3 if v is None else v
+    want = [t.cpu().clone() for t in (c.cache.k_codes, c.cache.k_scales, c.cache.v_codes, c.cache.v_scales)]
+    at, tables = 0, c.tables.tolist()
+    for b, n in enumerate(new):
+        for x, codes, scales in ((k, want[0], want[1]), (v, want[2], want[3])):
+            _append64(codes, scales, x[at:at + n].cpu(), tables[b], old[b], n, c.page)
+        at += n
+    iqq.iqq_kv8_append(c.cache, k, v, c.tables, _i32([a + b for a, b in zip(old, new)]), _cu(new), flags=flags)
+    for got, ref in zip((c.cache.k_codes, c.cache.k_scales, c.cache.v_codes, c.cache.v_scales), want):
+        assert torch.equal(got.cpu(), ref)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("page,dim,kv", [(16, 64, 1), (32, 128, 3), (64, 128, 2), (128, 64, 2), (128, 128, 1)])
+def test_append_exact(iqq, dtype, page, dim, kv):
+    """Sequences that begin, continue inside a page, end on and off page borders, take nothing,
+    and cross many pages; pages no new token reaches, and codes behind the last token, stay."""
+    old = [0, 0, 5, page - 1, page, page + 3, 7, 2 * page + 1]
+    new = [1, page, 1, 1, page, 3 * page + 5, 0, 40]
+    c = Case(iqq, [a + b for a, b in zip(old, new)], kv, dim, page, page + dim)
+    _append_and_check(iqq, c, old, new, dtype)
+
+
+def test_append_token_after_token(iqq):
+    """A page filled one token a call, its scale growing now and then."""
+    c = Case(iqq, [40, 33], 2, 64, 32, 5)
+    for i in range(33):
+        k = c.randn(2, 2, 64) * (1.0 + (i % 5))
+        _append_and_check(iqq, c, [i, i], [1, 1], F32, k=k, v=k * 2.0 ** -130 if i % 7 == 0 else k)
+
+
+def test_append_strided_and_ties(iqq):
+    """k and v as parts of one fused projection; values on and next to halves of the scale."""
+    c = Case(iqq, [70], 2, 64, 64, 6)
+    fused = c.randn(70, 8, 64, dtype=BF16)
+    _append_and_check(iqq, c, [0], [70], BF16, k=fused[:, 4:6], v=fused[:, 6:8])
+    half = (torch.arange(64, device="cuda") + 0.5) * 0.037
+    k = half.expand(70, 2, 64).clone()
+    k[:, :, 1::3] = torch.nextafter(k[:, :, 1::3], torch.zeros_like(k[:, :, 1::3]))
+    k[:, :, 63] = 127 * 0.037
+    _append_and_check(iqq, c, [0], [70], F32, k=k, v=-k)
+
+
+def test_append_nonfinite_and_bad_indices(iqq):
+    c = Case(iqq, [20, 20, 20], 2, 64, 16, 7)
+    k = c.randn(6, 2, 64)
+    k[0, 1, 3], k[3, 0, 0] = float("nan"), float("inf")
+    before = c.cache.k_scales.clone()
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    iqq.iqq_kv8_append(c.cache, k, k, c.tables, _i32([20, 20, 20]), _i32([0, 2, 4, 6]), flags=flags)
+    assert int(flags.item()) == iqq.FLAG_NONFINITE_INPUT
+    for b, h in ((0, 1), (1, 0)):
+        assert torch.isnan(c.cache.k_scales[c.tables[b, 1], h])
+    assert torch.isfinite(c.cache.k_scales[c.tables[0, 1], 0])
+    # every index that is refused on the device: nothing of the cache changes
+    good = (c.tables, _i32([20, 20, 20]), _i32([0, 2, 4, 6]))
+    for tables, lens, cu in ((torch.full_like(c.tables, -1), *good[1:]),
+                             (torch.full_like(c.tables, c.cache.n_pages), *good[1:]),
+                             (good[0], _i32([1, -5, 1]), good[2]),
+                             (good[0], good[1], _i32([9, 9, 12, 13])),
+                             (good[0], good[1], _i32([6, 4, 2, 0])),
+                             (good[0], _i32([10 ** 9] * 3), good[2])):
+        state = [t.clone() for t in (c.cache.k_codes, c.cache.v_codes, c.cache.k_scales, c.cache.v_scales)]
+        flags.zero_()
+        x = c.randn(6, 2, 64) * 50
+        iqq.iqq_kv8_append(c.cache, x, x, tables, lens, cu, flags=flags)
+        assert int(flags.item()) == iqq.FLAG_BAD_INDEX, (tables, lens, cu)
+        for t, was in zip((c.cache.k_codes, c.cache.v_codes, c.cache.k_scales, c.cache.v_scales), state):
+            assert torch.equal(t.nan_to_num(9.0), was.nan_to_num(9.0))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("page,dim,kv", [(16, 64, 1), (64, 128, 3)])
+def test_gather(iqq, dtype, page, dim, kv):
+    lens = [1, 100, page, 0, 3 * page + 1]
+    c = Case(iqq, lens, kv, dim, page, 8)
+    for new in (lens, [1, 7, 0, 0, page + 2]):
+        k = torch.full((sum(new) + 2, kv, dim), 7.0, dtype=dtype, device="cuda")
+        v = k.clone()
+        iqq.iqq_kv8_gather(c.cache, c.tables, _i32(lens), _cu(new), k, v)
+        assert (k[-2:] == 7.0).all() and (v[-2:] == 7.0).all()  # rows behind the last sequence
+        at = 0
+        for b, n in enumerate(new):
+            for h in range(kv):
+                for which, got in ((0, k), (1, v)):
+                    ref = c.values(b, which, h)[lens[b] - n:].float().to(dtype) if n else got[:0, 0]
+                    assert torch.equal(got[at:at + n, h], ref)
+            at += n
+
+
+def _attention64(c, b, h, group, q, n, scale):
+    """Outputs, lse and the error bound's parts (sum p |v|, largest sum |q k| scale) of n rows."""
+    k, v = c.values(b, 0, h // group), c.values(b, 1, h // group)
+    m = c.lens[b]
+    last = m - n + torch.arange(n, device="cuda")
+    seen = torch.arange(m, device="cuda")[None] <= last[:, None]
+    s = (q.double() @ k.t()) * scale
+    big = (q.double().abs() @ k.abs().t() * abs(scale)).amax(1) if m else torch.zeros(n, device="cuda").double()
+    s = s.masked_fill(~seen, -math.inf)
+    lse = torch.logsumexp(s, 1) if m else torch.full((n,), -math.inf, device="cuda").double()
+    p = torch.exp(s - torch.where(lse == -math.inf, 0.0, lse)[:, None])
+    return p @ v, lse, p @ v.abs(), big
+
+
+def _check_attention(iqq, c, new, heads, dtype, q=None, scale=None, pad=0):
+    total = sum(new)
+    q = c.randn(total + pad, heads, c.dim, dtype=dtype) if q is None else q
+    out = torch.full((total + pad, heads, c.dim), 7.0, dtype=dtype, device="cuda")
+    lse = torch.full((total + pad, heads), 7.0, device="cuda")
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    need = iqq.kv8_attention_workspace_bytes(c.cache, len(new), c.tables.shape[1], heads, total + pad)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda") if need else None
+    iqq.iqq_kv8_attention(c.cache, q, c.tables, _i32(c.lens), _cu(new), out, lse=lse, scale=scale, workspace=ws,
+                          flags=flags)
+    assert int(flags.item()) == 0
+    if pad:
+        assert (out[total:] == 7.0).all() and (lse[total:] == 7.0).all()
+    u, at = torch.finfo(dtype).eps / 2, 0
+    sc = c.dim ** -0.5 if scale is None else scale
+    for b, n in enumerate(new):
+        for h in range(heads):
+            o, l, mass, big = _attention64(c, b, h, heads // c.kv, q[at:at + n, h], n, sc)
+            keys = c.lens[b]
+            bound = mass * (u + 2 * (c.dim + 8) * 2.0 ** -24 * big[:, None] + (keys + 64) * 2.0 ** -24)
+            bound = bound + u * o.abs() * (1 + u) + STEP[dtype]
+            got = out[at:at + n, h].double()
+            assert ((got - o).abs() <= bound).all(), (b, h, float(((got - o).abs() - bound).max()))
+            gl = lse[at:at + n, h].double()
+            fine = torch.isfinite(l)
+            assert torch.equal(fine, torch.isfinite(gl)) and (gl[~fine] == -math.inf).all()
+            off = (gl - l).abs()[fine] - (2 * (c.dim + 8) * 2.0 ** -24 * big[fine] + (keys + 64) * 2.0 ** -24
+                                          + 2.0 ** -22 * l[fine].abs())
+            assert off.numel() == 0 or off.max() <= 0, float(off.max())
+        at += n
+    return out
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("page,dim,kv,group", [(16, 64, 2, 1), (32, 128, 1, 4), (64, 128, 2, 8), (128, 64, 1, 5),
+                                               (64, 64, 1, 16), (128, 128, 1, 3), (16, 128, 1, 24)])
+def test_attention_one_token(iqq, dtype, page, dim, kv, group):
+    """Lengths from one token, on and next to page and tile borders."""
+    lens = [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 300, 1000, 1025]
+    c = Case(iqq, lens, kv, dim, page, 11 + page)
+    _check_attention(iqq, c, [1] * len(lens), kv * group, dtype, pad=1)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("page,dim,kv,group", [(16, 64, 2, 1), (32, 128, 1, 4), (64, 128, 2, 2), (128, 64, 1, 5)])
+def test_attention_ragged_chunks(iqq, dtype, page, dim, kv, group):
+    """Chunks that are the whole sequence, its end, a few tokens, none, and longer than the
+    sequence (rows that see nothing)."""
+    lens = [1, 70, 300, 129, 64, 500, 257, 3, 0]
+    new = [1, 70, 5, 128, 0, 33, 200, 7, 2]
+    c = Case(iqq, lens, kv, dim, page, 13 + page)
+    out = _check_attention(iqq, c, new, kv * group, dtype, pad=3)
+    at = sum(new[:7])
+    assert (out[at:at + 4] == 0).all() and (out[at + 7:at + 9] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("lens,new,kv,group", [([9000], [1], 1, 4), ([40000], [1], 2, 8), ([5000, 3, 8111], [1, 1, 1], 1, 2),
+                                               ([3000], [1500], 1, 2), ([6100], [17], 2, 4)])
+def test_attention_long(iqq, dtype, lens, new, kv, group):
+    c = Case(iqq, lens, kv, 128, 64, 17)
+    _check_attention(iqq, c, new, kv * group, dtype)
+
+
+def test_attention_steep_scores_and_scale(iqq):
+    """Weights that one key takes almost whole, late and early, negative scale, scale 0."""
+    c = Case(iqq, [400, 90], 1, 64, 32, 19)
+    q = c.randn(2, 2, 64, dtype=BF16) * 8
+    for scale in (1.0, -0.5, 0.0, 2.0 ** -20):
+        _check_attention(iqq, c, [1, 1], 2, BF16, q=q, scale=scale)
+
+
+def test_attention_scales_of_pages(iqq):
+    """Pages of zeros (scale 0) and of scales many binades apart."""
+    for dtype in (BF16, F16):
+        c = Case(iqq, [300, 40], 2, 64, 16, 23)
+        c.cache.v_scales.mul_(torch.exp2(torch.randint(-12, 1, c.cache.v_scales.shape, generator=c.g, device="cuda").float()))
+        c.cache.k_scales.mul_(torch.exp2(torch.randint(-6, 2, c.cache.k_scales.shape, generator=c.g, device="cuda").float()))
+        for t in (c.cache.k_scales, c.cache.v_scales):
+            t[c.tables[0, 2]] = 0.0
+            t[c.tables[0, 18]] = 0.0
+        c.cache.v_scales[c.tables[1].long()] = 0.0
+        _check_attention(iqq, c, [9, 40], 4, dtype)
+
+
+def test_attention_nan_page_is_contained(iqq):
+    """A page whose scale is NaN makes NaN of the rows that see it, and of no others: rows that
+    end before the page, other heads, other sequences; pages behind the end are not looked at."""
+    c = Case(iqq, [100, 100], 2, 64, 16, 29)
+    c.cache.k_scales[c.tables[0, 4], 1] = float("nan")
+    c.cache.v_scales[c.tables[0, 5], 0] = float("nan")
+    c.cache.k_scales[c.spare] = float("nan")
+    q = c.randn(200, 4, 64, dtype=BF16)
+    out = iqq.kv8_attention(c.cache, q, c.tables, _i32([100, 100]), _i32([0, 100, 200]))
+    bad = torch.isnan(out).any(2)
+    want = torch.zeros_like(bad)
+    want[64:100, 2:] = True
+    want[80:100, :2] = True
+    assert torch.equal(bad, want)
+
+
+def test_attention_bad_indices_are_left_out(iqq):
+    c = Case(iqq, [100, 50], 1, 64, 16, 31)
+    q = c.randn(2, 2, 64, dtype=BF16)
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = (_i32([100, 50]), _i32([0, 1, 2]))
+    good = iqq.kv8_attention(c.cache, q, c.tables, *args, flags=flags)
+    assert int(flags.item()) == 0
+    bad = c.tables.clone()
+    bad[0, 3], bad[0, 6] = -7, 10 ** 6
+    out = iqq.kv8_attention(c.cache, q, bad, *args, flags=flags)
+    assert int(flags.item()) == iqq.FLAG_BAD_INDEX and torch.equal(out[1], good[1]) and torch.isfinite(out).all()
+    # the pages left out are hidden: the same as the 80 other tokens alone
+    flags.zero_()
+    keep = torch.cat([c.tables[:1, [0, 1, 2, 4, 5]], c.tables[1:, :5]])
+    short = iqq.kv8_attention(c.cache, q, keep, _i32([80, 50]), args[1])
+    torch.testing.assert_close(out.float(), short.float(), rtol=2.0 ** -7, atol=1e-3)
+    # a table too narrow for the length: its tokens only
+    out = iqq.kv8_attention(c.cache, q, c.tables[:, :4], *args, flags=flags)
+    assert int(flags.item()) == iqq.FLAG_BAD_INDEX
+    short = iqq.kv8_attention(c.cache, q, c.tables, _i32([64, 50]), args[1])
+    torch.testing.assert_close(out.float(), short.float(), rtol=2.0 ** -7, atol=1e-3)
+    # spans out of range: their rows stay as they were
+    for cu in ([0, 3, 2], [-4, 1, 2], [2, 1, 0]):
+        flags.zero_()
+        out = torch.full_like(q, 7.0)
+        ws = torch.empty(iqq.kv8_attention_workspace_bytes(c.cache, 2, c.tables.shape[1], 2, 2), dtype=torch.uint8, device="cuda")
+        iqq.iqq_kv8_attention(c.cache, q, c.tables, args[0], _i32(cu), out, workspace=ws, flags=flags)
+        assert int(flags.item()) == iqq.FLAG_BAD_INDEX
+        assert torch.isfinite(out).all()
+
+
+def test_attention_strided_q_and_offsets_past_32_bits(iqq):
+    """q as part of a fused projection; a cache larger than 4 GiB, its last pages in use."""
+    kv, dim, page = 8, 128, 128
+    n_pages = (1 << 32) // (kv * dim * page) + 40
+    codes = torch.zeros(2, n_pages, kv, page, dim, dtype=torch.int8, device="cuda")
+    tail = torch.randint(-127, 128, (2, 40, kv, page, dim), dtype=torch.int8, device="cuda")
+    codes[:, -40:] = tail
+    scales = torch.full((n_pages, kv), 0.01, device="cuda")
+    big = iqq.Kv8Cache(codes[0], codes[1], scales, scales.clone())
+    small = iqq.Kv8Cache(tail[0].contiguous(), tail[1].contiguous(), scales[-40:].clone(), scales[-40:].clone())
+    fused = torch.randn(3, 24, dim, device="cuda").to(BF16)
+    q, tables = fused[:, 8:24], torch.randperm(40, device="cuda")[:36].reshape(3, 12).to(torch.int32)
+    lens, cu = _i32([1500, 1, 700]), _i32([0, 1, 2, 3])
+    a = iqq.kv8_attention(big, q, tables + (n_pages - 40), lens, cu)
+    b = iqq.kv8_attention(small, q.contiguous(), tables, lens, cu)
+    assert torch.equal(a, b)
+    k, v = torch.randn(3, kv, dim, device="cuda"), torch.randn(3, kv, dim, device="cuda")
+    iqq.iqq_kv8_append(big, k, v, tables + (n_pages - 40), lens, cu)
+    iqq.iqq_kv8_append(small, k, v, tables, lens, cu)
+    assert torch.equal(big.k_codes[-40:], small.k_codes) and torch.equal(big.v_codes[-40:], small.v_codes)
+    ka, va = iqq.kv8_gather(big, tables + (n_pages - 40), lens, _cu([1500, 1, 700]), 2201)
+    kb, vb = iqq.kv8_gather(small, tables, lens, _cu([1500, 1, 700]), 2201)
+    assert torch.equal(ka, kb) and torch.equal(va, vb)
+
+
+def test_append_then_attend_as_a_model_does(iqq):
+    """A prompt and decoding steps through append and attention, captured as a graph with its
+    lengths on the device: each step's output against the values the cache then holds."""
+    kv, heads, dim, page = 2, 8, 128, 32
+    c = Case(iqq, [0, 0], kv, dim, page, 37, spare=20)
+    c.tables = _i32([c.spare[:8], c.spare[8:16]])
+    prompt = [45, 70]
+    k, v = c.randn(115, kv, dim, dtype=BF16), c.randn(115, kv, dim, dtype=BF16)
+    iqq.iqq_kv8_append(c.cache, k, v, c.tables, _i32(prompt), _cu(prompt))
+    c.lens = prompt
+    _check_attention(iqq, c, prompt, heads, BF16)
+    lens, cu = _i32(prompt), _i32([0, 1, 2])
+    k1, v1, q1 = (torch.zeros(2, n, dim, dtype=BF16, device="cuda") for n in (kv, kv, heads))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lens += 1
+        iqq.iqq_kv8_append(c.cache, k1, v1, c.tables, lens, cu)
+        out = iqq.kv8_attention(c.cache, q1, c.tables, lens, cu)
+    for step in range(40):
+        for t in (k1, v1, q1):
+            t.copy_(c.randn(*t.shape))
+        graph.replay()
+        c.lens = [m + step + 1 for m in prompt]
+        assert lens.tolist() == c.lens
+        eager = _check_attention(iqq, c, [1, 1], heads, BF16, q=q1)
+        assert torch.equal(out, eager)
+
+
+def test_attention_on_two_streams_at_once(iqq):
+    """Two calls on two streams, each with its own workspace, give what each gives alone."""
+    a, b = Case(iqq, [30000], 2, 128, 64, 41), Case(iqq, [20000, 9000], 2, 128, 64, 43)
+    qa, qb = a.randn(1, 8, 128, dtype=F16), b.randn(2, 8, 128, dtype=F16)
+    args_a, args_b = (a.tables, _i32(a.lens), _i32([0, 1])), (b.tables, _i32(b.lens), _i32([0, 1, 2]))
+    alone = iqq.kv8_attention(a.cache, qa, *args_a), iqq.kv8_attention(b.cache, qb, *args_b)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(10):
+        x = iqq.kv8_attention(a.cache, qa, *args_a, stream=s1)
+        y = iqq.kv8_attention(b.cache, qb, *args_b, stream=s2)
+        torch.cuda.synchronize()
+        assert torch.equal(x, alone[0]) and torch.equal(y, alone[1])
