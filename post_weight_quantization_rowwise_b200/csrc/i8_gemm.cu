@@ -2,85 +2,439 @@
 // channel, on sm_100a.
 //
 // y[t][r] = ((float(sum_j a[t][j] w[r][j]) * a_scales[t]) * w_scales[r]) + bias[r], the
-// integer sum exact in 32 bits.
+// integer sum exact in 32 bits, so neither the order of the sum nor its split changes a value.
+//
+// Both kernels run tcgen05.mma.kind::i8 from 128-byte-swizzled tiles that TMA brings in (k and
+// edge rows beyond the matrices arrive as zeros), with the output channels along the tensor
+// memory's lanes and the tokens along its columns: a warp of the epilogue then holds 32
+// neighbouring channels of one token and writes them as one run, whatever y's pitch and
+// alignment.  One warp loads, one issues the products, four carry the sums out.
+//
+//  pair kernel   tiles of 256 channels x up to 256 tokens by a pair of CTAs (cta_group::2: each
+//                holds half of both operands), persistent, two accumulators, so a tile's sums
+//                are carried out while the next one's products run.  Bound by the tensor cores.
+//  split kernel  tiles of 128 channels x up to 256 tokens, the k axis split over a cluster of up
+//                to 8 CTAs whose partial sums meet in shared memory: when tokens are few, the
+//                weights' bytes bound the product and every SM has to read its share of them.
+#include <algorithm>
+#include <atomic>
+
 #include "i8_code.cuh"
+#include "sm100.cuh"
 
 namespace {
 
-constexpr int kTile = 64, kStep = 64;  // 64x64 outputs a CTA, 64 bytes of k a step
+constexpr int kThreads = 192;        // warp 0 loads, warp 1 multiplies, warps 2..5 finish
+constexpr int kStep = 128;           // bytes of k a stage: one swizzle row
+constexpr int kRows = 128;           // channels a CTA
+constexpr int kABytes = kRows * kStep;
+constexpr int kMaxStages = 12;
+constexpr int kSmem = 227 * 1024 - 1024;  // beside the static shared memory
+constexpr int kSmemHalf = 112 * 1024;     // two CTAs an SM
 
 struct Args {
-    const int8_t* a;
     const float* as;
-    const int8_t* w;
     const float* ws;
     const float* bias;
     void* y;
-    int64_t lda, ldw, ldy, n_tok, n_out;
-    int k;
+    uint32_t* flags;
+    int64_t ldy, n_tok, n_out;
+    int64_t m_tiles, t_tiles;
+    int kblocks, tn, stages, split;
 };
 
-// 16 bytes of a row from byte j, zeros behind k.
-__device__ __forceinline__ uint4 load16(const int8_t* row, int j, int k)
+struct Bars {
+    uint64_t full[kMaxStages], empty[kMaxStages], done[2], taken[2];
+    uint32_t tmem;
+};
+
+__device__ __forceinline__ float finish(int sum, float da, float dw, float bias)
 {
-    if (j + 16 <= k) return __ldg(reinterpret_cast<const uint4*>(row + j));
-    uint32_t w[4];
+    return __fadd_rn(__fmul_rn(__fmul_rn(static_cast<float>(sum), da), dw), bias);
+}
+
+// Sixteen columns (tokens t ..) of this lane's channel r.
+template <class T>
+__device__ __forceinline__ void put16(const Args& P, const uint32_t (&v)[16], int64_t t, int64_t r, float dw, float bias)
+{
+    T* y = static_cast<T*>(P.y) + t * P.ldy + r;
+    const int n = P.n_tok - t < 16 ? static_cast<int>(P.n_tok - t) : 16;
+    if (r >= P.n_out) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        w[i] = 0u;
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-            if (j + 4 * i + b < k) w[i] |= static_cast<uint32_t>(static_cast<uint8_t>(row[j + 4 * i + b])) << (8 * b);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 16; ++i)
+        if (i < n) y[i * P.ldy] = iqq::from_f32<T>(finish(static_cast<int>(v[i]), __ldg(P.as + t + i), dw, bias));
+}
+
+// (0 + bias and no bias differ for no value but -0, which the product of a zero sum may have)
+__device__ __forceinline__ float bias_of(const Args& P, int64_t r)
+{
+    return P.bias != nullptr && r < P.n_out ? __ldg(P.bias + r) : 0.0f;
 }
 
 template <class T>
-__global__ void __launch_bounds__(256) i8_gemm_kernel(const Args P)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap, const Args P)
 {
-    __shared__ uint32_t sa[kTile][kStep / 4 + 1], sw[kTile][kStep / 4 + 1];
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kTile, t0 = static_cast<int64_t>(blockIdx.y) * kTile;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int lr = tid >> 2, lj = (tid & 3) * 16;
-    int acc[4][4] = {};
-    for (int j0 = 0; j0 < P.k; j0 += kStep) {
-        uint4 va = make_uint4(0, 0, 0, 0), vw = va;
-        if (t0 + lr < P.n_tok) va = load16(P.a + (t0 + lr) * P.lda, j0 + lj, P.k);
-        if (r0 + lr < P.n_out) vw = load16(P.w + (r0 + lr) * P.ldw, j0 + lj, P.k);
-        const int c = lj / 4;
-        sa[lr][c] = va.x; sa[lr][c + 1] = va.y; sa[lr][c + 2] = va.z; sa[lr][c + 3] = va.w;
-        sw[lr][c] = vw.x; sw[lr][c + 1] = vw.y; sw[lr][c + 2] = vw.z; sw[lr][c + 3] = vw.w;
-        __syncthreads();
-#pragma unroll 4
-        for (int i = 0; i < kStep / 4; ++i) {
-            int a[4], w[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                a[u] = static_cast<int>(sa[ty + 16 * u][i]);
-                w[u] = static_cast<int>(sw[tx + 16 * u][i]);
+    extern __shared__ uint8_t raw[];
+    __shared__ Bars S;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t base = (iqq::smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t rank = iqq::cluster_rank();
+    const int half = P.tn >> 1;
+    const uint32_t stage_bytes = kABytes + static_cast<uint32_t>(half) * kStep;
+    const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, tiles = P.m_tiles * P.t_tiles;
+    bool late = false;  // a wait of this thread ran out
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < P.stages; ++i) {
+            iqq::bar_init(iqq::smem_u32(&S.full[i]), 1);
+            iqq::bar_init(iqq::smem_u32(&S.empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            iqq::bar_init(iqq::smem_u32(&S.done[i]), 1);
+            iqq::bar_init(iqq::smem_u32(&S.taken[i]), 8);
+        }
+        iqq::bar_init_fence();
+        iqq::tma_prefetch_map(&wmap);
+        iqq::tma_prefetch_map(&amap);
+    }
+    if (warp == 1) iqq::tmem_alloc<2>(iqq::smem_u32(&S.tmem), 512);
+    iqq::tc_fence_before();
+    iqq::cluster_sync();
+    iqq::tc_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint32_t tmem = S.tmem;
+
+    if (warp == 0 && lane == 0) {
+        int64_t issued = 0;
+        int s = 0;
+        uint32_t ph = 0;
+        for (int64_t i = pair; i < tiles && !late; i += pairs) {
+            const int m0 = static_cast<int>(i / P.t_tiles) * 2 * kRows + static_cast<int>(rank) * kRows;
+            const int t0 = static_cast<int>(i % P.t_tiles) * P.tn + static_cast<int>(rank) * half;
+            for (int kb = 0; kb < P.kblocks; ++kb) {
+                if (!iqq::bar_wait(iqq::smem_u32(&S.empty[s]), ph ^ 1u)) {
+                    late = true;
+                    break;
+                }
+                const uint32_t bar = iqq::map_rank(iqq::smem_u32(&S.full[s]), 0), at = base + s * stage_bytes;
+                if (rank == 0) iqq::bar_expect(iqq::smem_u32(&S.full[s]), 2 * stage_bytes);
+                iqq::tma_load_pair(at, &wmap, kb * kStep, m0, bar);
+                iqq::tma_load_pair(at + kABytes, &amap, kb * kStep, t0, bar);
+                ++issued;
+                if (++s == P.stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
             }
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) acc[u][v] = __dp4a(a[u], w[v], acc[u][v]);
         }
-        __syncthreads();
-    }
-    T* y = static_cast<T*>(P.y);
+        // every copy has landed (the products waited for them) unless a wait ran out
+        if (rank == 0)
+            for (int64_t i = issued > P.stages ? issued - P.stages : 0; i < issued; ++i)
+                late |= !iqq::bar_wait(iqq::smem_u32(&S.full[i % P.stages]), static_cast<uint32_t>(i / P.stages) & 1u);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        const uint32_t idesc = iqq::idesc_i8(2 * kRows, P.tn);
+        int s = 0, turn = 0;
+        uint32_t ph = 0;
+        for (int64_t i = pair; i < tiles && !late; i += pairs, ++turn) {
+            const int buf = turn & 1;
+            late = !iqq::bar_wait(iqq::smem_u32(&S.taken[buf]), (static_cast<uint32_t>(turn >> 1) & 1u) ^ 1u);
+            iqq::tc_fence_after();
+            for (int kb = 0; kb < P.kblocks && !late; ++kb) {
+                if (!iqq::bar_wait(iqq::smem_u32(&S.full[s]), ph)) {
+                    late = true;
+                    break;
+                }
+                iqq::tc_fence_after();
+                const uint32_t at = base + s * stage_bytes;
+                const uint64_t a = iqq::desc_k128(at), b = iqq::desc_k128(at + kABytes);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const int64_t t = t0 + ty + 16 * u;
-        if (t >= P.n_tok) continue;
-        const float da = __ldg(P.as + t);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const int64_t r = r0 + tx + 16 * v;
-            if (r >= P.n_out) continue;
-            float o = __fmul_rn(__fmul_rn(static_cast<float>(acc[u][v]), da), __ldg(P.ws + r));
-            if (P.bias != nullptr) o = __fadd_rn(o, __ldg(P.bias + r));
-            y[t * P.ldy + r] = iqq::from_f32<T>(o);
+                for (int u = 0; u < kStep / 32; ++u)
+                    iqq::mma_i8<2>(tmem + buf * 256, a + 2 * u, b + 2 * u, idesc, kb > 0 || u > 0);
+                iqq::tc_commit<2>(iqq::smem_u32(&S.empty[s]));
+                if (++s == P.stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            iqq::tc_commit<2>(iqq::smem_u32(&S.done[buf]));
+        }
+    } else if (warp >= 2) {
+        const int quad = warp & 3;
+        int turn = 0;
+        for (int64_t i = pair; i < tiles; i += pairs, ++turn) {
+            const int buf = turn & 1;
+            const int64_t r = (i / P.t_tiles) * 2 * kRows + rank * kRows + quad * 32 + lane, t0 = (i % P.t_tiles) * P.tn;
+            const float dw = r < P.n_out ? __ldg(P.ws + r) : 0.0f, bias = bias_of(P, r);
+            late = !iqq::bar_wait(iqq::smem_u32(&S.done[buf]), static_cast<uint32_t>(turn >> 1) & 1u);
+            if (__any_sync(0xffffffffu, late)) break;
+            iqq::tc_fence_after();
+            const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * 256;
+            const int cols = P.n_tok - t0 < P.tn ? static_cast<int>(P.n_tok - t0) : P.tn;
+            for (int c = 0; c < cols; c += 16) {
+                uint32_t v[16];
+                iqq::tmem_ld16(at + c, v);
+                iqq::tmem_wait_ld();
+                put16<T>(P, v, t0 + c, r, dw, bias);
+            }
+            iqq::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) iqq::bar_arrive_cluster(iqq::map_rank(iqq::smem_u32(&S.taken[buf]), 0));
         }
     }
+    if (late) iqq::raise_flags(P.flags, IQQ_FLAG_WAIT_TIMEOUT);
+    __syncwarp();
+    iqq::tc_fence_before();
+    iqq::cluster_sync();  // the pair is done with each other's barriers and tensor memory
+    iqq::tc_fence_after();
+    if (warp == 1) iqq::tmem_free<2>(tmem, 512);
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads)
+split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap, const Args P,
+             const uint32_t columns)
+{
+    extern __shared__ uint8_t raw[];
+    __shared__ Bars S;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t base = (iqq::smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t rank = P.split > 1 ? iqq::cluster_rank() : 0u;
+    const uint32_t stage_bytes = kABytes + static_cast<uint32_t>(P.tn) * kStep;
+    const int64_t tile = blockIdx.x / static_cast<uint32_t>(P.split);
+    const int64_t m0 = (tile / P.t_tiles) * kRows, t0 = (tile % P.t_tiles) * P.tn;
+    // this CTA's part of the k axis
+    const int kb0 = static_cast<int>(static_cast<int64_t>(P.kblocks) * rank / P.split);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(P.kblocks) * (rank + 1) / P.split);
+    bool late = false;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < P.stages; ++i) {
+            iqq::bar_init(iqq::smem_u32(&S.full[i]), 1);
+            iqq::bar_init(iqq::smem_u32(&S.empty[i]), 1);
+        }
+        iqq::bar_init(iqq::smem_u32(&S.done[0]), 1);
+        iqq::bar_init_fence();
+        iqq::tma_prefetch_map(&wmap);
+        iqq::tma_prefetch_map(&amap);
+    }
+    if (warp == 1) iqq::tmem_alloc<1>(iqq::smem_u32(&S.tmem), columns);
+    iqq::tc_fence_before();
+    __syncthreads();
+    iqq::tc_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const uint32_t tmem = S.tmem;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // into L2 while the kernel before still runs (a line it then writes is written there)
+            for (int kb = kb0; kb < kb1 && kb < kb0 + 16; ++kb)
+                iqq::tma_prefetch_l2(&wmap, kb * kStep, static_cast<int>(m0));
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            int s = 0;
+            uint32_t ph = 0;
+            int issued = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!iqq::bar_wait(iqq::smem_u32(&S.empty[s]), ph ^ 1u)) {
+                    late = true;
+                    break;
+                }
+                const uint32_t bar = iqq::smem_u32(&S.full[s]), at = base + s * stage_bytes;
+                iqq::bar_expect(bar, stage_bytes);
+                iqq::tma_load(at, &wmap, kb * kStep, static_cast<int>(m0), bar);
+                iqq::tma_load(at + kABytes, &amap, kb * kStep, static_cast<int>(t0), bar);
+                ++issued;
+                if (++s == P.stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            // every copy has landed (the products waited for them) unless a wait ran out
+            for (int i = issued > P.stages ? issued - P.stages : 0; i < issued; ++i)
+                late |= !iqq::bar_wait(iqq::smem_u32(&S.full[i % P.stages]), static_cast<uint32_t>(i / P.stages) & 1u);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = iqq::idesc_i8(kRows, P.tn);
+            int s = 0;
+            uint32_t ph = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!iqq::bar_wait(iqq::smem_u32(&S.full[s]), ph)) {
+                    late = true;
+                    break;
+                }
+                iqq::tc_fence_after();
+                const uint32_t at = base + s * stage_bytes;
+                const uint64_t a = iqq::desc_k128(at), b = iqq::desc_k128(at + kABytes);
+#pragma unroll
+                for (int u = 0; u < kStep / 32; ++u)
+                    iqq::mma_i8<1>(tmem, a + 2 * u, b + 2 * u, idesc, kb > kb0 || u > 0);
+                iqq::tc_commit<1>(iqq::smem_u32(&S.empty[s]));
+                if (++s == P.stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            iqq::tc_commit<1>(iqq::smem_u32(&S.done[0]));
+        }
+    }
+    __syncwarp();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    late |= !iqq::bar_wait(iqq::smem_u32(&S.done[0]), 0);
+    __syncwarp();
+    iqq::tc_fence_after();
+
+    const int quad = warp & 3, row = quad * 32 + lane;
+    const int cols = P.n_tok - t0 < P.tn ? static_cast<int>(P.n_tok - t0) : P.tn;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    if (P.split == 1) {
+        if (warp >= 2) {
+            const int64_t r = m0 + row;
+            const float dw = r < P.n_out ? __ldg(P.ws + r) : 0.0f, bias = bias_of(P, r);
+            for (int c = 0; c < cols; c += 16) {
+                uint32_t v[16];
+                iqq::tmem_ld16(lanes + c, v);
+                iqq::tmem_wait_ld();
+                put16<T>(P, v, t0 + c, r, dw, bias);
+            }
+        }
+    } else {
+        // Column c belongs to the cluster's CTA floor(c * split / cols): everybody sends it its
+        // part, into the stages' memory (free once every CTA's products are done).
+        const int per = (cols + P.split - 1) / P.split;
+        iqq::cluster_sync();
+        if (warp >= 2) {
+            for (int c = 0; c < cols; c += 16) {
+                uint32_t v[16];
+                iqq::tmem_ld16(lanes + c, v);
+                iqq::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    if (c + i >= cols) break;
+                    const int owner = (c + i) * P.split / cols;
+                    const int first = (owner * cols + P.split - 1) / P.split;
+                    const uint32_t at = base + (((rank * per + (c + i - first)) * kRows + row) << 2);
+                    iqq::st_cluster(iqq::map_rank(at, static_cast<uint32_t>(owner)), v[i]);
+                }
+            }
+        }
+        __syncwarp();
+        iqq::cluster_sync();
+        const int first = (static_cast<int>(rank) * cols + P.split - 1) / P.split;
+        const int end = ((static_cast<int>(rank) + 1) * cols + P.split - 1) / P.split;
+        const uint32_t* part = reinterpret_cast<const uint32_t*>(raw + (base - iqq::smem_u32(raw)));
+        for (int i = threadIdx.x; i < (end - first) * kRows; i += kThreads) {
+            uint32_t sum = 0;
+            for (int src = 0; src < P.split; ++src) sum += part[src * per * kRows + i];
+            const int64_t t = t0 + first + i / kRows, r = m0 + i % kRows;
+            if (r < P.n_out)
+                static_cast<T*>(P.y)[t * P.ldy + r] =
+                    iqq::from_f32<T>(finish(static_cast<int>(sum), __ldg(P.as + t), __ldg(P.ws + r), bias_of(P, r)));
+        }
+    }
+    if (late) iqq::raise_flags(P.flags, IQQ_FLAG_WAIT_TIMEOUT);
+    iqq::tc_fence_before();
+    __syncthreads();
+    iqq::tc_fence_after();
+    if (warp == 1) iqq::tmem_free<1>(tmem, columns);
+}
+
+// k == 0: the empty sums.
+template <class T>
+__global__ void __launch_bounds__(256) empty_kernel(const Args P)
+{
+    const int64_t n = P.n_tok * P.n_out, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
+        const int64_t t = i / P.n_out, r = i % P.n_out;
+        static_cast<T*>(P.y)[t * P.ldy + r] = iqq::from_f32<T>(finish(0, P.as[t], P.ws[r], bias_of(P, r)));
+    }
+}
+
+iqq_status opt_in(const void* kernel, std::atomic<uint64_t>& done)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return iqq::launch_status();
+    const uint64_t bit = 1ULL << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return IQQ_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+        return iqq::launch_status();
+    if (dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+    return IQQ_OK;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Where the pair kernel runs (else the split kernel), and its token tile.
+bool plan_pair(Args& P, int sms)
+{
+    const int64_t m = ceil_div(P.n_out, 2 * kRows), pairs = sms / 2;
+    int64_t best = INT64_MAX;
+    for (int tn = 32; tn <= 256; tn += 32) {
+        const int64_t cost = ceil_div(m * ceil_div(P.n_tok, tn), pairs) * (tn + 24);
+        if (cost <= best) {
+            best = cost;
+            P.tn = tn;
+        }
+    }
+    P.m_tiles = m;
+    P.t_tiles = ceil_div(P.n_tok, P.tn);
+    return m * P.t_tiles * 2 > pairs && P.n_tok > 64;
+}
+
+template <class T>
+iqq_status launch(Args P, const int8_t* a, int64_t lda, const int8_t* w, int64_t ldw, int64_t k, cudaStream_t st)
+{
+    static std::atomic<uint64_t> pair_done{0}, split_done{0};
+    if (k == 0) {
+        empty_kernel<T><<<static_cast<unsigned>(std::min<int64_t>(ceil_div(P.n_tok * P.n_out, 256), 4096)), 256, 0, st>>>(P);
+        return iqq::launch_status();
+    }
+    const int sms = iqq::sm_count();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    CUtensorMap wmap, amap;
+    iqq_status s = iqq::byte_map(&wmap, w, k, P.n_out, ldw, kRows);
+    if (s != IQQ_OK) return s;
+    if (plan_pair(P, sms)) {
+        s = iqq::byte_map(&amap, a, k, P.n_tok, lda, P.tn / 2);
+        if (s == IQQ_OK) s = opt_in(reinterpret_cast<const void*>(pair_kernel<T>), pair_done);
+        if (s != IQQ_OK) return s;
+        P.stages = std::min<int>(kMaxStages, (kSmem - 1024 - static_cast<int>(sizeof(Bars))) / (kABytes + P.tn / 2 * kStep));
+        const int64_t pairs = std::min<int64_t>(P.m_tiles * P.t_tiles, sms / 2);
+        cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+        cfg.dynamicSmemBytes = kSmem - sizeof(Bars);  // the whole SM's: it takes the whole tensor memory
+        cudaLaunchKernelEx(&cfg, pair_kernel<T>, wmap, amap, P);
+        return iqq::launch_status();
+    }
+    P.tn = P.n_tok >= 256 ? 256 : static_cast<int>(ceil_div(P.n_tok, 16) * 16);
+    P.m_tiles = ceil_div(P.n_out, kRows);
+    P.t_tiles = ceil_div(P.n_tok, P.tn);
+    const int64_t tiles = P.m_tiles * P.t_tiles, slots = P.tn <= 64 ? 2 * sms : sms;
+    P.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, slots / tiles, static_cast<int64_t>(P.kblocks)})));
+    if (tiles * P.split > 0x7fffffffLL) return IQQ_ERR_SHAPE;
+    const int stage = kABytes + P.tn * kStep, room = (P.tn <= 64 ? kSmemHalf : kSmem - static_cast<int>(sizeof(Bars))) - 1024;
+    P.stages = std::min(kMaxStages, room / stage);
+    uint32_t columns = 32;
+    while (columns < static_cast<uint32_t>(P.tn)) columns *= 2;
+    s = iqq::byte_map(&amap, a, k, P.n_tok, lda, P.tn);
+    if (s == IQQ_OK) s = opt_in(reinterpret_cast<const void*>(split_kernel<T>), split_done);
+    if (s != IQQ_OK) return s;
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * P.split));
+    cfg.dynamicSmemBytes = static_cast<size_t>(P.stages * stage + 1024);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(P.split);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = P.split > 1 ? 2 : 1;
+    cudaLaunchKernelEx(&cfg, split_kernel<T>, wmap, amap, P, columns);
+    return iqq::launch_status();
 }
 
 }  // namespace
@@ -98,9 +452,10 @@ extern "C" iqq_status iqq_gemm_i8(const int8_t* a, int64_t lda, const float* a_s
         ldy = n_out;
     }
     if (n_out == 1) ldw = pitch;
-    if (lda < k || ldw < k || ldy < n_out || !iqq::size_ok(n_tok, lda > 0 ? lda : 1, 1) ||
-        !iqq::size_ok(n_out, ldw > 0 ? ldw : 1, 1) || !iqq::size_ok(n_tok, ldy, 4) || n_tok > 64LL * 65535 ||
-        n_out > 64LL * 0x7fffffff)
+    constexpr int64_t kMost = 0x7fffffff - 1024, kFar = (1LL << 40) - 16;  // a tile's coordinates and pitch
+    if (lda < k || ldw < k || ldy < n_out || n_tok > kMost || n_out > kMost || lda > kFar || ldw > kFar ||
+        !iqq::size_ok(n_tok, lda > 0 ? lda : 1, 1) || !iqq::size_ok(n_out, ldw > 0 ? ldw : 1, 1) ||
+        !iqq::size_ok(n_tok, ldy, 4))
         return IQQ_ERR_SHAPE;
     if (y == nullptr || a_scales == nullptr || w_scales == nullptr) return IQQ_ERR_NULL;
     if (k > 0 && (a == nullptr || w == nullptr)) return IQQ_ERR_NULL;
@@ -108,13 +463,20 @@ extern "C" iqq_status iqq_gemm_i8(const int8_t* a, int64_t lda, const float* a_s
         !iqq::aligned(w_scales, 4) || !iqq::aligned(bias, 4) || !iqq::aligned(d_flags, 4) ||
         !iqq::aligned(y, static_cast<uintptr_t>(iqq::dtype_bytes(y_dtype))))
         return IQQ_ERR_ALIGN;
-    const Args P = {a, a_scales, w, w_scales, bias, y, lda, ldw, ldy, n_tok, n_out, static_cast<int>(k)};
-    const dim3 grid(static_cast<unsigned>((n_out + kTile - 1) / kTile), static_cast<unsigned>((n_tok + kTile - 1) / kTile));
+    Args P = {};
+    P.as = a_scales;
+    P.ws = w_scales;
+    P.bias = bias;
+    P.y = y;
+    P.flags = d_flags;
+    P.ldy = ldy;
+    P.n_tok = n_tok;
+    P.n_out = n_out;
+    P.kblocks = static_cast<int>(ceil_div(k, kStep));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     switch (y_dtype) {
-    case IQQ_F32: i8_gemm_kernel<float><<<grid, 256, 0, st>>>(P); break;
-    case IQQ_BF16: i8_gemm_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(P); break;
-    default: i8_gemm_kernel<__half><<<grid, 256, 0, st>>>(P); break;
+    case IQQ_F32: return launch<float>(P, a, lda, w, ldw, k, st);
+    case IQQ_BF16: return launch<__nv_bfloat16>(P, a, lda, w, ldw, k, st);
+    default: return launch<__half>(P, a, lda, w, ldw, k, st);
     }
-    return iqq::launch_status();
 }

@@ -116,7 +116,8 @@ def _check(y, a, da, w, dw, bias):
 @pytest.mark.parametrize("n_tok,n_out,k", [
     (1, 1, 1), (1, 4096, 4096), (1, 130, 11000), (2, 257, 129), (5, 64, 16), (8, 300, 4095), (16, 11008, 1024),
     (17, 1000, 640), (33, 129, 2048), (64, 512, 14336), (65, 511, 333), (100, 4099, 256), (128, 128, 128),
-    (192, 640, 4096), (200, 300, 5000), (257, 513, 1000), (777, 1031, 2200), (1025, 260, 90), (3, 5, 131071)])
+    (192, 640, 4096), (200, 300, 5000), (257, 513, 1000), (777, 1031, 2200), (1025, 260, 90), (3, 5, 131071),
+    (2000, 3001, 300), (1100, 11008, 500), (5000, 2100, 140)])
 def test_gemm_shapes(iqq, dtype, n_tok, n_out, k):
     a, w = _codes(n_tok, k, 1 + k), _codes(n_out, k, 2 + n_out, pad=32)
     da = _rand((n_tok, 1), F32, 3)[:, 0].abs() * 1e-3 + 1e-5
