@@ -101,7 +101,9 @@ class _LazyLib:
     def __getattr__(self, name):
         if _LazyLib._handle is None:
             _LazyLib._handle = _load()
-        return getattr(_LazyLib._handle, name)
+        fn = getattr(_LazyLib._handle, name)
+        self.__dict__[name] = fn  # found without this method from now on
+        return fn
 
 
 _lib = _LazyLib()
@@ -626,21 +628,22 @@ def _dtype_code(name, dtype) -> int:
     return code
 
 
-def _launch(fn, x, stream, *args) -> None:
-    """Calls fn(*args, stream) on the device of x (made the current one for the call when it is
-    not) and checks the status; stream None is the current stream of that device."""
+def _launch(fn, index, stream, *args) -> None:
+    """Calls fn(*args, stream) with CUDA device `index` current and checks the status; stream None
+    is the current stream of that device."""
     import torch
-    dev = x.device
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the data on {dev}")
-    call = getattr(_lib, fn)
-    if torch.cuda.current_device() == dev.index:
-        status = call(*args, stream.cuda_stream)
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device_index != index:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the data on cuda:{index}")
     else:
-        with torch.cuda.device(dev):
-            status = call(*args, stream.cuda_stream)
+        handle = stream.cuda_stream
+    call = getattr(_lib, fn)
+    if torch.cuda.current_device() == index:
+        status = call(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = call(*args, handle)
     if status != 0:
         raise IQQError(fn, status)
 
@@ -659,21 +662,31 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _need_rows(name, t, dtype=None) -> None:
-    """A CUDA matrix whose rows are contiguous (they may be further apart than their length)."""
-    if not t.is_cuda:
+def _device_index(name, t) -> int:
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    return index
+
+
+def _rows(name, t, dtype, index):
+    """(rows, columns, distance of rows) of a matrix on CUDA device `index` whose rows are
+    contiguous (they may be further apart than their length)."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name} must be 2-D with contiguous rows")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+    return shape[0], shape[1], stride[0]
 
 
-def _need_vector(name, t, count, dtype, device) -> None:
+def _need_vector(name, t, count, dtype, index) -> None:
     if t is None:
         return
-    if t.dtype != dtype or t.device != device or not t.is_contiguous() or t.numel() < count:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {count} values on {device}")
+    if t.dtype is not dtype or t.get_device() != index or t.numel() < count or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {count} values on cuda:{index}")
 
 
 def iqq_quantize_i8_rows(x, codes, scales, flags=None, stream=None):
@@ -681,16 +694,15 @@ def iqq_quantize_i8_rows(x, codes, scales, flags=None, stream=None):
     The rows of x may be any distance apart; codes int8 [nrows, n] with rows a multiple of 16
     bytes apart."""
     import torch
-    _need_rows("x", x)
-    _need_rows("codes", codes, torch.int8)
+    index = _device_index("x", x)
+    nrows, n, ldx = _rows("x", x, None, index)
+    crows, cn, ldc = _rows("codes", codes, torch.int8, index)
     code = _dtype_code("x", x.dtype)
-    nrows, n = x.shape
-    if codes.shape != x.shape:
-        raise ValueError(f"codes must be {tuple(x.shape)}, got {tuple(codes.shape)}")
-    _same_device(x, codes=codes)
-    _need_vector("scales", scales, nrows, torch.float32, x.device)
-    _need_vector("flags", flags, 1, torch.int32, x.device)
-    _launch("iqq_quantize_i8_rows", x, stream, code, x.data_ptr(), x.stride(0), codes.data_ptr(), codes.stride(0),
+    if crows != nrows or cn != n:
+        raise ValueError(f"codes must be {(nrows, n)}, got {(crows, cn)}")
+    _need_vector("scales", scales, nrows, torch.float32, index)
+    _need_vector("flags", flags, 1, torch.int32, index)
+    _launch("iqq_quantize_i8_rows", index, stream, code, x.data_ptr(), ldx, codes.data_ptr(), ldc,
             scales.data_ptr(), nrows, n, _at(flags))
     return codes, scales
 
@@ -711,23 +723,19 @@ def iqq_gemm_i8(a_codes, a_scales, w_codes, w_scales, y, bias=None, flags=None, 
     """y [n_tok, n_out] (float32, bfloat16 or float16) = a_codes [n_tok, k] @ w_codes [n_out, k].T,
     scaled by a_scales [n_tok] and w_scales [n_out], plus bias [n_out] (float32)."""
     import torch
-    _need_rows("a_codes", a_codes, torch.int8)
-    _need_rows("w_codes", w_codes, torch.int8)
-    _need_rows("y", y)
+    index = _device_index("a_codes", a_codes)
+    n_tok, k, lda = _rows("a_codes", a_codes, torch.int8, index)
+    n_out, kw, ldw = _rows("w_codes", w_codes, torch.int8, index)
+    ytok, yout, ldy = _rows("y", y, None, index)
     code = _dtype_code("y", y.dtype)
-    n_tok, k = a_codes.shape
-    n_out = w_codes.shape[0]
-    if w_codes.shape[1] != k or y.shape[0] != n_tok or y.shape[1] != n_out:
-        raise ValueError(f"a_codes {tuple(a_codes.shape)}, w_codes {tuple(w_codes.shape)} and y {tuple(y.shape)} "
-                         "do not fit")
-    _same_device(a_codes, w_codes=w_codes, y=y)
-    _need_vector("a_scales", a_scales, n_tok, torch.float32, a_codes.device)
-    _need_vector("w_scales", w_scales, n_out, torch.float32, a_codes.device)
-    _need_vector("bias", bias, n_out, torch.float32, a_codes.device)
-    _need_vector("flags", flags, 1, torch.int32, a_codes.device)
-    _launch("iqq_gemm_i8", a_codes, stream, a_codes.data_ptr(), a_codes.stride(0), a_scales.data_ptr(),
-            w_codes.data_ptr(), w_codes.stride(0), w_scales.data_ptr(), _at(bias), code, y.data_ptr(), y.stride(0),
-            n_tok, n_out, k, _at(flags))
+    if kw != k or ytok != n_tok or yout != n_out:
+        raise ValueError(f"a_codes {(n_tok, k)}, w_codes {(n_out, kw)} and y {(ytok, yout)} do not fit")
+    _need_vector("a_scales", a_scales, n_tok, torch.float32, index)
+    _need_vector("w_scales", w_scales, n_out, torch.float32, index)
+    _need_vector("bias", bias, n_out, torch.float32, index)
+    _need_vector("flags", flags, 1, torch.int32, index)
+    _launch("iqq_gemm_i8", index, stream, a_codes.data_ptr(), lda, a_scales.data_ptr(), w_codes.data_ptr(), ldw,
+            w_scales.data_ptr(), _at(bias), code, y.data_ptr(), ldy, n_tok, n_out, k, _at(flags))
     return y
 
 
@@ -771,7 +779,7 @@ class Kv8Cache:
             if t.shape != shape or t.device != k_codes.device:
                 raise ValueError(f"{name} must be {tuple(shape)} on {k_codes.device}, got {tuple(t.shape)} on {t.device}")
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
-        self.device = k_codes.device
+        self.device, self.index = k_codes.device, k_codes.get_device()
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = map(int, k_codes.shape)
         if self.page_size not in (16, 32, 64, 128) or self.head_dim not in (64, 128):
             raise ValueError("page_size must be 16, 32, 64 or 128 and head_dim 64 or 128")
@@ -795,22 +803,21 @@ def _kv8_seqs(cache, block_tables, seq_lens, cu_tokens):
     """iqq_kv8_seqs of block_tables int32 [n_seqs, width] (rows any distance apart), seq_lens int32
     [n_seqs] and cu_tokens int32 [n_seqs + 1], on the cache's device."""
     import torch
-    n_seqs = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
-    if (block_tables.dim() != 2 or block_tables.shape[0] != n_seqs or block_tables.dtype != torch.int32
-            or block_tables.device != cache.device or (block_tables.shape[1] > 1 and block_tables.stride(1) != 1)):
-        raise ValueError(f"block_tables must be int32 [n_seqs, width] with contiguous rows on {cache.device}")
-    _need_vector("seq_lens", seq_lens, n_seqs, torch.int32, cache.device)
-    _need_vector("cu_tokens", cu_tokens, n_seqs + 1, torch.int32, cache.device)
-    return _Kv8SeqsStruct(block_tables.data_ptr(), block_tables.stride(0), block_tables.shape[1],
-                          seq_lens.data_ptr(), cu_tokens.data_ptr(), n_seqs)
+    n_seqs, width, stride = _rows("block_tables", block_tables, torch.int32, cache.index)
+    if seq_lens.dim() != 1 or seq_lens.shape[0] != n_seqs:
+        raise ValueError(f"seq_lens must be [{n_seqs}], as block_tables has rows")
+    _need_vector("seq_lens", seq_lens, n_seqs, torch.int32, cache.index)
+    _need_vector("cu_tokens", cu_tokens, n_seqs + 1, torch.int32, cache.index)
+    return _Kv8SeqsStruct(block_tables.data_ptr(), stride, width, seq_lens.data_ptr(), cu_tokens.data_ptr(), n_seqs)
 
 
-def _need_heads(name, t, cache, heads) -> None:
-    """[n_tokens, heads, head_dim] with contiguous heads, on the cache's device."""
-    if t.dim() != 3 or t.device != cache.device or t.shape[2] != cache.head_dim or t.stride(2) != 1:
+def _heads(name, t, cache):
+    """(tokens, heads, their strides) of [n_tokens, heads, head_dim] with contiguous heads, on the
+    cache's device."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or t.get_device() != cache.index or shape[2] != cache.head_dim or stride[2] != 1:
         raise ValueError(f"{name} must be [n_tokens, heads, {cache.head_dim}] with contiguous heads on {cache.device}")
-    if heads is not None and t.shape[1] != heads:
-        raise ValueError(f"{name} must have {heads} heads, got {t.shape[1]}")
+    return shape[0], shape[1], stride[0], stride[1]
 
 
 def iqq_kv8_append(cache, k, v, block_tables, seq_lens, cu_tokens, flags=None, stream=None):
@@ -818,31 +825,32 @@ def iqq_kv8_append(cache, k, v, block_tables, seq_lens, cu_tokens, flags=None, s
     heads any multiple of 16 bytes apart) into the cache, as the last cu_tokens[b+1] - cu_tokens[b]
     of the seq_lens[b] tokens of each sequence."""
     import torch
-    _need_heads("k", k, cache, cache.n_kv_heads)
-    _need_heads("v", v, cache, cache.n_kv_heads)
+    n_tokens, heads, kt, kh = _heads("k", k, cache)
+    vtok, vheads, vt, vh = _heads("v", v, cache)
     code = _dtype_code("k", k.dtype)
-    if v.dtype != k.dtype or v.shape[0] != k.shape[0]:
-        raise ValueError("k and v must have the same type and number of tokens")
-    _need_vector("flags", flags, 1, torch.int32, cache.device)
+    if heads != cache.n_kv_heads or vheads != heads or vtok != n_tokens or v.dtype is not k.dtype:
+        raise ValueError(f"k and v must have {cache.n_kv_heads} heads, the same type and number of tokens")
+    _need_vector("flags", flags, 1, torch.int32, cache.index)
     seqs = _kv8_seqs(cache, block_tables, seq_lens, cu_tokens)
-    _launch("iqq_kv8_append", k, stream, cache._ref, ctypes.byref(seqs), code, k.data_ptr(), k.stride(0), k.stride(1),
-            v.data_ptr(), v.stride(0), v.stride(1), k.shape[0], _at(flags))
+    _launch("iqq_kv8_append", cache.index, stream, cache._ref, ctypes.byref(seqs), code, k.data_ptr(), kt, kh,
+            v.data_ptr(), vt, vh, n_tokens, _at(flags))
 
 
 def iqq_kv8_gather(cache, block_tables, seq_lens, cu_tokens, k_out, v_out, flags=None, stream=None):
     """The values of the last cu_tokens[b+1] - cu_tokens[b] cached tokens of each sequence, into
     k_out and v_out [n_tokens, n_kv_heads, head_dim] (contiguous; float32, bfloat16 or float16)."""
     import torch
-    _need_heads("k_out", k_out, cache, cache.n_kv_heads)
+    n_tokens, heads = _heads("k_out", k_out, cache)[:2]
     code = _dtype_code("k_out", k_out.dtype)
-    if v_out.dtype != k_out.dtype or v_out.shape != k_out.shape or v_out.device != k_out.device:
-        raise ValueError("k_out and v_out must have the same type, shape and device")
+    if heads != cache.n_kv_heads or v_out.dtype is not k_out.dtype or v_out.shape != k_out.shape or (
+            v_out.get_device() != cache.index):
+        raise ValueError(f"k_out and v_out must have {cache.n_kv_heads} heads, the same type, shape and device")
     if not k_out.is_contiguous() or not v_out.is_contiguous():
         raise ValueError("k_out and v_out must be contiguous")
-    _need_vector("flags", flags, 1, torch.int32, cache.device)
+    _need_vector("flags", flags, 1, torch.int32, cache.index)
     seqs = _kv8_seqs(cache, block_tables, seq_lens, cu_tokens)
-    _launch("iqq_kv8_gather", k_out, stream, cache._ref, ctypes.byref(seqs), code, k_out.data_ptr(), v_out.data_ptr(),
-            k_out.shape[0], _at(flags))
+    _launch("iqq_kv8_gather", cache.index, stream, cache._ref, ctypes.byref(seqs), code, k_out.data_ptr(),
+            v_out.data_ptr(), n_tokens, _at(flags))
     return k_out, v_out
 
 
@@ -869,19 +877,17 @@ def iqq_kv8_attention(cache, q, block_tables, seq_lens, cu_tokens, out, lse=None
     like q) and lse (optional float32 [n_tokens, n_heads]).  scale None: head_dim ** -0.5.
     workspace: uint8, kv8_attention_workspace_bytes; one for each call that may run at a time."""
     import torch
-    _need_heads("q", q, cache, None)
+    n_tokens, n_heads, qt, qh = _heads("q", q, cache)
     code = _dtype_code("q", q.dtype)
-    if out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or not out.is_contiguous():
+    if out.dtype is not q.dtype or out.shape != q.shape or out.get_device() != cache.index or not out.is_contiguous():
         raise ValueError("out must be contiguous, of q's shape, type and device")
-    n_tokens, n_heads = q.shape[0], q.shape[1]
-    _need_vector("lse", lse, n_tokens * n_heads, torch.float32, cache.device)
-    _need_vector("flags", flags, 1, torch.int32, cache.device)
-    _need_vector("workspace", workspace, 0, torch.uint8, cache.device)
+    _need_vector("lse", lse, n_tokens * n_heads, torch.float32, cache.index)
+    _need_vector("flags", flags, 1, torch.int32, cache.index)
+    _need_vector("workspace", workspace, 0, torch.uint8, cache.index)
     seqs = _kv8_seqs(cache, block_tables, seq_lens, cu_tokens)
-    _launch("iqq_kv8_attention", q, stream, cache._ref, ctypes.byref(seqs), code, q.data_ptr(), q.stride(0),
-            q.stride(1), n_heads, n_tokens, out.data_ptr(), _at(lse),
-            cache.head_dim ** -0.5 if scale is None else scale, _at(workspace),
-            0 if workspace is None else workspace.numel(), _at(flags))
+    _launch("iqq_kv8_attention", cache.index, stream, cache._ref, ctypes.byref(seqs), code, q.data_ptr(), qt, qh,
+            n_heads, n_tokens, out.data_ptr(), _at(lse), cache.head_dim ** -0.5 if scale is None else scale,
+            _at(workspace), 0 if workspace is None else workspace.numel(), _at(flags))
     return out
 
 
