@@ -17,7 +17,6 @@
 //                to 8 CTAs whose partial sums meet in shared memory: when tokens are few, the
 //                weights' bytes bound the product and every SM has to read its share of them.
 #include <algorithm>
-#include <atomic>
 
 #include "i8_code.cuh"
 #include "sm100.cuh"
@@ -351,18 +350,6 @@ __global__ void __launch_bounds__(256) empty_kernel(const Args P)
     }
 }
 
-iqq_status opt_in(const void* kernel, std::atomic<uint64_t>& done)
-{
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return iqq::launch_status();
-    const uint64_t bit = 1ULL << (dev & 63);
-    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return IQQ_OK;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-        return iqq::launch_status();
-    if (dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
-    return IQQ_OK;
-}
-
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Where the pair kernel runs (else the split kernel), and its token tile.
@@ -404,7 +391,7 @@ iqq_status launch(Args P, const int8_t* a, int64_t lda, const int8_t* w, int64_t
     if (s != IQQ_OK) return s;
     if (plan_pair(P, sms)) {
         s = iqq::byte_map(&amap, a, k, P.n_tok, lda, P.tn / 2);
-        if (s == IQQ_OK) s = opt_in(reinterpret_cast<const void*>(pair_kernel<T>), pair_done);
+        if (s == IQQ_OK) s = iqq::opt_in_smem(reinterpret_cast<const void*>(pair_kernel<T>), kSmem, pair_done);
         if (s != IQQ_OK) return s;
         P.stages = std::min<int>(kMaxStages, (kSmem - 1024 - static_cast<int>(sizeof(Bars))) / (kABytes + P.tn / 2 * kStep));
         const int64_t pairs = std::min<int64_t>(P.m_tiles * P.t_tiles, sms / 2);
@@ -424,7 +411,7 @@ iqq_status launch(Args P, const int8_t* a, int64_t lda, const int8_t* w, int64_t
     uint32_t columns = 32;
     while (columns < static_cast<uint32_t>(P.tn)) columns *= 2;
     s = iqq::byte_map(&amap, a, k, P.n_tok, lda, P.tn);
-    if (s == IQQ_OK) s = opt_in(reinterpret_cast<const void*>(split_kernel<T>), split_done);
+    if (s == IQQ_OK) s = iqq::opt_in_smem(reinterpret_cast<const void*>(split_kernel<T>), kSmem, split_done);
     if (s != IQQ_OK) return s;
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * P.split));
     cfg.dynamicSmemBytes = static_cast<size_t>(P.stages * stage + 1024);

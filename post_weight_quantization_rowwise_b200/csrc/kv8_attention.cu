@@ -6,17 +6,18 @@
 // sequence that share a key/value head are packed together (row r is token r / group, head
 // r % group of the group), so a page is read once for all of them.
 //
-// decode kernel (few rows a sequence).  Bound by the cache's bytes.  A warp takes 16 keys at a
-// time straight from global memory into the operand registers of mma.m16n8k16:
+// decode kernel (few rows a sequence).  Bound by the cache's bytes.  One warp streams the pages'
+// tiles into a ring of stages (cp.async.bulk, the scales beside them by cp.async); four warps
+// take 16 keys of a stage each, straight into the operand registers of mma.m16n8k16:
 //     S^T = K Q^T (16 keys x 8 rows),  O^T = V^T P^T (16 dimensions x 8 rows).
 // The order of the dimensions in a dot product, and of the rows of V^T, is free, so each lane
-// loads 16 contiguous bytes and no transposition through shared memory is needed; P^T goes from
-// the accumulators' layout to the operand's by movmatrix.  int8 codes become binary16 exactly:
-// the byte b of a code c, in the low byte of 0x6400, is the binary16 1152 + c after b ^= 0x80,
-// and 1152 is subtracted.  Rows of q become binary16 exactly as well, by a power of two for each
-// row that brings its largest value near 2^14 (values below 2^-38 of it round, which is beyond
-// the binary32 sums).  The weights p_j are rounded to binary16, times the page's value scale over
-// a power of two that follows the largest such scale: 2^-11 each, as fine as the output's type or
+// reads 16 contiguous bytes and nothing is transposed through shared memory; P^T goes from the
+// accumulators' layout to the operand's by movmatrix.  int8 codes become binary16 exactly: the
+// byte b of a code c, in the low byte of 0x6400, is the binary16 1152 + c after b ^= 0x80, and
+// 1152 is subtracted.  Rows of q become binary16 exactly as well, by a power of two for each row
+// that brings its largest value near 2^14 (values below 2^-38 of it round, which is beyond the
+// binary32 sums).  The weights p_j are rounded to binary16, times the page's value scale over a
+// power of two that follows the largest such scale: 2^-11 each, as fine as the output's type or
 // finer.  The running maximum moves only when a score passes it by 2^8, so a block costs one vote.
 //
 // The keys of a sequence are split over CTAs (and the four warps of one) so that the machine is
@@ -27,6 +28,7 @@
 #include <algorithm>
 
 #include "kv8.cuh"
+#include "sm100.cuh"
 
 namespace {
 
@@ -34,8 +36,9 @@ using iqq::Kv8;
 using iqq::Span;
 
 constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kSegment = 2048;   // keys whose pages are looked up at a time
+constexpr int kThreads = 32 * kWarps;       // that compute; one more warp loads
+constexpr int kStageBytes = 16384;          // keys and values of a stage
+constexpr int kStages = 4;
 constexpr int kMinChunk = 256;   // keys a CTA takes at least
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -50,10 +53,10 @@ struct Args {
     float* part_lse;
 };
 
-// The keys of a CTA: a sequence's length divided by the launch's splits, whole multiples of 64.
+// The keys of a CTA: a sequence's length divided by the launch's splits, a multiple of every page size.
 __device__ __forceinline__ int64_t chunk_of(int64_t len, int splits)
 {
-    const int64_t c = ((len + splits - 1) / splits + 63) / 64 * 64;
+    const int64_t c = ((len + splits - 1) / splits + 127) / 128 * 128;
     return c < kMinChunk ? kMinChunk : c;
 }
 
@@ -94,49 +97,108 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 16 keys of a page for this lane: keys g and g+8 (dimensions 16t.. of each 64), and the values
-// of keys 2t, 2t+1, 2t+8, 2t+9 (dimensions D/8 * g ..); g = lane / 4, t = lane % 4.
-template <int D>
-struct Block {
-    uint32_t k[2][D / 16];
-    uint32_t v[4][D / 32];
+// Shared memory of the decode kernel.  A stage holds kKeys keys' codes, then their values', in
+// the order of the keys, and the scales of each 16 keys.
+template <int D, int NT>
+struct Smem {
+    static constexpr int kRows = 8 * NT, kKeys = kStageBytes / (2 * D);
+    union {
+        uint8_t stage[kStages][kStageBytes];
+        float o[kWarps][kRows][D];  // the warps' parts, once the stages are done with
+    };
+    float ks[kStages][kKeys / 16], vs[kStages][kKeys / 16];
+    int live[kStages];              // which 16 keys have a page, a bit each
+    uint64_t full[kStages], empty[kStages];
+    float m[kWarps][kRows], l[kWarps][kRows];
 };
 
-template <int D>
-__device__ __forceinline__ void load_block(Block<D>& B, const Kv8& C, int page, int kvh, int off, int g, int t)
+// Copies `bytes` (a multiple of 16) to shared memory, counted by the barrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
 {
-    const int64_t at = (((static_cast<int64_t>(page) * C.heads + kvh) << C.page_log2) + off) * D;
-    const int8_t* k = C.codes[0] + at;
-    const int8_t* v = C.codes[1] + at;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(k + (g + 8 * h) * D + 64 * i + 16 * t));
-            B.k[h][4 * i] = w.x; B.k[h][4 * i + 1] = w.y; B.k[h][4 * i + 2] = w.z; B.k[h][4 * i + 3] = w.w;
-        }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int8_t* p = v + (2 * t + (i & 1) + 8 * (i >> 1)) * D + D / 8 * g;
-        if constexpr (D == 128) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-            B.v[i][0] = w.x; B.v[i][1] = w.y; B.v[i][2] = w.z; B.v[i][3] = w.w;
-        } else {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-            B.v[i][0] = w.x; B.v[i][1] = w.y;
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void async_load4(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// Arrives on the barrier when this thread's cp.async so far are done.
+__device__ __forceinline__ void async_arrive(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// The loading warp: keys j0 .. j1-1 of sequence b, a stage at a time.  A lane takes the pieces of
+// one page within a stage (kKeys or page_size keys, whichever is less), 32 pieces at a time.
+template <int D, int NT>
+__device__ __forceinline__ bool feed(Smem<D, NT>& S, const Kv8& C, int b, int kvh, int64_t j0, int64_t j1, uint32_t* flags)
+{
+    constexpr int kKeys = Smem<D, NT>::kKeys;
+    const int lane = threadIdx.x & 31;
+    const int piece = min(kKeys, 1 << C.page_log2), per = kKeys / piece;  // keys a piece, pieces a stage
+    const int batch = 32 / per;                                         // stages whose pages are looked up at once
+    const int stages = static_cast<int>((j1 - j0 + kKeys - 1) / kKeys);
+    const auto page_of = [&](int st0) {
+        const int64_t key = j0 + static_cast<int64_t>(st0) * kKeys + lane * piece;
+        return key < j1 ? iqq::page_at(C, b, key >> C.page_log2) : -2;
+    };
+    int s = 0, issued = 0, page = page_of(0);
+    uint32_t ph = 0;
+    bool late = false;
+    for (int st0 = 0; st0 < stages && !late; st0 += batch) {
+        const int here = page;
+        if (st0 + batch < stages) page = page_of(st0 + batch);
+        if (here == -1) iqq::raise_flags(flags, IQQ_FLAG_BAD_INDEX);
+        const uint32_t live = __ballot_sync(0xffffffffu, here >= 0);
+        for (int i = 0; i < batch && st0 + i < stages; ++i) {
+            late = !iqq::bar_wait(iqq::smem_u32(&S.empty[s]), ph ^ 1u);
+            if (__any_sync(0xffffffffu, late)) break;
+            const uint32_t bar = iqq::smem_u32(&S.full[s]);
+            const uint32_t mine = (live >> (i * per)) & ((1u << per) - 1u);
+            if (lane == 0) {
+                uint32_t keys = 0;  // a bit for each 16 keys
+                for (int u = 0; u < per; ++u)
+                    if (mine >> u & 1u) keys |= ((1u << (piece / 16)) - 1u) << (u * (piece / 16));
+                S.live[s] = static_cast<int>(keys);
+                iqq::bar_expect(bar, static_cast<uint32_t>(__popc(mine)) * piece * D * 2);
+            }
+            __syncwarp();
+            const int u = lane - i * per;
+            if (u >= 0 && u < per && here >= 0) {
+                const int64_t key = j0 + static_cast<int64_t>(st0) * kKeys + lane * piece;
+                const int64_t cell = static_cast<int64_t>(here) * C.heads + kvh;
+                const int64_t at = ((cell << C.page_log2) + (key & ((1 << C.page_log2) - 1))) * D;
+                const uint32_t to = iqq::smem_u32(&S.stage[s][0]) + u * piece * D;
+                bulk_load(to, C.codes[0] + at, piece * D, bar);
+                bulk_load(to + kKeys * D, C.codes[1] + at, piece * D, bar);
+                for (int k = 0; k < piece / 16; ++k) {
+                    async_load4(iqq::smem_u32(&S.ks[s][u * (piece / 16) + k]), C.scales[0] + cell);
+                    async_load4(iqq::smem_u32(&S.vs[s][u * (piece / 16) + k]), C.scales[1] + cell);
+                }
+            }
+            async_arrive(bar);
+            ++issued;
+            if (++s == kStages) {
+                s = 0;
+                ph ^= 1u;
+            }
         }
     }
+    // every copy has landed (somebody waited for it) unless a wait ran out
+    for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+        late |= !iqq::bar_wait(iqq::smem_u32(&S.full[i % kStages]), static_cast<uint32_t>(i / kStages) & 1u);
+    return !late;
 }
 
 template <class T, int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? (D == 64 ? 4 : 3) : 2)
+__global__ void __launch_bounds__(kThreads + 32, NT == 1 ? 3 : 2)
 decode_kernel(const Kv8 C, const Args A, uint32_t* __restrict__ flags)
 {
     constexpr int kRows = 8 * NT, kK = D / 16, kM = D / 16;  // k steps of S, 16-row tiles of O^T
-    __shared__ int s_page[kSegment / 16];
-    __shared__ float s_ks[kSegment / 16], s_vs[kSegment / 16];
-    __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
-    __shared__ __align__(16) float s_o[kWarps][kRows][D];
+    constexpr int kKeys = Smem<D, NT>::kKeys;
+    extern __shared__ __align__(128) uint8_t raw[];
+    Smem<D, NT>& S = *reinterpret_cast<Smem<D, NT>*>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -158,6 +220,22 @@ decode_kernel(const Kv8 C, const Args A, uint32_t* __restrict__ flags)
     const int64_t j0 = split * chunk;
     if (split > 0 && j0 >= len) return;
     const int64_t j1 = min(seen, j0 + chunk);
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            iqq::bar_init(iqq::smem_u32(&S.full[i]), 33);        // expect_tx, and the lanes' scales
+            iqq::bar_init(iqq::smem_u32(&S.empty[i]), kWarps);
+        }
+        iqq::bar_init_fence();
+    }
+    __syncthreads();
+    if (warp == kWarps) {
+        if (j1 > j0 && !feed<D, NT>(S, C, b, kvh, j0, j1, flags)) iqq::raise_flags(flags, IQQ_FLAG_WAIT_TIMEOUT);
+        __syncwarp();
+        __syncthreads();
+        __syncthreads();
+        return;
+    }
 
     // the rows of q this lane feeds (row g of each 8), as binary16 times 2^-e
     uint32_t bq[NT][kK][2];
@@ -226,47 +304,48 @@ decode_kernel(const Kv8 C, const Args A, uint32_t* __restrict__ flags)
             for (int i = 0; i < 4; ++i) o[n][d][i] = 0.0f;
     }
 
-    const int page_size = 1 << C.page_log2;
-    for (int64_t seg = j0; seg < j1; seg += kSegment) {
-        const int64_t seg_end = min(j1, seg + kSegment);
-        const int64_t p0 = seg >> C.page_log2;
-        const int pages = static_cast<int>(((seg_end - 1) >> C.page_log2) - p0) + 1;
-        if (seg > j0) __syncthreads();
-        if (tid < pages) {
-            const int p = iqq::page_at(C, b, p0 + tid);
-            s_page[tid] = p;
-            const int64_t cell = static_cast<int64_t>(p) * C.heads + kvh;
-            s_ks[tid] = p < 0 ? 0.0f : __ldg(C.scales[0] + cell);
-            s_vs[tid] = p < 0 ? 0.0f : __ldg(C.scales[1] + cell);
-            if (p < 0) iqq::raise_flags(flags, IQQ_FLAG_BAD_INDEX);
+    const int stages = j1 > j0 ? static_cast<int>((j1 - j0 + kKeys - 1) / kKeys) : 0;
+    int st = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < stages; ++i) {
+        const bool late = !iqq::bar_wait(iqq::smem_u32(&S.full[st]), ph);
+        if (__any_sync(0xffffffffu, late)) {
+            iqq::raise_flags(flags, IQQ_FLAG_WAIT_TIMEOUT);
+            break;
         }
-        __syncthreads();
-        const int blocks = static_cast<int>((seg_end - seg + 15) >> 4);
-        auto place = [&](int i) { return static_cast<int>(((seg + 16 * i) >> C.page_log2) - p0); };
-        auto fetch = [&](int i, Block<D>& B) {
-            const int p = s_page[place(i)];
-            if (p >= 0) load_block<D>(B, C, p, kvh, static_cast<int>((seg + 16 * i) & (page_size - 1)), g, t);
-        };
-        Block<D> cur, next;
-        if (warp < blocks) fetch(warp, cur);
-        for (int i = warp; i < blocks; i += kWarps) {
-            if (i + kWarps < blocks) fetch(i + kWarps, next);
-            const int at = place(i);
-            const int key0 = static_cast<int>(seg - j0) + 16 * i;  // from j0
-            if (s_page[at] >= 0) {
-                const float ks = s_ks[at], vs = s_vs[at];
-                float x[NT][4];
+        const int live = S.live[st];
+#pragma unroll
+        for (int u = 0; u < kKeys / (16 * kWarps); ++u) {
+            const int at = u * kWarps + warp;        // which 16 keys of the stage
+            const int key0 = i * kKeys + 16 * at;    // from j0
+            if (live >> at & 1) {
+                const float ks = S.ks[st][at], vs = S.vs[st][at];
+                const uint8_t* kp = &S.stage[st][16 * at * D + g * D + 16 * t];
+                const uint8_t* vp = &S.stage[st][kKeys * D + 16 * at * D + 2 * t * D + D / 8 * g];
+                float x[NT][4], x2[NT][4];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[n][e] = 0.0f;
+                    for (int e = 0; e < 4; ++e) x[n][e] = x2[n][e] = 0.0f;
+                // keys g and g+8, dimensions 16t .. of each 64; two chains of sums
 #pragma unroll
-                for (int j = 0; j < kK; ++j) {
-                    const uint32_t a0 = codes_even(cur.k[0][j]), a2 = codes_odd(cur.k[0][j]);
-                    const uint32_t a1 = codes_even(cur.k[1][j]), a3 = codes_odd(cur.k[1][j]);
+                for (int h = 0; h < D / 64; ++h) {
+                    const uint4 k0 = *reinterpret_cast<const uint4*>(kp + 64 * h);
+                    const uint4 k1 = *reinterpret_cast<const uint4*>(kp + 8 * D + 64 * h);
+                    const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma(x[n], a0, a1, a2, a3, bq[n][j][0], bq[n][j][1]);
+                    for (int c = 0; c < 4; ++c) {
+                        const int j = 4 * h + c;
+                        const uint32_t a0 = codes_even(w0[c]), a2 = codes_odd(w0[c]);
+                        const uint32_t a1 = codes_even(w1[c]), a3 = codes_odd(w1[c]);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma(c & 1 ? x2[n] : x[n], a0, a1, a2, a3, bq[n][j][0], bq[n][j][1]);
+                    }
                 }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[n][e] += x2[n][e];
                 const bool masked = key0 + 16 > clear;
                 bool moved = false;
 #pragma unroll
@@ -331,25 +410,39 @@ decode_kernel(const Kv8 C, const Args A, uint32_t* __restrict__ flags)
                     bp[n][0] = transpose8(pack_h2(p[0], p[1]));
                     bp[n][1] = transpose8(pack_h2(p[2], p[3]));
                 }
+                // keys 2t, 2t+1, 2t+8, 2t+9, dimensions D/8 * g ..: 16-row tile d is bytes 2d, 2d+1
 #pragma unroll
-                for (int d = 0; d < kM; d += 2) {
-                    // bytes 2d .. 2d+3 of the lane's dimensions: tiles d and d+1
-                    const uint32_t w01a = __byte_perm(cur.v[0][d / 2], cur.v[1][d / 2], 0x5410);
-                    const uint32_t w23a = __byte_perm(cur.v[2][d / 2], cur.v[3][d / 2], 0x5410);
-                    const uint32_t w01b = __byte_perm(cur.v[0][d / 2], cur.v[1][d / 2], 0x7632);
-                    const uint32_t w23b = __byte_perm(cur.v[2][d / 2], cur.v[3][d / 2], 0x7632);
-                    const uint32_t a0 = codes_even(w01a), a1 = codes_odd(w01a), a2 = codes_even(w23a), a3 = codes_odd(w23a);
-                    const uint32_t c0 = codes_even(w01b), c1 = codes_odd(w01b), c2 = codes_even(w23b), c3 = codes_odd(w23b);
+                for (int h = 0; h < D / 64; ++h) {
+                    uint2 v[4];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        mma(o[n][d], a0, a1, a2, a3, bp[n][0], bp[n][1]);
-                        mma(o[n][d + 1], c0, c1, c2, c3, bp[n][0], bp[n][1]);
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = *reinterpret_cast<const uint2*>(vp + ((e & 1) + 8 * (e >> 1)) * D + 8 * h);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t w0 = c ? v[0].y : v[0].x, w1 = c ? v[1].y : v[1].x;
+                        const uint32_t w2 = c ? v[2].y : v[2].x, w3 = c ? v[3].y : v[3].x;
+                        const uint32_t lo01 = __byte_perm(w0, w1, 0x5410), hi01 = __byte_perm(w0, w1, 0x7632);
+                        const uint32_t lo23 = __byte_perm(w2, w3, 0x5410), hi23 = __byte_perm(w2, w3, 0x7632);
+                        const uint32_t a0 = codes_even(lo01), a1 = codes_odd(lo01), a2 = codes_even(lo23), a3 = codes_odd(lo23);
+                        const uint32_t c0 = codes_even(hi01), c1 = codes_odd(hi01), c2 = codes_even(hi23), c3 = codes_odd(hi23);
+                        const int d = 4 * h + 2 * c;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma(o[n][d], a0, a1, a2, a3, bp[n][0], bp[n][1]);
+                            mma(o[n][d + 1], c0, c1, c2, c3, bp[n][0], bp[n][1]);
+                        }
                     }
                 }
             }
-            cur = next;
+        }
+        __syncwarp();
+        if (lane == 0) iqq::bar_arrive(iqq::smem_u32(&S.empty[st]));
+        if (++st == kStages) {
+            st = 0;
+            ph ^= 1u;
         }
     }
+    __syncthreads();  // the stages' memory is free
 
     // the warps' parts meet: rows 2t, 2t+1 of each 8, dimensions D/8 * g + 2d, + 1 of tile d
 #pragma unroll
@@ -361,12 +454,12 @@ decode_kernel(const Kv8 C, const Args A, uint32_t* __restrict__ flags)
             l[n][h] += __shfl_xor_sync(0xffffffffu, l[n][h], 16);
             const int r = 8 * n + 2 * t + h;
             if (g == 0) {
-                s_m[warp][r] = m[n][h];
-                s_l[warp][r] = l[n][h];
+                S.m[warp][r] = m[n][h];
+                S.l[warp][r] = l[n][h];
             }
 #pragma unroll
             for (int d = 0; d < kM; ++d)
-                *reinterpret_cast<float2*>(&s_o[warp][r][D / 8 * g + 2 * d]) = make_float2(o[n][d][h] * vref, o[n][d][2 + h] * vref);
+                *reinterpret_cast<float2*>(&S.o[warp][r][D / 8 * g + 2 * d]) = make_float2(o[n][d][h] * vref, o[n][d][2 + h] * vref);
         }
     __syncthreads();
     const bool whole = chunk >= len;  // this CTA has every key
@@ -374,17 +467,17 @@ decode_kernel(const Kv8 C, const Args A, uint32_t* __restrict__ flags)
         const int r = i / (D / 4), d = i % (D / 4) * 4;
         const int64_t row = first_row + r;
         if (row >= rows) continue;
-        float top = s_m[0][r];
+        float top = S.m[0][r];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, S.m[w][r]);
         const float mu = top == -INFINITY ? 0.0f : top;
         float sum = 0.0f;
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float f = ex2(s_m[w][r] - mu);
-            sum = fmaf(s_l[w][r], f, sum);
-            const float4 v = *reinterpret_cast<const float4*>(&s_o[w][r][d]);
+            const float f = ex2(S.m[w][r] - mu);
+            sum = fmaf(S.l[w][r], f, sum);
+            const float4 v = *reinterpret_cast<const float4*>(&S.o[w][r][d]);
             acc.x = fmaf(v.x, f, acc.x);
             acc.y = fmaf(v.y, f, acc.y);
             acc.z = fmaf(v.z, f, acc.z);
@@ -485,17 +578,18 @@ Plan plan_of(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int64_t n_hea
     p.row_tile = each <= 8 ? 8 : 16;
     p.slots = n_tokens * group / p.row_tile + seqs->n_seqs;
     const int64_t ctas = p.slots * cache->n_kv_heads, capacity = seqs->table_width * cache->page_size;
-    const int64_t want = (4LL * iqq::sm_count() + ctas - 1) / ctas, most = (capacity + kMinChunk - 1) / kMinChunk;
+    const int64_t want = (8LL * iqq::sm_count() + ctas - 1) / ctas, most = (capacity + kMinChunk - 1) / kMinChunk;
     p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, most, 1024})));
     return p;
 }
 
 template <class K>
-iqq_status start(K kernel, dim3 grid, cudaStream_t st, const Kv8& C, const Args& A, uint32_t* flags)
+iqq_status start(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t st, const Kv8& C, const Args& A, uint32_t* flags)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -509,14 +603,24 @@ iqq_status start(K kernel, dim3 grid, cudaStream_t st, const Kv8& C, const Args&
     return iqq::launch_status();
 }
 
+template <class T, int D, int NT>
+iqq_status start_decode(const Kv8& C, const Args& A, const Plan& p, cudaStream_t st, uint32_t* flags)
+{
+    static std::atomic<uint64_t> done{0};
+    constexpr size_t smem = sizeof(Smem<D, NT>);
+    const iqq_status s = iqq::opt_in_smem(reinterpret_cast<const void*>(decode_kernel<T, D, NT>), smem, done);
+    if (s != IQQ_OK) return s;
+    const dim3 grid(static_cast<unsigned>(p.slots), static_cast<unsigned>(p.splits), static_cast<unsigned>(C.heads));
+    return start(decode_kernel<T, D, NT>, grid, kThreads + 32, smem, st, C, A, flags);
+}
+
 template <class T, int D>
 iqq_status launch(const Kv8& C, const Args& A, const Plan& p, cudaStream_t st, uint32_t* flags)
 {
-    const dim3 grid(static_cast<unsigned>(p.slots), static_cast<unsigned>(p.splits), static_cast<unsigned>(C.heads));
-    const iqq_status s = p.row_tile == 8 ? start(decode_kernel<T, D, 1>, grid, st, C, A, flags)
-                                         : start(decode_kernel<T, D, 2>, grid, st, C, A, flags);
+    const iqq_status s = p.row_tile == 8 ? start_decode<T, D, 1>(C, A, p, st, flags) : start_decode<T, D, 2>(C, A, p, st, flags);
     if (s != IQQ_OK || p.splits == 1) return s;
-    return start(combine_kernel<T, D>, dim3(static_cast<unsigned>(C.n_tokens), static_cast<unsigned>(A.heads)), st, C, A, flags);
+    return start(combine_kernel<T, D>, dim3(static_cast<unsigned>(C.n_tokens), static_cast<unsigned>(A.heads)), kThreads, 0,
+                 st, C, A, flags);
 }
 
 bool shapes_ok(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int64_t n_heads, int64_t n_tokens)

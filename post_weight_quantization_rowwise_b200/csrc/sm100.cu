@@ -1,4 +1,4 @@
-// sm100.cu -- host side of sm100.cuh: tensor maps.
+// sm100.cu -- host side of sm100.cuh: tensor maps, shared-memory limits.
 #include "sm100.cuh"
 
 namespace {
@@ -37,5 +37,17 @@ iqq_status iqq::byte_map(CUtensorMap* map, const void* base, int64_t width, int6
         set_last_cuda_error(cudaErrorNotSupported);
         return IQQ_ERR_CUDA;
     }
+    return IQQ_OK;
+}
+
+iqq_status iqq::opt_in_smem(const void* kernel, size_t smem, std::atomic<uint64_t>& done)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return launch_status();
+    const uint64_t bit = dev < 64 ? 1ULL << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return IQQ_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+        return launch_status();
+    done.fetch_or(bit, std::memory_order_relaxed);
     return IQQ_OK;
 }

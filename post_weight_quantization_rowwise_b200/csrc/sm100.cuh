@@ -4,6 +4,8 @@
 
 #include <cuda.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace iqq {
@@ -188,6 +190,9 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16])
 }
 
 // ---- host ----
+
+// Lets a kernel take `smem` bytes of dynamic shared memory, once per device (`done`: a bit each).
+iqq_status opt_in_smem(const void* kernel, size_t smem, std::atomic<uint64_t>& done);
 
 // A 2-D tensor of bytes: rows of `width` bytes, `pitch` apart (16-byte aligned, a multiple of
 // 16), read in tiles of 128 bytes x box_rows with the 128-byte swizzle, zeros outside.
