@@ -491,6 +491,7 @@ iqq_status iqq_gemm_i8(const int8_t* a, int64_t lda, const float* a_scales, cons
  *  k_codes, v_codes    int8 [n_pages][n_kv_heads][page_size][head_dim], 16-byte aligned: a
  *                      page's tokens of one head are one contiguous tile.
  *  k_scales, v_scales  binary32 [n_pages][n_kv_heads], 4-byte aligned.
+ *  n_pages             at least 1 where a call has tokens.
  *  page_size           16, 32, 64 or 128.
  *  head_dim            64 or 128.
  */
@@ -572,6 +573,7 @@ iqq_status iqq_kv8_gather(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, 
  *
  *  dtype       IQQ_BF16 or IQQ_F16: the type of q and out.
  *  q           [n_tokens][n_heads][head_dim], strides as for k of iqq_kv8_append.
+ *  n_heads     a multiple of n_kv_heads; n_tokens * n_heads < 2^31.
  *  out         [n_tokens][n_heads][head_dim] contiguous, 16-byte aligned.
  *  lse         optional binary32 [n_tokens][n_heads]: log of the sum of exp(scale * q . k_j).
  *  scale       finite; head_dim^-1/2 as a rule.

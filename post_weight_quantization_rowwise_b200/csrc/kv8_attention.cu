@@ -20,9 +20,12 @@
 // power of two that follows the largest such scale: 2^-11 each, as fine as the output's type or
 // finer.  The running maximum moves only when a score passes it by 2^8, so a block costs one vote.
 //
-// The keys of a sequence are split over CTAs (and the four warps of one) so that the machine is
-// filled; partial results, each with its log-sum, meet in the workspace and combine_kernel joins
-// them.
+// Every launch is one wave of CTAs, and each takes an equal share of the work: the stages of all
+// sequences, heads and row tiles laid end to end, in an order that every CTA works out from the
+// lengths by one scan.  So a ragged batch, one long sequence and many short ones all fill the
+// machine evenly.  A tile that lies in one share is finished there; of the others each share
+// leaves a part, normalized and with its log-sum, in the workspace (two a CTA at most: where its
+// share begins and where it ends), and combine_kernel joins them.
 #include <math.h>
 
 #include <algorithm>
@@ -38,8 +41,7 @@ using iqq::Span;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;       // that compute; one more warp loads
 constexpr int kStageBytes = 16384;          // keys and values of a stage
-constexpr int kStages = 4;
-constexpr int kMinChunk = 256;   // keys a CTA takes at least
+constexpr int kMaxCtas = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Args {
@@ -47,18 +49,66 @@ struct Args {
     void* out;
     float* lse;
     int64_t q_token_stride, q_head_stride;
-    int32_t heads, group, splits;
+    int32_t heads, group;
     float scale;
-    float* part;      // [n_tokens * heads][splits][head_dim], then the log-sums [..][splits]
+    struct Mark* marks;  // [gridDim.x]
+    float* part;         // [gridDim.x][2][row tile][head_dim], then the log-sums [..][2][row tile]
     float* part_lse;
 };
 
-// The keys of a CTA: a sequence's length divided by the launch's splits, a multiple of every page size.
-__device__ __forceinline__ int64_t chunk_of(int64_t len, int splits)
-{
-    const int64_t c = ((len + splits - 1) / splits + 127) / 128 * 128;
-    return c < kMinChunk ? kMinChunk : c;
-}
+// The launch's stages in equal shares: `each`, and one more for the first `more` CTAs.
+struct Shares {
+    int64_t each;
+    int32_t more;
+    __device__ __forceinline__ Shares() {}
+    __device__ __forceinline__ Shares(int64_t total, int32_t ctas)
+    {
+        if (total >> 31 == 0) {  // (64-bit division is a long call)
+            each = static_cast<uint32_t>(total) / static_cast<uint32_t>(ctas);
+        } else {
+            each = total / ctas;
+        }
+        more = static_cast<int32_t>(total - each * ctas);
+    }
+    __device__ __forceinline__ int64_t start(int c) const { return each * c + min(c, more); }
+    __device__ __forceinline__ bool empty(int c) const { return each == 0 && c >= more; }
+};
+
+// What a CTA's share begins in: the tile (sequence, key/value head, row tile) whose stages are
+// t0 .. t1-1 of the launch's.
+struct Mark {
+    int64_t t0, t1;
+    Shares shares;
+    int32_t b, head, row_tile;
+};
+
+// A sequence as the launch sees it.  (n_tokens * heads < 2^31, so a sequence's rows and, with its
+// length below 2^31, its stages fit 32 bits; the stages of all its tiles need not.)
+template <int ROWS, int KEYS>
+struct Seq {
+    Span s;
+    int32_t rows, tiles, len, stages;
+    int64_t all;  // stages of every head and row tile
+    __device__ __forceinline__ Seq(const Kv8& C, int b, int group)
+    {
+        s = iqq::span_of(C, b);
+        rows = s.n * group;  // 0 for a bad span
+        tiles = (rows + ROWS - 1) / ROWS;
+        len = static_cast<int32_t>(s.len < C.capacity ? s.len : C.capacity);
+        stages = len <= 0 ? 1 : static_cast<int32_t>((static_cast<uint32_t>(len) + KEYS - 1) / KEYS);  // no key: one, for the zeros
+        all = static_cast<int64_t>(tiles) * stages * C.heads;
+    }
+    // Tile and stage within it of the sequence's stage `at`.
+    __device__ __forceinline__ void place(int64_t at, int32_t& head, int32_t& row_tile, int32_t& stage) const
+    {
+        int64_t tile;
+        if (at >> 31 == 0) tile = static_cast<uint32_t>(at) / static_cast<uint32_t>(stages);
+        else tile = at / stages;
+        stage = static_cast<int32_t>(at - tile * stages);
+        head = static_cast<int32_t>(static_cast<uint32_t>(tile) / static_cast<uint32_t>(tiles));  // (heads * tiles < 2^31)
+        row_tile = static_cast<int32_t>(tile - static_cast<int64_t>(head) * tiles);
+    }
+};
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -98,27 +148,51 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 }
 
 // Shared memory of the decode kernel.  A stage holds kKeys keys' codes, then their values', in
-// the order of the keys, and the scales of each 16 keys.
+// the order of the keys, as rows of 128 bytes with TMA's 128-byte swizzle (16-byte unit c of row r
+// at c ^ (r & 7)), so the operand reads below meet no bank twice; and the scales of each 16 keys.
 template <int D, int NT>
 struct Smem {
-    static constexpr int kRows = 8 * NT, kKeys = kStageBytes / (2 * D);
-    union {
-        uint8_t stage[kStages][kStageBytes];
-        float o[kWarps][kRows][D];  // the warps' parts, once the stages are done with
-    };
+    static constexpr int kRows = 8 * NT, kKeys = kStageBytes / (2 * D), kStages = NT == 1 ? 3 : 4;
+    uint8_t stage[kStages][kStageBytes];
+    float o[kWarps][kRows][D];      // the warps' parts of a tile
+    float m[kWarps][kRows], l[kWarps][kRows];
     float ks[kStages][kKeys / 16], vs[kStages][kKeys / 16];
     int live[kStages];              // which 16 keys have a page, a bit each
     uint64_t full[kStages], empty[kStages];
-    float m[kWarps][kRows], l[kWarps][kRows];
+    int64_t scan[kWarps + 1], offset;
+    int first, abort;
 };
 
-// Copies `bytes` (a multiple of 16) to shared memory, counted by the barrier.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-                 "r"(bytes), "r"(bar)
-                 : "memory");
-}
+// The stages from..to-1 (of its `stages`) of one tile: a CTA's work between two stores.
+struct Piece {
+    int32_t b, head, row_tile, from, to;
+};
+
+// A CTA's walk through its share: sequence b, `at` stages into it, `left` to go.
+template <int ROWS, int KEYS>
+struct Walk {
+    int b;
+    int64_t at, left;
+    __device__ __forceinline__ bool next(const Kv8& C, int group, Piece& P)
+    {
+        while (left > 0 && b < C.n_seqs) {
+            const Seq<ROWS, KEYS> q(C, b, group);
+            if (at >= q.all) {
+                at = 0;
+                ++b;
+                continue;
+            }
+            P.b = b;
+            q.place(at, P.head, P.row_tile, P.from);
+            P.to = left < q.stages - P.from ? P.from + static_cast<int32_t>(left) : q.stages;
+            at += P.to - P.from;
+            left -= P.to - P.from;
+            return true;
+        }
+        return false;
+    }
+};
+
 __device__ __forceinline__ void async_load4(uint32_t dst, const void* src)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -129,113 +203,190 @@ __device__ __forceinline__ void async_arrive(uint32_t bar)
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// The loading warp: keys j0 .. j1-1 of sequence b, a stage at a time.  A lane takes the pieces of
-// one page within a stage (kKeys or page_size keys, whichever is less), 32 pieces at a time.
+// The loading warp's ring, over all pieces of its share.
 template <int D, int NT>
-__device__ __forceinline__ bool feed(Smem<D, NT>& S, const Kv8& C, int b, int kvh, int64_t j0, int64_t j1, uint32_t* flags)
-{
-    constexpr int kKeys = Smem<D, NT>::kKeys;
-    const int lane = threadIdx.x & 31;
-    const int piece = min(kKeys, 1 << C.page_log2), per = kKeys / piece;  // keys a piece, pieces a stage
-    const int batch = 32 / per;                                         // stages whose pages are looked up at once
-    const int stages = static_cast<int>((j1 - j0 + kKeys - 1) / kKeys);
-    const auto page_of = [&](int st0) {
-        const int64_t key = j0 + static_cast<int64_t>(st0) * kKeys + lane * piece;
-        return key < j1 ? iqq::page_at(C, b, key >> C.page_log2) : -2;
-    };
-    int s = 0, issued = 0, page = page_of(0);
+struct Feed {
+    static constexpr int kKeys = Smem<D, NT>::kKeys, kStages = Smem<D, NT>::kStages;
+    Smem<D, NT>& S;
+    int s = 0;
     uint32_t ph = 0;
-    bool late = false;
-    for (int st0 = 0; st0 < stages && !late; st0 += batch) {
-        const int here = page;
-        if (st0 + batch < stages) page = page_of(st0 + batch);
-        if (here == -1) iqq::raise_flags(flags, IQQ_FLAG_BAD_INDEX);
-        const uint32_t live = __ballot_sync(0xffffffffu, here >= 0);
-        for (int i = 0; i < batch && st0 + i < stages; ++i) {
-            late = !iqq::bar_wait(iqq::smem_u32(&S.empty[s]), ph ^ 1u);
-            if (__any_sync(0xffffffffu, late)) break;
-            const uint32_t bar = iqq::smem_u32(&S.full[s]);
-            const uint32_t mine = (live >> (i * per)) & ((1u << per) - 1u);
-            if (lane == 0) {
-                uint32_t keys = 0;  // a bit for each 16 keys
-                for (int u = 0; u < per; ++u)
-                    if (mine >> u & 1u) keys |= ((1u << (piece / 16)) - 1u) << (u * (piece / 16));
-                S.live[s] = static_cast<int>(keys);
-                iqq::bar_expect(bar, static_cast<uint32_t>(__popc(mine)) * piece * D * 2);
-            }
-            __syncwarp();
-            const int u = lane - i * per;
-            if (u >= 0 && u < per && here >= 0) {
-                const int64_t key = j0 + static_cast<int64_t>(st0) * kKeys + lane * piece;
-                const int64_t cell = static_cast<int64_t>(here) * C.heads + kvh;
-                const int64_t at = ((cell << C.page_log2) + (key & ((1 << C.page_log2) - 1))) * D;
-                const uint32_t to = iqq::smem_u32(&S.stage[s][0]) + u * piece * D;
-                bulk_load(to, C.codes[0] + at, piece * D, bar);
-                bulk_load(to + kKeys * D, C.codes[1] + at, piece * D, bar);
-                for (int k = 0; k < piece / 16; ++k) {
-                    async_load4(iqq::smem_u32(&S.ks[s][u * (piece / 16) + k]), C.scales[0] + cell);
-                    async_load4(iqq::smem_u32(&S.vs[s][u * (piece / 16) + k]), C.scales[1] + cell);
+    int64_t issued = 0;
+
+    // Keys j0 .. j1-1 of sequence b.  A lane takes what a stage has of one page (kKeys or
+    // page_size keys, whichever is less), 32 of these at a time.
+    __device__ __forceinline__ bool keys(const CUtensorMap* kmap, const CUtensorMap* vmap, const Kv8& C, int b, int kvh,
+                                         int64_t j0, int64_t j1, uint32_t* flags)
+    {
+        const int lane = threadIdx.x & 31;
+        const int piece = min(kKeys, 1 << C.page_log2), per = kKeys / piece;  // keys of a lane, lanes of a stage
+        const int batch = 32 / per;                                           // stages looked up at once
+        const int64_t stages = (j1 - j0 + kKeys - 1) / kKeys;
+        const auto page_of = [&](int64_t st0) {
+            const int64_t key = j0 + st0 * kKeys + lane * piece;
+            return key < j1 ? iqq::page_at(C, b, key >> C.page_log2) : -2;
+        };
+        int page = page_of(0);
+        for (int64_t st0 = 0; st0 < stages; st0 += batch) {
+            const int here = page;
+            if (st0 + batch < stages) page = page_of(st0 + batch);
+            if (here == -1) iqq::raise_flags(flags, IQQ_FLAG_BAD_INDEX);
+            const uint32_t live = __ballot_sync(0xffffffffu, here >= 0);
+            for (int i = 0; i < batch && st0 + i < stages; ++i) {
+                const bool late = !iqq::bar_wait(iqq::smem_u32(&S.empty[s]), ph ^ 1u);
+                if (__any_sync(0xffffffffu, late)) return false;
+                const uint32_t bar = iqq::smem_u32(&S.full[s]);
+                const uint32_t mine = (live >> (i * per)) & (per == 32 ? 0xffffffffu : (1u << per) - 1u);
+                if (lane == 0) {
+                    uint32_t with = 0;  // a bit for each 16 keys
+                    for (int u = 0; u < per; ++u)
+                        if (mine >> u & 1u) with |= ((1u << (piece / 16)) - 1u) << (u * (piece / 16));
+                    S.live[s] = static_cast<int>(with);
+                    iqq::bar_expect(bar, static_cast<uint32_t>(__popc(mine)) * piece * D * 2);
+                }
+                __syncwarp();
+                const int u = lane - i * per;
+                if (u >= 0 && u < per && here >= 0) {
+                    const int64_t key = j0 + st0 * kKeys + lane * piece;
+                    const int64_t cell = static_cast<int64_t>(here) * C.heads + kvh;
+                    // the map's rows are 128 bytes; a page's 16 keys are whole groups of eight
+                    const int row = static_cast<int>(((cell << C.page_log2) + (key & ((1 << C.page_log2) - 1))) * D / 128);
+                    const uint32_t to = iqq::smem_u32(&S.stage[s][0]) + u * piece * D;
+                    iqq::tma_load(to, kmap, 0, row, bar);
+                    iqq::tma_load(to + kKeys * D, vmap, 0, row, bar);
+                    for (int k = 0; k < piece / 16; ++k) {
+                        async_load4(iqq::smem_u32(&S.ks[s][u * (piece / 16) + k]), C.scales[0] + cell);
+                        async_load4(iqq::smem_u32(&S.vs[s][u * (piece / 16) + k]), C.scales[1] + cell);
+                    }
+                }
+                async_arrive(bar);
+                ++issued;
+                if (++s == kStages) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
-            async_arrive(bar);
-            ++issued;
-            if (++s == kStages) {
-                s = 0;
-                ph ^= 1u;
-            }
         }
+        return true;
     }
-    // every copy has landed (somebody waited for it) unless a wait ran out
-    for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-        late |= !iqq::bar_wait(iqq::smem_u32(&S.full[i % kStages]), static_cast<uint32_t>(i / kStages) & 1u);
-    return !late;
-}
+
+    // Every copy has landed (somebody waited for it) unless a wait ran out.
+    __device__ __forceinline__ bool drain()
+    {
+        bool ok = true;
+        for (int64_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+            ok &= iqq::bar_wait(iqq::smem_u32(&S.full[i % kStages]), static_cast<uint32_t>(i / kStages) & 1u);
+        return ok;
+    }
+};
+
+// The four computing warps.
+__device__ __forceinline__ void meet() { asm volatile("barrier.sync 1, 128;" ::: "memory"); }
 
 template <class T, int D, int NT>
 __global__ void __launch_bounds__(kThreads + 32, NT == 1 ? 3 : 2)
-decode_kernel(const Kv8 C, const Args A, uint32_t* __restrict__ flags)
+decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const Kv8 C, const Args A,
+              uint32_t* __restrict__ flags)
 {
-    constexpr int kRows = 8 * NT, kK = D / 16, kM = D / 16;  // k steps of S, 16-row tiles of O^T
-    constexpr int kKeys = Smem<D, NT>::kKeys;
-    extern __shared__ __align__(128) uint8_t raw[];
-    Smem<D, NT>& S = *reinterpret_cast<Smem<D, NT>*>(raw);
+    using Sm = Smem<D, NT>;
+    constexpr int kRows = Sm::kRows, kKeys = Sm::kKeys, kK = D / 16, kM = D / 16;  // k steps of S, 16-row tiles of O^T
+    extern __shared__ __align__(1024) uint8_t raw[];
+    Sm& S = *reinterpret_cast<Sm*>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    iqq::check_spans(C, false, flags);
-
-    const int64_t slot = blockIdx.x;
-    const int split = blockIdx.y;
-    const int kvh = blockIdx.z;
-    const int b = iqq::seq_of_slot(C, slot, A.group, kRows, 1);
-    const Span s = iqq::span_of(C, b);
-    const int64_t first_row = (slot - iqq::slot_base(C, b, A.group, kRows, 1)) * kRows;
-    const int64_t rows = static_cast<int64_t>(s.n) * A.group;  // 0 for a bad span
-    if (first_row >= rows) return;
-    // keys this tile's rows can see at all, and this CTA's part of them
-    const int64_t len = s.len < C.capacity ? s.len : C.capacity;
-    const int64_t last_row = first_row + kRows < rows ? first_row + kRows - 1 : rows - 1;
-    const int64_t seen = min(len, s.start + last_row / A.group + 1);
-    const int64_t chunk = chunk_of(len, A.splits);
-    const int64_t j0 = split * chunk;
-    if (split > 0 && j0 >= len) return;
-    const int64_t j1 = min(seen, j0 + chunk);
-
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < Sm::kStages; ++i) {
             iqq::bar_init(iqq::smem_u32(&S.full[i]), 33);        // expect_tx, and the lanes' scales
             iqq::bar_init(iqq::smem_u32(&S.empty[i]), kWarps);
         }
         iqq::bar_init_fence();
+        S.first = -1;
+        S.abort = 0;
+        iqq::tma_prefetch_map(&kmap);
+        iqq::tma_prefetch_map(&vmap);
     }
-    __syncthreads();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // Where this CTA's share begins: a scan over the sequences, a run of them a thread.
+    Walk<kRows, kKeys> walk;
+    {
+        const int run = (C.n_seqs + kThreads + 31) / (kThreads + 32), b0 = min(C.n_seqs, tid * run), b1 = min(C.n_seqs, b0 + run);
+        int64_t sum = 0;
+        bool bad = false;
+        for (int b = b0; b < b1; ++b) {
+            const Seq<kRows, kKeys> q(C, b, A.group);
+            sum += q.all;
+            bad |= !q.s.ok || q.s.len > C.capacity;
+        }
+        if (bad && blockIdx.x == 0) iqq::raise_flags(flags, IQQ_FLAG_BAD_INDEX);
+        int64_t before = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += v;
+        }
+        if (lane == 31) S.scan[warp] = before;
+        __syncthreads();
+        int64_t total = 0;
+#pragma unroll
+        for (int w = 0; w <= kWarps; ++w) {
+            if (w < warp) before += S.scan[w];
+            total += S.scan[w];
+        }
+        before -= sum;
+        const Shares shares(total, gridDim.x);
+        const int64_t start = shares.start(blockIdx.x), end = shares.start(blockIdx.x + 1);
+        if (start >= before && start < before + sum) {
+            int64_t at = start - before;
+            int b = b0;
+            Seq<kRows, kKeys> q(C, b, A.group);
+            while (at >= q.all) {
+                at -= q.all;
+                q = Seq<kRows, kKeys>(C, ++b, A.group);
+            }
+            S.first = b;
+            S.offset = at;
+            Mark& M = A.marks[blockIdx.x];
+            int32_t stage;
+            q.place(at, M.head, M.row_tile, stage);
+            M.t0 = start - stage;
+            M.t1 = M.t0 + q.stages;
+            M.shares = shares;
+            M.b = b;
+        } else if (start >= total && tid == 0) {  // more CTAs than stages: an empty share at the end
+            A.marks[blockIdx.x].t0 = A.marks[blockIdx.x].t1 = start;
+        }
+        __syncthreads();
+        walk.b = S.first;
+        walk.at = S.offset;
+        walk.left = walk.b < 0 ? 0 : end - start;
+    }
+
+    Piece P;
     if (warp == kWarps) {
-        if (j1 > j0 && !feed<D, NT>(S, C, b, kvh, j0, j1, flags)) iqq::raise_flags(flags, IQQ_FLAG_WAIT_TIMEOUT);
-        __syncwarp();
-        __syncthreads();
-        __syncthreads();
+        Feed<D, NT> feed{S};
+        bool ok = true;
+        while (ok && walk.next(C, A.group, P)) {
+            const Seq<kRows, kKeys> q(C, P.b, A.group);
+            const int last_row = min(q.rows, (P.row_tile + 1) * kRows) - 1;
+            const int64_t seen = min(static_cast<int64_t>(q.len), q.s.start + last_row / A.group + 1);
+            const int64_t j0 = static_cast<int64_t>(P.from) * kKeys, j1 = min(seen, static_cast<int64_t>(P.to) * kKeys);
+            if (j1 > j0) ok = feed.keys(&kmap, &vmap, C, P.b, P.head, j0, j1, flags);
+        }
+        if (!feed.drain() || !ok) iqq::raise_flags(flags, IQQ_FLAG_WAIT_TIMEOUT);
         return;
     }
+
+    int st = 0, turn = 0;
+    uint32_t ph = 0;
+    while (walk.next(C, A.group, P)) {
+    const Seq<kRows, kKeys> Q(C, P.b, A.group);
+    const Span s = Q.s;
+    const int kvh = P.head;
+    const int32_t rows = Q.rows, first_row = P.row_tile * kRows;
+    const int64_t len = Q.len;
+    const int32_t last_row = min(rows, first_row + kRows) - 1;
+    const int64_t seen = min(len, s.start + last_row / A.group + 1);  // keys this tile's rows can see at all
+    const int64_t j0 = static_cast<int64_t>(P.from) * kKeys, j1 = min(seen, static_cast<int64_t>(P.to) * kKeys);
 
     // the rows of q this lane feeds (row g of each 8), as binary16 times 2^-e
     uint32_t bq[NT][kK][2];
@@ -243,17 +394,18 @@ decode_kernel(const Kv8 C, const Args A, uint32_t* __restrict__ flags)
     int limit[NT][2];      // keys of this CTA (from j0) below it are seen
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int64_t r = first_row + 8 * n + g;
+        const int32_t r = first_row + 8 * n + g;
         float v[D / 4];
         if (r < rows) {
-            const T* q = static_cast<const T*>(A.q) + (s.first + r / A.group) * A.q_token_stride +
-                         (kvh * A.group + r % A.group) * A.q_head_stride;
+            const int32_t token = r / A.group;
+            const T* q = static_cast<const T*>(A.q) + (s.first + token) * A.q_token_stride +
+                         (kvh * A.group + r - token * A.group) * A.q_head_stride;
 #pragma unroll
             for (int i = 0; i < D / 64; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float u[8];
-                    iqq::load8(q + 64 * i + 16 * t + 8 * h, u);
+                    iqq::load8(q + D / 4 * t + 16 * i + 8 * h, u);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[16 * i + 8 * h + e] = u[e];
                 }
@@ -273,15 +425,15 @@ decode_kernel(const Kv8 C, const Args A, uint32_t* __restrict__ flags)
         const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
         for (int j = 0; j < kK; ++j) {
-            // dimensions 64 (j/4) + 16 t + 4 (j%4) + {0, 2} and {1, 3}: as codes_even and codes_odd
-            const int i = 16 * (j >> 2) + 4 * (j & 3);
+            // dimensions D/4 t + 4 j + {0, 2} and {1, 3}: as codes_even and codes_odd
+            const int i = 4 * j;
             bq[n][j][0] = pack_h2(v[i] * down, v[i + 2] * down);
             bq[n][j][1] = pack_h2(v[i + 1] * down, v[i + 3] * down);
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             unscale[n][h] = __shfl_sync(0xffffffffu, up, (2 * t + h) * 4) * A.scale * kLog2e;
-            const int64_t row = first_row + 8 * n + 2 * t + h;
+            const int32_t row = first_row + 8 * n + 2 * t + h;
             const int64_t lim = row < rows ? min(len, s.start + row / A.group + 1) - j0 : 0;
             limit[n][h] = static_cast<int>(max(int64_t{0}, min(lim, int64_t{0x7fffffff})));
         }
@@ -304,34 +456,38 @@ decode_kernel(const Kv8 C, const Args A, uint32_t* __restrict__ flags)
             for (int i = 0; i < 4; ++i) o[n][d][i] = 0.0f;
     }
 
-    const int stages = j1 > j0 ? static_cast<int>((j1 - j0 + kKeys - 1) / kKeys) : 0;
-    int st = 0;
-    uint32_t ph = 0;
-    for (int i = 0; i < stages; ++i) {
+    const int64_t stages = j1 > j0 ? (j1 - j0 + kKeys - 1) / kKeys : 0;
+    for (int64_t i = 0; i < stages; ++i) {
         const bool late = !iqq::bar_wait(iqq::smem_u32(&S.full[st]), ph);
         if (__any_sync(0xffffffffu, late)) {
-            iqq::raise_flags(flags, IQQ_FLAG_WAIT_TIMEOUT);
+            S.abort = 1;
             break;
         }
         const int live = S.live[st];
 #pragma unroll
         for (int u = 0; u < kKeys / (16 * kWarps); ++u) {
             const int at = u * kWarps + warp;        // which 16 keys of the stage
-            const int key0 = i * kKeys + 16 * at;    // from j0
+            const int key0 = static_cast<int>(i) * kKeys + 16 * at;  // from j0
             if (live >> at & 1) {
                 const float ks = S.ks[st][at], vs = S.vs[st][at];
-                const uint8_t* kp = &S.stage[st][16 * at * D + g * D + 16 * t];
-                const uint8_t* vp = &S.stage[st][kKeys * D + 16 * at * D + 2 * t * D + D / 8 * g];
+                const uint8_t* kp = &S.stage[st][16 * at * D];
+                const uint8_t* vp = kp + kKeys * D;
                 float x[NT][4], x2[NT][4];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[n][e] = x2[n][e] = 0.0f;
-                // keys g and g+8, dimensions 16t .. of each 64; two chains of sums
+                // keys g and g+8, dimensions D/4 t ..; two chains of sums
 #pragma unroll
                 for (int h = 0; h < D / 64; ++h) {
-                    const uint4 k0 = *reinterpret_cast<const uint4*>(kp + 64 * h);
-                    const uint4 k1 = *reinterpret_cast<const uint4*>(kp + 8 * D + 64 * h);
+                    uint4 k0, k1;
+                    if constexpr (D == 128) {
+                        k0 = *reinterpret_cast<const uint4*>(kp + g * 128 + (((2 * t + h) ^ g) << 4));
+                        k1 = *reinterpret_cast<const uint4*>(kp + g * 128 + (((2 * t + h) ^ g) << 4) + 1024);
+                    } else {  // two keys a row of 128 bytes
+                        k0 = *reinterpret_cast<const uint4*>(kp + (g >> 1) * 128 + ((((g & 1) * 4 + t) ^ (g >> 1)) << 4));
+                        k1 = *reinterpret_cast<const uint4*>(kp + (4 + (g >> 1)) * 128 + ((((g & 1) * 4 + t) ^ (4 + (g >> 1))) << 4));
+                    }
                     const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -411,16 +567,24 @@ decode_kernel(const Kv8 C, const Args A, uint32_t* __restrict__ flags)
                     bp[n][1] = transpose8(pack_h2(p[2], p[3]));
                 }
                 // keys 2t, 2t+1, 2t+8, 2t+9, dimensions D/8 * g ..: 16-row tile d is bytes 2d, 2d+1
+                uint32_t v[4][D / 32];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (D == 128) {
+                        const int r = 2 * t + (e & 1);
+                        const uint4 w = *reinterpret_cast<const uint4*>(vp + (r + 8 * (e >> 1)) * 128 + ((g ^ r) << 4));
+                        v[e][0] = w.x; v[e][1] = w.y; v[e][2] = w.z; v[e][3] = w.w;
+                    } else {
+                        const int r = t + 4 * (e >> 1);
+                        const uint2 w = *reinterpret_cast<const uint2*>(vp + r * 128 + ((((e & 1) * 4 + (g >> 1)) ^ r) << 4) + 8 * (g & 1));
+                        v[e][0] = w.x; v[e][1] = w.y;
+                    }
+                }
 #pragma unroll
                 for (int h = 0; h < D / 64; ++h) {
-                    uint2 v[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        v[e] = *reinterpret_cast<const uint2*>(vp + ((e & 1) + 8 * (e >> 1)) * D + 8 * h);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const uint32_t w0 = c ? v[0].y : v[0].x, w1 = c ? v[1].y : v[1].x;
-                        const uint32_t w2 = c ? v[2].y : v[2].x, w3 = c ? v[3].y : v[3].x;
+                        const uint32_t w0 = v[0][2 * h + c], w1 = v[1][2 * h + c], w2 = v[2][2 * h + c], w3 = v[3][2 * h + c];
                         const uint32_t lo01 = __byte_perm(w0, w1, 0x5410), hi01 = __byte_perm(w0, w1, 0x7632);
                         const uint32_t lo23 = __byte_perm(w2, w3, 0x5410), hi23 = __byte_perm(w2, w3, 0x7632);
                         const uint32_t a0 = codes_even(lo01), a1 = codes_odd(lo01), a2 = codes_even(lo23), a3 = codes_odd(lo23);
@@ -437,12 +601,11 @@ decode_kernel(const Kv8 C, const Args A, uint32_t* __restrict__ flags)
         }
         __syncwarp();
         if (lane == 0) iqq::bar_arrive(iqq::smem_u32(&S.empty[st]));
-        if (++st == kStages) {
+        if (++st == Sm::kStages) {
             st = 0;
             ph ^= 1u;
         }
     }
-    __syncthreads();  // the stages' memory is free
 
     // the warps' parts meet: rows 2t, 2t+1 of each 8, dimensions D/8 * g + 2d, + 1 of tile d
 #pragma unroll
@@ -461,12 +624,17 @@ decode_kernel(const Kv8 C, const Args A, uint32_t* __restrict__ flags)
             for (int d = 0; d < kM; ++d)
                 *reinterpret_cast<float2*>(&S.o[warp][r][D / 8 * g + 2 * d]) = make_float2(o[n][d][h] * vref, o[n][d][2 + h] * vref);
         }
-    __syncthreads();
-    const bool whole = chunk >= len;  // this CTA has every key
+    meet();
+    if (S.abort) {  // (seen by all four warps together)
+        iqq::raise_flags(flags, IQQ_FLAG_WAIT_TIMEOUT);
+        break;
+    }
+    const bool whole = P.from == 0 && P.to == Q.stages;  // this CTA has every key
+    const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (turn > 0)) * kRows;
     for (int i = tid; i < kRows * (D / 4); i += kThreads) {
         const int r = i / (D / 4), d = i % (D / 4) * 4;
-        const int64_t row = first_row + r;
-        if (row >= rows) continue;
+        const int32_t row = first_row + r;
+        if (row >= rows) break;
         float top = S.m[0][r];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) top = fmaxf(top, S.m[w][r]);
@@ -487,7 +655,8 @@ decode_kernel(const Kv8 C, const Args A, uint32_t* __restrict__ flags)
         const float inv = none ? 0.0f : __fdiv_rn(1.0f, sum);
         acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
         const float lse = none ? -INFINITY : top + log2f(sum);
-        const int64_t at = (s.first + row / A.group) * A.heads + kvh * A.group + row % A.group;
+        const int32_t token = row / A.group;
+        const int64_t at = static_cast<int64_t>(s.first + token) * A.heads + kvh * A.group + row - token * A.group;
         if (whole) {
             T* out = static_cast<T*>(A.out) + at * D + d;
             out[0] = iqq::from_f32<T>(acc.x);
@@ -496,95 +665,121 @@ decode_kernel(const Kv8 C, const Args A, uint32_t* __restrict__ flags)
             out[3] = iqq::from_f32<T>(acc.w);
             if (A.lse != nullptr && d == 0) A.lse[at] = lse / kLog2e;
         } else {
-            *reinterpret_cast<float4*>(A.part + (at * A.splits + split) * D + d) = acc;
-            if (d == 0) A.part_lse[at * A.splits + split] = lse;
+            *reinterpret_cast<float4*>(A.part + (part + r) * D + d) = acc;
+            if (d == 0) A.part_lse[part + r] = lse;
         }
+    }
+    meet();  // the parts have been read
+    ++turn;
     }
 }
 
-// Joins a row's parts, each normalized and with its log-sum (base 2): a CTA a row and head, its
-// warps taking the parts in turn.
-template <class T, int D>
+// Joins the parts of a tile that shares c-1, c, c+1 .. cut, a CTA a row: CTA c takes it when its
+// share is the first to begin inside the tile.  Share c-1's part is its last piece (its first, if
+// it begins with the tile); the others begin inside, so it is their first.
+template <class T, int D, int ROWS>
 __global__ void __launch_bounds__(kThreads)
-combine_kernel(const Kv8 C, const Args A)
+combine_kernel(const Kv8 C, const Args A, const int ctas)
 {
     constexpr int kE = D / 32;
-    __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][D];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ float s_w[kMaxCtas], s_red[kWarps], s_o[kWarps][D];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x + 1, r = blockIdx.y;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t token = blockIdx.x, at = token * A.heads + blockIdx.y;
-    const int b = iqq::seq_of_slot(C, token, 1, 1, 0);
-    const Span s = iqq::span_of(C, b);
-    if (token < s.first || token >= s.first + s.n) return;
-    const int64_t len = s.len < C.capacity ? s.len : C.capacity;
-    const int64_t chunk = chunk_of(len, A.splits);
-    if (chunk >= len) return;  // written by its one CTA
-    // parts that hold keys this token sees (the first always exists)
-    const int64_t seen = max(int64_t{1}, min(len, s.start + (token - s.first) + 1));
-    const int parts = static_cast<int>((seen + chunk - 1) / chunk);
-    const float* lse = A.part_lse + at * A.splits;
-    float m = -INFINITY, l = 0.0f, o[kE] = {};
-    for (int p = warp; p < parts; p += kWarps) {
-        const float x = lse[p];
-        if (x == -INFINITY) continue;
-        const float top = fmaxf(m, x);  // (a NaN part keeps m and makes the weight NaN)
-        const float keep = m == -INFINITY ? 0.0f : ex2(m - top), w = ex2(x - (top == -INFINITY ? 0.0f : top));
-        m = top;
-        l = fmaf(l, keep, w);
-        const float* v = A.part + (at * A.splits + p) * D + lane * kE;
+    const Mark M = A.marks[c];
+    if (M.t0 == M.t1) return;
+    const int64_t prev = M.shares.start(c - 1);
+    if (M.shares.start(c) <= M.t0 || prev > M.t0) return;
+    const Span s = iqq::span_of(C, M.b);
+    const int32_t row = M.row_tile * ROWS + r;
+    if (row >= s.n * A.group) return;
+    // the shares c-1 .. end-1 have parts
+    int end;
+    {
+        int lo = c, hi = ctas;  // share lo begins before t1, share hi does not (or is none)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (M.shares.start(mid) < M.t1) lo = mid;
+            else hi = mid;
+        }
+        end = hi;
+    }
+    const int parts = end - c + 1;
+    const auto slot = [&](int p) {
+        return ((static_cast<int64_t>(c - 1 + p) * 2 + (p == 0 && prev < M.t0)) * ROWS + r);
+    };
+    // the weights of the parts: exp2 of the log-sums, less the largest
+    float top = -INFINITY;
+    for (int p = tid; p < parts; p += kThreads) {
+        const float x = M.shares.empty(c - 1 + p) ? -INFINITY : A.part_lse[slot(p)];
+        s_w[p] = x;
+        top = fmaxf(top, x);  // (skips NaN, whose part makes everything NaN)
+    }
 #pragma unroll
-        for (int e = 0; e < kE; ++e) o[e] = fmaf(o[e], keep, w * v[e]);
+    for (int o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) s_red[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_red[w]);
+    const float mu = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f, o[kE] = {};
+#pragma unroll 8
+    for (int p = warp; p < parts; p += kWarps) {
+        const float x = s_w[p];
+        if (x == -INFINITY) continue;
+        const float w = ex2(x - mu);
+        sum += w;
+        const float* v = A.part + slot(p) * D + lane * kE;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) o[e] = fmaf(w, v[e], o[e]);
     }
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
-    }
+    __syncthreads();
+    if (lane == 0) s_red[warp] = sum;
 #pragma unroll
     for (int e = 0; e < kE; ++e) s_o[warp][lane * kE + e] = o[e];
     __syncthreads();
-    const int d = threadIdx.x;
-    if (d >= D) return;
-    float top = s_m[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
-    const float mu = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f, acc = 0.0f;
+    if (tid >= D) return;
+    float acc = 0.0f;
+    sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2(s_m[w] - mu);
-        sum = fmaf(s_l[w], f, sum);
-        acc = fmaf(s_o[w][d], f, acc);
+        sum += s_red[w];
+        acc += s_o[w][tid];
     }
     const bool none = top == -INFINITY && sum == 0.0f;
-    static_cast<T*>(A.out)[at * D + d] = iqq::from_f32<T>(none ? 0.0f : acc / sum);
-    if (A.lse != nullptr && d == 0) A.lse[at] = none ? -INFINITY : (top + log2f(sum)) / kLog2e;
+    const int32_t token = row / A.group;
+    const int64_t at = static_cast<int64_t>(s.first + token) * A.heads + M.head * A.group + row - token * A.group;
+    static_cast<T*>(A.out)[at * D + tid] = iqq::from_f32<T>(none ? 0.0f : acc / sum);
+    if (A.lse != nullptr && tid == 0) A.lse[at] = none ? -INFINITY : (top + log2f(sum)) / kLog2e;
 }
 
 struct Plan {
     int row_tile;     // rows a CTA
-    int64_t slots;    // row tiles of all sequences
-    int splits;
+    int64_t ctas;     // shares
+    size_t marks, part, lse;  // bytes of the workspace's parts
 };
 
-// The launch goes by shapes alone (lengths are on the device).  Row tiles of 8 while a sequence's
-// share of the tokens fits, else of 16.  Splits fill the machine about four CTAs an SM deep when
-// every sequence is as long as the table is wide, but leave a CTA kMinChunk keys.
+// The launch goes by shapes alone (lengths are on the device): row tiles of 8 while a sequence's
+// share of the tokens fits, else of 16; as many CTAs as fit the machine, or fewer where the tables
+// leave less than a stage each.
 Plan plan_of(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int64_t n_heads, int64_t n_tokens)
 {
     Plan p;
-    const int64_t group = n_heads / cache->n_kv_heads;
+    const int64_t group = n_heads / cache->n_kv_heads, keys = kStageBytes / (2 * cache->head_dim);
     const int64_t each = (n_tokens + seqs->n_seqs - 1) / seqs->n_seqs * group;
     p.row_tile = each <= 8 ? 8 : 16;
-    p.slots = n_tokens * group / p.row_tile + seqs->n_seqs;
-    const int64_t ctas = p.slots * cache->n_kv_heads, capacity = seqs->table_width * cache->page_size;
-    const int64_t want = (8LL * iqq::sm_count() + ctas - 1) / ctas, most = (capacity + kMinChunk - 1) / kMinChunk;
-    p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, most, 1024})));
+    const int64_t tiles = (n_tokens * group / p.row_tile + seqs->n_seqs) * cache->n_kv_heads;
+    const int64_t stages = std::max<int64_t>(1, (seqs->table_width * cache->page_size + keys - 1) / keys);
+    const int64_t most = std::min<int64_t>(kMaxCtas, (p.row_tile == 8 ? 3 : 2) * iqq::sm_count());
+    p.ctas = tiles >= most ? most : std::min<int64_t>(most, tiles * std::min<int64_t>(stages, most));
+    p.marks = (static_cast<size_t>(p.ctas) * sizeof(Mark) + 15) / 16 * 16;
+    p.part = static_cast<size_t>(p.ctas) * 2 * p.row_tile * cache->head_dim * sizeof(float);
+    p.lse = static_cast<size_t>(p.ctas) * 2 * p.row_tile * sizeof(float);
     return p;
 }
 
-template <class K>
-iqq_status start(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t st, const Kv8& C, const Args& A, uint32_t* flags)
+template <class... P, class... A>
+iqq_status start(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -596,37 +791,35 @@ iqq_status start(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t st,
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if constexpr (std::is_invocable_v<K, Kv8, Args, uint32_t*>)
-        cudaLaunchKernelEx(&cfg, kernel, C, A, flags);
-    else
-        cudaLaunchKernelEx(&cfg, kernel, C, A);
+    cudaLaunchKernelEx(&cfg, kernel, args...);
     return iqq::launch_status();
 }
 
 template <class T, int D, int NT>
-iqq_status start_decode(const Kv8& C, const Args& A, const Plan& p, cudaStream_t st, uint32_t* flags)
+iqq_status launch(const Kv8& C, const Args& A, const Plan& p, cudaStream_t st, uint32_t* flags)
 {
     static std::atomic<uint64_t> done{0};
     constexpr size_t smem = sizeof(Smem<D, NT>);
-    const iqq_status s = iqq::opt_in_smem(reinterpret_cast<const void*>(decode_kernel<T, D, NT>), smem, done);
+    iqq_status s = iqq::opt_in_smem(reinterpret_cast<const void*>(decode_kernel<T, D, NT>), smem, done);
     if (s != IQQ_OK) return s;
-    const dim3 grid(static_cast<unsigned>(p.slots), static_cast<unsigned>(p.splits), static_cast<unsigned>(C.heads));
-    return start(decode_kernel<T, D, NT>, grid, kThreads + 32, smem, st, C, A, flags);
-}
-
-template <class T, int D>
-iqq_status launch(const Kv8& C, const Args& A, const Plan& p, cudaStream_t st, uint32_t* flags)
-{
-    const iqq_status s = p.row_tile == 8 ? start_decode<T, D, 1>(C, A, p, st, flags) : start_decode<T, D, 2>(C, A, p, st, flags);
-    if (s != IQQ_OK || p.splits == 1) return s;
-    return start(combine_kernel<T, D>, dim3(static_cast<unsigned>(C.n_tokens), static_cast<unsigned>(A.heads)), kThreads, 0,
-                 st, C, A, flags);
+    // the codes as rows of 128 bytes, read as much of a page at a time as a stage takes
+    CUtensorMap maps[2];
+    const int64_t rows = (static_cast<int64_t>(C.n_pages) * C.heads << C.page_log2) * D / 128;
+    const int box = std::min(Smem<D, NT>::kKeys, 1 << C.page_log2) * D / 128;
+    for (int i = 0; i < 2; ++i) {
+        s = iqq::byte_map(&maps[i], C.codes[i], 128, rows, 128, box);
+        if (s != IQQ_OK) return s;
+    }
+    s = start(decode_kernel<T, D, NT>, dim3(static_cast<unsigned>(p.ctas)), kThreads + 32, smem, st, maps[0], maps[1], C, A, flags);
+    if (s != IQQ_OK || p.ctas == 1) return s;
+    return start(combine_kernel<T, D, 8 * NT>, dim3(static_cast<unsigned>(p.ctas - 1), 8 * NT), kThreads, 0, st, C, A,
+                 static_cast<int>(p.ctas));
 }
 
 bool shapes_ok(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int64_t n_heads, int64_t n_tokens)
 {
     return cache != nullptr && seqs != nullptr && cache->n_kv_heads >= 1 && n_heads >= 1 && n_heads <= 65535 &&
-           n_heads % cache->n_kv_heads == 0 && n_tokens >= 1 && n_tokens <= 0x7fffffffLL && seqs->n_seqs >= 1 &&
+           n_heads % cache->n_kv_heads == 0 && n_tokens >= 1 && n_tokens <= 0x7fffffffLL / n_heads && seqs->n_seqs >= 1 &&
            seqs->n_seqs <= (1LL << 24) && cache->page_size >= 1 && seqs->table_width >= 0;
 }
 
@@ -637,8 +830,7 @@ extern "C" size_t iqq_kv8_attention_workspace_bytes(const iqq_kv8_cache* cache, 
 {
     if (!shapes_ok(cache, seqs, n_heads, n_tokens)) return 0;
     const Plan p = plan_of(cache, seqs, n_heads, n_tokens);
-    if (p.splits == 1) return 0;
-    return static_cast<size_t>(n_tokens) * n_heads * p.splits * (cache->head_dim + 1) * sizeof(float);
+    return p.marks + p.part + p.lse;
 }
 
 extern "C" iqq_status iqq_kv8_attention(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int dtype, const void* q,
@@ -653,11 +845,11 @@ extern "C" iqq_status iqq_kv8_attention(const iqq_kv8_cache* cache, const iqq_kv
     if (c != IQQ_OK) return c;
     if (n_tokens == 1) q_token_stride = 0;
     if (n_heads == 1) q_head_stride = 0;
-    if (n_heads < 1 || n_heads % C.heads != 0 || n_heads > 65535 || q_token_stride < 0 || q_head_stride < 0)
+    if (n_heads < 1 || n_heads % C.heads != 0 || n_heads > 65535 || q_token_stride < 0 || q_head_stride < 0 ||
+        n_tokens * n_heads > 0x7fffffffLL)
         return IQQ_ERR_SHAPE;
     if (n_tokens == 0 || C.n_seqs == 0) return IQQ_OK;
     const Plan p = plan_of(cache, seqs, n_heads, n_tokens);
-    if (p.slots > 0x7fffffffLL) return IQQ_ERR_SHAPE;
     const size_t need = iqq_kv8_attention_workspace_bytes(cache, seqs, n_heads, n_tokens);
     if (q == nullptr || out == nullptr || (need > 0 && workspace == nullptr)) return IQQ_ERR_NULL;
     if (workspace_bytes < need) return IQQ_ERR_SHAPE;
@@ -672,13 +864,17 @@ extern "C" iqq_status iqq_kv8_attention(const iqq_kv8_cache* cache, const iqq_kv
     A.q_head_stride = q_head_stride;
     A.heads = static_cast<int32_t>(n_heads);
     A.group = static_cast<int32_t>(n_heads / C.heads);
-    A.splits = p.splits;
     A.scale = scale;
-    A.part = static_cast<float*>(workspace);
-    if (need > 0) A.part_lse = A.part + n_tokens * n_heads * p.splits * cache->head_dim;
+    char* ws = static_cast<char*>(workspace);
+    A.marks = reinterpret_cast<Mark*>(ws);
+    A.part = reinterpret_cast<float*>(ws + p.marks);
+    A.part_lse = reinterpret_cast<float*>(ws + p.marks + p.part);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool wide = cache->head_dim == 128;
-    if (dtype == IQQ_BF16)
-        return wide ? launch<__nv_bfloat16, 128>(C, A, p, st, d_flags) : launch<__nv_bfloat16, 64>(C, A, p, st, d_flags);
-    return wide ? launch<__half, 128>(C, A, p, st, d_flags) : launch<__half, 64>(C, A, p, st, d_flags);
+    const auto go = [&](auto zero) {
+        using T = decltype(zero);
+        if (cache->head_dim == 128)
+            return p.row_tile == 8 ? launch<T, 128, 1>(C, A, p, st, d_flags) : launch<T, 128, 2>(C, A, p, st, d_flags);
+        return p.row_tile == 8 ? launch<T, 64, 1>(C, A, p, st, d_flags) : launch<T, 64, 2>(C, A, p, st, d_flags);
+    };
+    return dtype == IQQ_BF16 ? go(__nv_bfloat16{}) : go(__half{});
 }

@@ -205,8 +205,8 @@ iqq_status iqq::kv8_check(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, 
         return IQQ_ERR_SHAPE;
     if (seqs->n_seqs > 1 && seqs->table_stride < seqs->table_width) return IQQ_ERR_SHAPE;
     if (seqs->n_seqs > 0 && n_tokens > 0) {
-        if (cache->n_pages > 0 && (cache->k_codes == nullptr || cache->v_codes == nullptr || cache->k_scales == nullptr ||
-                                   cache->v_scales == nullptr))
+        if (cache->n_pages == 0) return IQQ_ERR_SHAPE;
+        if (cache->k_codes == nullptr || cache->v_codes == nullptr || cache->k_scales == nullptr || cache->v_scales == nullptr)
             return IQQ_ERR_NULL;
         if (seqs->seq_lens == nullptr || seqs->cu_tokens == nullptr ||
             (seqs->table_width > 0 && seqs->block_tables == nullptr))
