@@ -8,7 +8,7 @@
 //
 // decode kernel (few rows a sequence).  Bound by the cache's bytes.  One warp streams the pages'
 // tiles into a ring of stages (cp.async.bulk, the scales beside them by cp.async); four warps
-// take 16 keys of a stage each, straight into the operand registers of mma.m16n8k16:
+// take 32 keys of a stage each, straight into the operand registers of mma.m16n8k16:
 //     S^T = K Q^T (16 keys x 8 rows),  O^T = V^T P^T (16 dimensions x 8 rows).
 // The order of the dimensions in a dot product, and of the rows of V^T, is free, so each lane
 // reads 16 contiguous bytes and nothing is transposed through shared memory; P^T goes from the
@@ -40,9 +40,10 @@ using iqq::Span;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;       // that compute; one more warp loads
-constexpr int kStageBytes = 16384;          // keys and values of a stage
+constexpr int kKeys = 128;                  // keys of a stage: 32 a warp
 constexpr int kMaxCtas = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNone = -3.4028234663852886e38f;  // the maximum of no score: below every finite one
 
 struct Args {
     const void* q;
@@ -79,12 +80,12 @@ struct Shares {
 struct Mark {
     int64_t t0, t1;
     Shares shares;
-    int32_t b, head, row_tile;
+    int32_t token, head, row0, rows;  // the sequence's first packed row; the tile's first row, and how many
 };
 
 // A sequence as the launch sees it.  (n_tokens * heads < 2^31, so a sequence's rows and, with its
 // length below 2^31, its stages fit 32 bits; the stages of all its tiles need not.)
-template <int ROWS, int KEYS>
+template <int ROWS>
 struct Seq {
     Span s;
     int32_t rows, tiles, len, stages;
@@ -95,7 +96,7 @@ struct Seq {
         rows = s.n * group;  // 0 for a bad span
         tiles = (rows + ROWS - 1) / ROWS;
         len = static_cast<int32_t>(s.len < C.capacity ? s.len : C.capacity);
-        stages = len <= 0 ? 1 : static_cast<int32_t>((static_cast<uint32_t>(len) + KEYS - 1) / KEYS);  // no key: one, for the zeros
+        stages = len <= 0 ? 1 : static_cast<int32_t>((static_cast<uint32_t>(len) + kKeys - 1) / kKeys);  // no key: one, for the zeros
         all = static_cast<int64_t>(tiles) * stages * C.heads;
     }
     // Tile and stage within it of the sequence's stage `at`.
@@ -141,7 +142,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a)
 }
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -152,10 +153,10 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 // at c ^ (r & 7)), so the operand reads below meet no bank twice; and the scales of each 16 keys.
 template <int D, int NT>
 struct Smem {
-    static constexpr int kRows = 8 * NT, kKeys = kStageBytes / (2 * D), kStages = NT == 1 ? 3 : 4;
-    uint8_t stage[kStages][kStageBytes];
-    float o[kWarps][kRows][D];      // the warps' parts of a tile
-    float m[kWarps][kRows], l[kWarps][kRows];
+    static constexpr int kRows = 8 * NT, kStages = D == 128 ? (NT == 1 ? 2 : 3) : 4, kHalf = kKeys * D;
+    uint8_t stage[kStages][2 * kHalf];
+    float4 o[2][NT * D / 16][32];   // accumulators of two warps, as their lanes hold them
+    float m[2][kRows], l[2][kRows];
     float ks[kStages][kKeys / 16], vs[kStages][kKeys / 16];
     int live[kStages];              // which 16 keys have a page, a bit each
     uint64_t full[kStages], empty[kStages];
@@ -169,14 +170,14 @@ struct Piece {
 };
 
 // A CTA's walk through its share: sequence b, `at` stages into it, `left` to go.
-template <int ROWS, int KEYS>
+template <int ROWS>
 struct Walk {
     int b;
     int64_t at, left;
     __device__ __forceinline__ bool next(const Kv8& C, int group, Piece& P)
     {
         while (left > 0 && b < C.n_seqs) {
-            const Seq<ROWS, KEYS> q(C, b, group);
+            const Seq<ROWS> q(C, b, group);
             if (at >= q.all) {
                 at = 0;
                 ++b;
@@ -206,7 +207,7 @@ __device__ __forceinline__ void async_arrive(uint32_t bar)
 // The loading warp's ring, over all pieces of its share.
 template <int D, int NT>
 struct Feed {
-    static constexpr int kKeys = Smem<D, NT>::kKeys, kStages = Smem<D, NT>::kStages;
+    static constexpr int kStages = Smem<D, NT>::kStages;
     Smem<D, NT>& S;
     int s = 0;
     uint32_t ph = 0;
@@ -252,7 +253,7 @@ struct Feed {
                     const int row = static_cast<int>(((cell << C.page_log2) + (key & ((1 << C.page_log2) - 1))) * D / 128);
                     const uint32_t to = iqq::smem_u32(&S.stage[s][0]) + u * piece * D;
                     iqq::tma_load(to, kmap, 0, row, bar);
-                    iqq::tma_load(to + kKeys * D, vmap, 0, row, bar);
+                    iqq::tma_load(to + Smem<D, NT>::kHalf, vmap, 0, row, bar);
                     for (int k = 0; k < piece / 16; ++k) {
                         async_load4(iqq::smem_u32(&S.ks[s][u * (piece / 16) + k]), C.scales[0] + cell);
                         async_load4(iqq::smem_u32(&S.vs[s][u * (piece / 16) + k]), C.scales[1] + cell);
@@ -288,7 +289,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               uint32_t* __restrict__ flags)
 {
     using Sm = Smem<D, NT>;
-    constexpr int kRows = Sm::kRows, kKeys = Sm::kKeys, kK = D / 16, kM = D / 16;  // k steps of S, 16-row tiles of O^T
+    constexpr int kRows = Sm::kRows, kK = D / 16, kM = D / 16;  // k steps of S, 16-row tiles of O^T
     extern __shared__ __align__(1024) uint8_t raw[];
     Sm& S = *reinterpret_cast<Sm*>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -307,13 +308,13 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // Where this CTA's share begins: a scan over the sequences, a run of them a thread.
-    Walk<kRows, kKeys> walk;
+    Walk<kRows> walk;
     {
         const int run = (C.n_seqs + kThreads + 31) / (kThreads + 32), b0 = min(C.n_seqs, tid * run), b1 = min(C.n_seqs, b0 + run);
         int64_t sum = 0;
         bool bad = false;
         for (int b = b0; b < b1; ++b) {
-            const Seq<kRows, kKeys> q(C, b, A.group);
+            const Seq<kRows> q(C, b, A.group);
             sum += q.all;
             bad |= !q.s.ok || q.s.len > C.capacity;
         }
@@ -338,20 +339,23 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         if (start >= before && start < before + sum) {
             int64_t at = start - before;
             int b = b0;
-            Seq<kRows, kKeys> q(C, b, A.group);
+            Seq<kRows> q(C, b, A.group);
             while (at >= q.all) {
                 at -= q.all;
-                q = Seq<kRows, kKeys>(C, ++b, A.group);
+                q = Seq<kRows>(C, ++b, A.group);
             }
             S.first = b;
             S.offset = at;
-            Mark& M = A.marks[blockIdx.x];
-            int32_t stage;
-            q.place(at, M.head, M.row_tile, stage);
+            Mark M;
+            int32_t stage, row_tile;
+            q.place(at, M.head, row_tile, stage);
             M.t0 = start - stage;
             M.t1 = M.t0 + q.stages;
             M.shares = shares;
-            M.b = b;
+            M.token = q.s.first;
+            M.row0 = row_tile * kRows;
+            M.rows = min(kRows, q.rows - M.row0);
+            A.marks[blockIdx.x] = M;
         } else if (start >= total && tid == 0) {  // more CTAs than stages: an empty share at the end
             A.marks[blockIdx.x].t0 = A.marks[blockIdx.x].t1 = start;
         }
@@ -366,7 +370,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         Feed<D, NT> feed{S};
         bool ok = true;
         while (ok && walk.next(C, A.group, P)) {
-            const Seq<kRows, kKeys> q(C, P.b, A.group);
+            const Seq<kRows> q(C, P.b, A.group);
             const int last_row = min(q.rows, (P.row_tile + 1) * kRows) - 1;
             const int64_t seen = min(static_cast<int64_t>(q.len), q.s.start + last_row / A.group + 1);
             const int64_t j0 = static_cast<int64_t>(P.from) * kKeys, j1 = min(seen, static_cast<int64_t>(P.to) * kKeys);
@@ -379,7 +383,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     int st = 0, turn = 0;
     uint32_t ph = 0;
     while (walk.next(C, A.group, P)) {
-    const Seq<kRows, kKeys> Q(C, P.b, A.group);
+    const Seq<kRows> Q(C, P.b, A.group);
     const Span s = Q.s;
     const int kvh = P.head;
     const int32_t rows = Q.rows, first_row = P.row_tile * kRows;
@@ -434,20 +438,20 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         for (int h = 0; h < 2; ++h) {
             unscale[n][h] = __shfl_sync(0xffffffffu, up, (2 * t + h) * 4) * A.scale * kLog2e;
             const int32_t row = first_row + 8 * n + 2 * t + h;
-            const int64_t lim = row < rows ? min(len, s.start + row / A.group + 1) - j0 : 0;
+            const int64_t lim = row < rows ? min(len, s.start + row / A.group + 1) - j0 : 0x7fffffff;  // (padding: no mask)
             limit[n][h] = static_cast<int>(max(int64_t{0}, min(lim, int64_t{0x7fffffff})));
         }
     }
     // below this key (from j0) no row of the tile needs a mask
     const int64_t clear64 = min(len, s.start + first_row / A.group + 1) - j0;
-    const int clear = last_row - first_row + 1 == kRows ? static_cast<int>(max(int64_t{0}, min(clear64, int64_t{0x7fffffff}))) : 0;
+    const int clear = static_cast<int>(max(int64_t{0}, min(clear64, int64_t{0x7fffffff})));
 
-    float m[NT][2], l[NT][2], o[NT][kM][4], vref = 0.0f;
+    float m[NT][2], l[NT][2], o[NT][kM][4], vref = 0.0f, vinv = 1.0f;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            m[n][h] = -INFINITY;
+            m[n][h] = kNone;
             l[n][h] = 0.0f;
         }
 #pragma unroll
@@ -463,139 +467,145 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             S.abort = 1;
             break;
         }
-        const int live = S.live[st];
+        const int key0 = static_cast<int>(i) * kKeys + 32 * warp;  // from j0
+        const uint8_t* kp = &S.stage[st][32 * warp * D];
+        const uint8_t* vp = kp + Sm::kHalf;
+        // scores: x[u][n] of keys 16u + g and 16u + g + 8 (elements 0, 1 and 2, 3), rows 2t, 2t+1
+        float x[2][NT][4], vs[2];
 #pragma unroll
-        for (int u = 0; u < kKeys / (16 * kWarps); ++u) {
-            const int at = u * kWarps + warp;        // which 16 keys of the stage
-            const int key0 = static_cast<int>(i) * kKeys + 16 * at;  // from j0
-            if (live >> at & 1) {
-                const float ks = S.ks[st][at], vs = S.vs[st][at];
-                const uint8_t* kp = &S.stage[st][16 * at * D];
-                const uint8_t* vp = kp + kKeys * D;
-                float x[NT][4], x2[NT][4];
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[u][n][e] = 0.0f;
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {
+                // keys g and g+8, dimensions D/4 t ..
+                uint4 k0, k1;
+                const uint8_t* k = kp + 16 * u * D;
+                if constexpr (D == 128) {
+                    k0 = *reinterpret_cast<const uint4*>(k + g * 128 + (((2 * t + h) ^ g) << 4));
+                    k1 = *reinterpret_cast<const uint4*>(k + g * 128 + (((2 * t + h) ^ g) << 4) + 1024);
+                } else {  // two keys a row of 128 bytes
+                    k0 = *reinterpret_cast<const uint4*>(k + (g >> 1) * 128 + ((((g & 1) * 4 + t) ^ (g >> 1)) << 4));
+                    k1 = *reinterpret_cast<const uint4*>(k + (4 + (g >> 1)) * 128 + ((((g & 1) * 4 + t) ^ (4 + (g >> 1))) << 4));
+                }
+                const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t a0 = codes_even(w0[c]), a2 = codes_odd(w0[c]);
+                    const uint32_t a1 = codes_even(w1[c]), a3 = codes_odd(w1[c]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma(x[u][n], a0, a1, a2, a3, bq[n][4 * h + c][0], bq[n][4 * h + c][1]);
+                }
+            }
+            const float ks = S.ks[st][2 * warp + u];
+            vs[u] = S.vs[st][2 * warp + u];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[u][n][e] *= unscale[n][e & 1] * ks;
+        }
+        const int live = S.live[st] >> (2 * warp);
+        const bool masked = key0 + 32 > clear || (live & 3) != 3;
+        if (masked) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const bool dead = !(live >> u & 1);
+                if (dead) vs[u] = 0.0f;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[n][e] = x2[n][e] = 0.0f;
-                // keys g and g+8, dimensions D/4 t ..; two chains of sums
+                    for (int e = 0; e < 4; ++e)
+                        if (dead || key0 + 16 * u + g + (e & 2) * 4 >= limit[n][e & 1]) x[u][n][e] = -INFINITY;
+            }
+        }
+        bool moved = false;
+        float top[NT][2];
 #pragma unroll
-                for (int h = 0; h < D / 64; ++h) {
-                    uint4 k0, k1;
-                    if constexpr (D == 128) {
-                        k0 = *reinterpret_cast<const uint4*>(kp + g * 128 + (((2 * t + h) ^ g) << 4));
-                        k1 = *reinterpret_cast<const uint4*>(kp + g * 128 + (((2 * t + h) ^ g) << 4) + 1024);
-                    } else {  // two keys a row of 128 bytes
-                        k0 = *reinterpret_cast<const uint4*>(kp + (g >> 1) * 128 + ((((g & 1) * 4 + t) ^ (g >> 1)) << 4));
-                        k1 = *reinterpret_cast<const uint4*>(kp + (4 + (g >> 1)) * 128 + ((((g & 1) * 4 + t) ^ (4 + (g >> 1))) << 4));
-                    }
-                    const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int j = 4 * h + c;
-                        const uint32_t a0 = codes_even(w0[c]), a2 = codes_odd(w0[c]);
-                        const uint32_t a1 = codes_even(w1[c]), a3 = codes_odd(w1[c]);
+            for (int h = 0; h < 2; ++h) {
+                top[n][h] = fmaxf(fmaxf(x[0][n][h], x[0][n][2 + h]), fmaxf(x[1][n][h], x[1][n][2 + h]));
+                moved |= top[n][h] > m[n][h] + 8.0f;
+            }
+        if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma(c & 1 ? x2[n] : x[n], a0, a1, a2, a3, bq[n][j][0], bq[n][j][1]);
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float v = fmaxf(top[n][h], m[n][h]);
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                    const float f = ex2(m[n][h] - v);
+                    m[n][h] = v;
+                    l[n][h] *= f;
+#pragma unroll
+                    for (int d = 0; d < kM; ++d) {
+                        o[n][d][h] *= f;
+                        o[n][d][2 + h] *= f;
                     }
                 }
+        }
+        if (vs[0] > vref || vs[1] > vref) {  // (uniform) the next power of two above the larger
+            const uint32_t up = (__float_as_uint(fmaxf(vs[0], vs[1])) & 0x7f800000u) + 0x00800000u;
+            const float f = vref * __uint_as_float(0x7f000000u - up);  // over a power of two: exact
+            vref = __uint_as_float(up);
+            vinv = __uint_as_float(0x7f000000u - up);
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[n][e] += x2[n][e];
-                const bool masked = key0 + 16 > clear;
-                bool moved = false;
+                for (int d = 0; d < kM; ++d)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[n][d][e] *= f;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const float vf = vs[u] * vinv;
+            uint32_t bp[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p[e] = ex2(x[u][n][e] - m[n][e & 1]);
+                l[n][0] += p[0] + p[2];
+                l[n][1] += p[1] + p[3];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p[e] *= vf;
+                if (masked) {  // (a hidden key's page may have the scale NaN)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (x[u][n][e] == -INFINITY) p[e] = 0.0f;
+                }
+                bp[n][0] = transpose8(pack_h2(p[0], p[1]));
+                bp[n][1] = transpose8(pack_h2(p[2], p[3]));
+            }
+            // keys 2t, 2t+1, 2t+8, 2t+9, dimensions D/8 g ..: 16-row tile d is bytes 2d, 2d+1
+            uint32_t v[4][D / 32];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint8_t* w = vp + 16 * u * D;
+                if constexpr (D == 128) {
+                    const int r = 2 * t + (e & 1);
+                    const uint4 c = *reinterpret_cast<const uint4*>(w + (r + 8 * (e >> 1)) * 128 + ((g ^ r) << 4));
+                    v[e][0] = c.x; v[e][1] = c.y; v[e][2] = c.z; v[e][3] = c.w;
+                } else {
+                    const int r = t + 4 * (e >> 1);
+                    const uint2 c = *reinterpret_cast<const uint2*>(w + r * 128 + ((((e & 1) * 4 + (g >> 1)) ^ r) << 4) + 8 * (g & 1));
+                    v[e][0] = c.x; v[e][1] = c.y;
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                const uint32_t lo01 = __byte_perm(v[0][c], v[1][c], 0x5410), hi01 = __byte_perm(v[0][c], v[1][c], 0x7632);
+                const uint32_t lo23 = __byte_perm(v[2][c], v[3][c], 0x5410), hi23 = __byte_perm(v[2][c], v[3][c], 0x7632);
+                const uint32_t a0 = codes_even(lo01), a1 = codes_odd(lo01), a2 = codes_even(lo23), a3 = codes_odd(lo23);
+                const uint32_t c0 = codes_even(hi01), c1 = codes_odd(hi01), c2 = codes_even(hi23), c3 = codes_odd(hi23);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float f = unscale[n][h] * ks;
-                        x[n][h] *= f;
-                        x[n][2 + h] *= f;
-                        if (masked) {
-                            if (key0 + g >= limit[n][h]) x[n][h] = -INFINITY;
-                            if (key0 + g + 8 >= limit[n][h]) x[n][2 + h] = -INFINITY;
-                        }
-                        moved |= fmaxf(x[n][h], x[n][2 + h]) > m[n][h] + 8.0f;
-                    }
-                }
-                if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float top = fmaxf(x[n][h], x[n][2 + h]);
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                            top = fmaxf(top, m[n][h]);
-                            const float f = top == -INFINITY ? 1.0f : ex2(m[n][h] - top);
-                            m[n][h] = top;
-                            l[n][h] *= f;
-#pragma unroll
-                            for (int d = 0; d < kM; ++d) {
-                                o[n][d][h] *= f;
-                                o[n][d][2 + h] *= f;
-                            }
-                        }
-                }
-                if (vs > vref) {  // (uniform) the next power of two above vs
-                    const float up = __uint_as_float((__float_as_uint(vs) & 0x7f800000u) + 0x00800000u);
-                    const float f = vref == 0.0f ? 1.0f : __fdiv_rn(vref, up);
-                    vref = up;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int d = 0; d < kM; ++d)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) o[n][d][e] *= f;
-                }
-                const float vf = vs == 0.0f ? 0.0f : __fdiv_rn(vs, vref == 0.0f ? 1.0f : vref);
-                uint32_t bp[NT][2];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float p[4];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float mu = m[n][h] == -INFINITY ? 0.0f : m[n][h];
-                        p[h] = ex2(x[n][h] - mu);
-                        p[2 + h] = ex2(x[n][2 + h] - mu);
-                        l[n][h] += p[h] + p[2 + h];
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) p[e] = x[n][e] == -INFINITY ? 0.0f : p[e] * vf;
-                    bp[n][0] = transpose8(pack_h2(p[0], p[1]));
-                    bp[n][1] = transpose8(pack_h2(p[2], p[3]));
-                }
-                // keys 2t, 2t+1, 2t+8, 2t+9, dimensions D/8 * g ..: 16-row tile d is bytes 2d, 2d+1
-                uint32_t v[4][D / 32];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (D == 128) {
-                        const int r = 2 * t + (e & 1);
-                        const uint4 w = *reinterpret_cast<const uint4*>(vp + (r + 8 * (e >> 1)) * 128 + ((g ^ r) << 4));
-                        v[e][0] = w.x; v[e][1] = w.y; v[e][2] = w.z; v[e][3] = w.w;
-                    } else {
-                        const int r = t + 4 * (e >> 1);
-                        const uint2 w = *reinterpret_cast<const uint2*>(vp + r * 128 + ((((e & 1) * 4 + (g >> 1)) ^ r) << 4) + 8 * (g & 1));
-                        v[e][0] = w.x; v[e][1] = w.y;
-                    }
-                }
-#pragma unroll
-                for (int h = 0; h < D / 64; ++h) {
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const uint32_t w0 = v[0][2 * h + c], w1 = v[1][2 * h + c], w2 = v[2][2 * h + c], w3 = v[3][2 * h + c];
-                        const uint32_t lo01 = __byte_perm(w0, w1, 0x5410), hi01 = __byte_perm(w0, w1, 0x7632);
-                        const uint32_t lo23 = __byte_perm(w2, w3, 0x5410), hi23 = __byte_perm(w2, w3, 0x7632);
-                        const uint32_t a0 = codes_even(lo01), a1 = codes_odd(lo01), a2 = codes_even(lo23), a3 = codes_odd(lo23);
-                        const uint32_t c0 = codes_even(hi01), c1 = codes_odd(hi01), c2 = codes_even(hi23), c3 = codes_odd(hi23);
-                        const int d = 4 * h + 2 * c;
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            mma(o[n][d], a0, a1, a2, a3, bp[n][0], bp[n][1]);
-                            mma(o[n][d + 1], c0, c1, c2, c3, bp[n][0], bp[n][1]);
-                        }
-                    }
+                    mma(o[n][2 * c], a0, a1, a2, a3, bp[n][0], bp[n][1]);
+                    mma(o[n][2 * c + 1], c0, c1, c2, c3, bp[n][0], bp[n][1]);
                 }
             }
         }
@@ -607,7 +617,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
     }
 
-    // the warps' parts meet: rows 2t, 2t+1 of each 8, dimensions D/8 * g + 2d, + 1 of tile d
+    // the warps' parts meet: 2 and 3 with 0 and 1, then 1 with 0; lane g, t holds rows 2t, 2t+1 of
+    // each 8, dimensions D/8 g + 2d, + 1 of tile d
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -615,84 +626,109 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             l[n][h] += __shfl_xor_sync(0xffffffffu, l[n][h], 4);
             l[n][h] += __shfl_xor_sync(0xffffffffu, l[n][h], 8);
             l[n][h] += __shfl_xor_sync(0xffffffffu, l[n][h], 16);
-            const int r = 8 * n + 2 * t + h;
-            if (g == 0) {
-                S.m[warp][r] = m[n][h];
-                S.l[warp][r] = l[n][h];
-            }
-#pragma unroll
-            for (int d = 0; d < kM; ++d)
-                *reinterpret_cast<float2*>(&S.o[warp][r][D / 8 * g + 2 * d]) = make_float2(o[n][d][h] * vref, o[n][d][2 + h] * vref);
         }
-    meet();
-    if (S.abort) {  // (seen by all four warps together)
+#pragma unroll
+    for (int step = 2; step > 0; step /= 2) {
+        if (warp >= step && warp < 2 * step) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (g == 0) {
+                        S.m[warp - step][8 * n + 2 * t + h] = m[n][h];
+                        S.l[warp - step][8 * n + 2 * t + h] = l[n][h];
+                    }
+#pragma unroll
+                for (int d = 0; d < kM; ++d)
+                    S.o[warp - step][n * kM + d][lane] = make_float4(o[n][d][0] * vref, o[n][d][1] * vref, o[n][d][2] * vref, o[n][d][3] * vref);
+            }
+        }
+        meet();
+        if (step == 2 && S.abort) break;  // (all four warps together)
+        if (warp < step) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float own[2], other[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float mo = S.m[warp][8 * n + 2 * t + h], v = fmaxf(m[n][h], mo);
+                    own[h] = ex2(m[n][h] - v);
+                    other[h] = ex2(mo - v);
+                    l[n][h] = fmaf(l[n][h], own[h], S.l[warp][8 * n + 2 * t + h] * other[h]);
+                    m[n][h] = v;
+                    own[h] *= vref;
+                }
+#pragma unroll
+                for (int d = 0; d < kM; ++d) {
+                    const float4 v = S.o[warp][n * kM + d][lane];
+                    o[n][d][0] = fmaf(o[n][d][0], own[0], v.x * other[0]);
+                    o[n][d][1] = fmaf(o[n][d][1], own[1], v.y * other[1]);
+                    o[n][d][2] = fmaf(o[n][d][2], own[0], v.z * other[0]);
+                    o[n][d][3] = fmaf(o[n][d][3], own[1], v.w * other[1]);
+                }
+            }
+            vref = 1.0f;
+        }
+        meet();
+    }
+    if (S.abort) {
         iqq::raise_flags(flags, IQQ_FLAG_WAIT_TIMEOUT);
         break;
     }
-    const bool whole = P.from == 0 && P.to == Q.stages;  // this CTA has every key
-    const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (turn > 0)) * kRows;
-    for (int i = tid; i < kRows * (D / 4); i += kThreads) {
-        const int r = i / (D / 4), d = i % (D / 4) * 4;
-        const int32_t row = first_row + r;
-        if (row >= rows) break;
-        float top = S.m[0][r];
+    if (warp == 0) {
+        const bool whole = P.from == 0 && P.to == Q.stages;  // this CTA has every key
+        const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (turn > 0)) * kRows;
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, S.m[w][r]);
-        const float mu = top == -INFINITY ? 0.0f : top;
-        float sum = 0.0f;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = ex2(S.m[w][r] - mu);
-            sum = fmaf(S.l[w][r], f, sum);
-            const float4 v = *reinterpret_cast<const float4*>(&S.o[w][r][d]);
-            acc.x = fmaf(v.x, f, acc.x);
-            acc.y = fmaf(v.y, f, acc.y);
-            acc.z = fmaf(v.z, f, acc.z);
-            acc.w = fmaf(v.w, f, acc.w);
-        }
-        const bool none = top == -INFINITY && sum == 0.0f;
-        const float inv = none ? 0.0f : __fdiv_rn(1.0f, sum);
-        acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
-        const float lse = none ? -INFINITY : top + log2f(sum);
-        const int32_t token = row / A.group;
-        const int64_t at = static_cast<int64_t>(s.first + token) * A.heads + kvh * A.group + row - token * A.group;
-        if (whole) {
-            T* out = static_cast<T*>(A.out) + at * D + d;
-            out[0] = iqq::from_f32<T>(acc.x);
-            out[1] = iqq::from_f32<T>(acc.y);
-            out[2] = iqq::from_f32<T>(acc.z);
-            out[3] = iqq::from_f32<T>(acc.w);
-            if (A.lse != nullptr && d == 0) A.lse[at] = lse / kLog2e;
-        } else {
-            *reinterpret_cast<float4*>(A.part + (part + r) * D + d) = acc;
-            if (d == 0) A.part_lse[part + r] = lse;
-        }
+            for (int h = 0; h < 2; ++h) {
+                const int32_t r = 8 * n + 2 * t + h, row = first_row + r;
+                if (row >= rows) continue;
+                const bool none = m[n][h] == kNone && l[n][h] == 0.0f;
+                const float inv = none ? 0.0f : __fdiv_rn(1.0f, l[n][h]);
+                const float lse = none ? -INFINITY : m[n][h] + log2f(l[n][h]);
+                const int32_t token = row / A.group;
+                const int64_t at = static_cast<int64_t>(s.first + token) * A.heads + kvh * A.group + row - token * A.group;
+                if (whole) {
+                    __align__(16) T v[D / 8];
+#pragma unroll
+                    for (int d = 0; d < kM; ++d) {
+                        v[2 * d] = iqq::from_f32<T>(o[n][d][h] * inv);
+                        v[2 * d + 1] = iqq::from_f32<T>(o[n][d][2 + h] * inv);
+                    }
+                    uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(A.out) + at * D + D / 8 * g);
+#pragma unroll
+                    for (int i = 0; i < D / 64; ++i) out[i] = reinterpret_cast<const uint4*>(v)[i];
+                    if (A.lse != nullptr && g == 0) A.lse[at] = lse / kLog2e;
+                } else {
+                    float2* out = reinterpret_cast<float2*>(A.part + (part + r) * D + D / 8 * g);
+#pragma unroll
+                    for (int d = 0; d < kM; ++d) out[d] = make_float2(o[n][d][h] * inv, o[n][d][2 + h] * inv);
+                    if (g == 0) A.part_lse[part + r] = lse;
+                }
+            }
     }
-    meet();  // the parts have been read
     ++turn;
     }
 }
 
-// Joins the parts of a tile that shares c-1, c, c+1 .. cut, a CTA a row: CTA c takes it when its
-// share is the first to begin inside the tile.  Share c-1's part is its last piece (its first, if
-// it begins with the tile); the others begin inside, so it is their first.
+// Joins the parts of a tile that shares c-1, c, c+1 .. cut: CTA c takes it when its share is the
+// first to begin inside the tile.  Share c-1's part is its last piece (its first, if it begins with
+// the tile); the others begin inside, so it is their first.  Two warps a row, eight parts in
+// flight each.
 template <class T, int D, int ROWS>
-__global__ void __launch_bounds__(kThreads)
-combine_kernel(const Kv8 C, const Args A, const int ctas)
+__global__ void __launch_bounds__(ROWS * 64)
+combine_kernel(const Args A, const int ctas)
 {
-    constexpr int kE = D / 32;
-    __shared__ float s_w[kMaxCtas], s_red[kWarps], s_o[kWarps][D];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x + 1, r = blockIdx.y;
+    constexpr int kE = D / 32, kFlight = 8;
+    __shared__ float s_m[ROWS][2], s_l[ROWS][2], s_o[ROWS][D];
+    const int lane = threadIdx.x & 31, r = threadIdx.x >> 6, half = (threadIdx.x >> 5) & 1, c = blockIdx.x + 1;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Mark M = A.marks[c];
     if (M.t0 == M.t1) return;
     const int64_t prev = M.shares.start(c - 1);
     if (M.shares.start(c) <= M.t0 || prev > M.t0) return;
-    const Span s = iqq::span_of(C, M.b);
-    const int32_t row = M.row_tile * ROWS + r;
-    if (row >= s.n * A.group) return;
     // the shares c-1 .. end-1 have parts
     int end;
     {
@@ -705,52 +741,59 @@ combine_kernel(const Kv8 C, const Args A, const int ctas)
         end = hi;
     }
     const int parts = end - c + 1;
-    const auto slot = [&](int p) {
-        return ((static_cast<int64_t>(c - 1 + p) * 2 + (p == 0 && prev < M.t0)) * ROWS + r);
-    };
-    // the weights of the parts: exp2 of the log-sums, less the largest
-    float top = -INFINITY;
-    for (int p = tid; p < parts; p += kThreads) {
-        const float x = M.shares.empty(c - 1 + p) ? -INFINITY : A.part_lse[slot(p)];
-        s_w[p] = x;
-        top = fmaxf(top, x);  // (skips NaN, whose part makes everything NaN)
+    float m = -INFINITY, l = 0.0f, o[kE] = {};
+    if (r < M.rows) {
+        for (int p0 = half; p0 < parts; p0 += 2 * kFlight) {
+            float x[kFlight], v[kFlight][kE];
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                const int p = p0 + 2 * i;
+                x[i] = -INFINITY;
+                if (p < parts && !M.shares.empty(c - 1 + p)) {
+                    const int64_t at = (static_cast<int64_t>(c - 1 + p) * 2 + (p == 0 && prev < M.t0)) * ROWS + r;
+                    x[i] = A.part_lse[at];
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) v[i][e] = A.part[at * D + lane * kE + e];
+                }
+            }
+            float top = m;
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) top = fmaxf(top, x[i]);  // (skips NaN, whose part makes everything NaN)
+            const float mu = top == -INFINITY ? 0.0f : top, keep = ex2(m - mu);
+            m = top;
+            l *= keep;
+#pragma unroll
+            for (int e = 0; e < kE; ++e) o[e] *= keep;
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                if (x[i] == -INFINITY) continue;
+                const float w = ex2(x[i] - mu);
+                l += w;
+#pragma unroll
+                for (int e = 0; e < kE; ++e) o[e] = fmaf(w, v[i][e], o[e]);
+            }
+        }
     }
+    if (lane == 0) {
+        s_m[r][half] = m;
+        s_l[r][half] = l;
+    }
+    if (half == 1) {
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) s_red[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_red[w]);
-    const float mu = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f, o[kE] = {};
-#pragma unroll 8
-    for (int p = warp; p < parts; p += kWarps) {
-        const float x = s_w[p];
-        if (x == -INFINITY) continue;
-        const float w = ex2(x - mu);
-        sum += w;
-        const float* v = A.part + slot(p) * D + lane * kE;
-#pragma unroll
-        for (int e = 0; e < kE; ++e) o[e] = fmaf(w, v[e], o[e]);
+        for (int e = 0; e < kE; ++e) s_o[r][lane * kE + e] = o[e];
     }
     __syncthreads();
-    if (lane == 0) s_red[warp] = sum;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) s_o[warp][lane * kE + e] = o[e];
-    __syncthreads();
-    if (tid >= D) return;
-    float acc = 0.0f;
-    sum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        sum += s_red[w];
-        acc += s_o[w][tid];
-    }
+    if (half == 1 || r >= M.rows) return;
+    const float top = fmaxf(m, s_m[r][1]), mu = top == -INFINITY ? 0.0f : top;
+    const float f0 = ex2(m - mu), f1 = ex2(s_m[r][1] - mu), sum = fmaf(l, f0, s_l[r][1] * f1);
     const bool none = top == -INFINITY && sum == 0.0f;
-    const int32_t token = row / A.group;
-    const int64_t at = static_cast<int64_t>(s.first + token) * A.heads + M.head * A.group + row - token * A.group;
-    static_cast<T*>(A.out)[at * D + tid] = iqq::from_f32<T>(none ? 0.0f : acc / sum);
-    if (A.lse != nullptr && tid == 0) A.lse[at] = none ? -INFINITY : (top + log2f(sum)) / kLog2e;
+    const int32_t row = M.row0 + r, token = row / A.group;
+    const int64_t at = static_cast<int64_t>(M.token + token) * A.heads + M.head * A.group + row - token * A.group;
+    const float inv = none ? 0.0f : __fdiv_rn(1.0f, sum);
+    T* out = static_cast<T*>(A.out) + at * D + lane * kE;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) out[e] = iqq::from_f32<T>(none ? 0.0f : fmaf(o[e], f0, s_o[r][lane * kE + e] * f1) * inv);
+    if (A.lse != nullptr && lane == 0) A.lse[at] = none ? -INFINITY : (top + log2f(sum)) / kLog2e;
 }
 
 struct Plan {
@@ -765,11 +808,11 @@ struct Plan {
 Plan plan_of(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int64_t n_heads, int64_t n_tokens)
 {
     Plan p;
-    const int64_t group = n_heads / cache->n_kv_heads, keys = kStageBytes / (2 * cache->head_dim);
+    const int64_t group = n_heads / cache->n_kv_heads;
     const int64_t each = (n_tokens + seqs->n_seqs - 1) / seqs->n_seqs * group;
     p.row_tile = each <= 8 ? 8 : 16;
     const int64_t tiles = (n_tokens * group / p.row_tile + seqs->n_seqs) * cache->n_kv_heads;
-    const int64_t stages = std::max<int64_t>(1, (seqs->table_width * cache->page_size + keys - 1) / keys);
+    const int64_t stages = std::max<int64_t>(1, (seqs->table_width * cache->page_size + kKeys - 1) / kKeys);
     const int64_t most = std::min<int64_t>(kMaxCtas, (p.row_tile == 8 ? 3 : 2) * iqq::sm_count());
     p.ctas = tiles >= most ? most : std::min<int64_t>(most, tiles * std::min<int64_t>(stages, most));
     p.marks = (static_cast<size_t>(p.ctas) * sizeof(Mark) + 15) / 16 * 16;
@@ -805,14 +848,14 @@ iqq_status launch(const Kv8& C, const Args& A, const Plan& p, cudaStream_t st, u
     // the codes as rows of 128 bytes, read as much of a page at a time as a stage takes
     CUtensorMap maps[2];
     const int64_t rows = (static_cast<int64_t>(C.n_pages) * C.heads << C.page_log2) * D / 128;
-    const int box = std::min(Smem<D, NT>::kKeys, 1 << C.page_log2) * D / 128;
+    const int box = std::min(kKeys, 1 << C.page_log2) * D / 128;
     for (int i = 0; i < 2; ++i) {
         s = iqq::byte_map(&maps[i], C.codes[i], 128, rows, 128, box);
         if (s != IQQ_OK) return s;
     }
     s = start(decode_kernel<T, D, NT>, dim3(static_cast<unsigned>(p.ctas)), kThreads + 32, smem, st, maps[0], maps[1], C, A, flags);
     if (s != IQQ_OK || p.ctas == 1) return s;
-    return start(combine_kernel<T, D, 8 * NT>, dim3(static_cast<unsigned>(p.ctas - 1), 8 * NT), kThreads, 0, st, C, A,
+    return start(combine_kernel<T, D, 8 * NT>, dim3(static_cast<unsigned>(p.ctas - 1)), 8 * NT * 64, 0, st, A,
                  static_cast<int>(p.ctas));
 }
 
