@@ -96,7 +96,11 @@ struct Seq {
         rows = s.n * group;  // 0 for a bad span
         tiles = (rows + ROWS - 1) / ROWS;
         len = static_cast<int32_t>(s.len < C.capacity ? s.len : C.capacity);
-        stages = len <= 0 ? 1 : static_cast<int32_t>((static_cast<uint32_t>(len) + kKeys - 1) / kKeys);  // no key: one, for the zeros
+        // One more than the keys fill, the first: what a tile costs beside its keys (its rows of q,
+        // joining the warps' parts, storing) is about a stage's time, and without it CTAs whose share
+        // is many short sequences finish last (64 sequences of 50 to 8000 tokens: SMs apart by 20%).
+        // It also is the one stage of a sequence without keys, whose rows get zeros.
+        stages = 1 + static_cast<int32_t>((static_cast<uint32_t>(max(len, 0)) + kKeys - 1) / kKeys);
         all = static_cast<int64_t>(tiles) * stages * C.heads;
     }
     // Tile and stage within it of the sequence's stage `at`.
@@ -167,6 +171,8 @@ struct Smem {
 // The stages from..to-1 (of its `stages`) of one tile: a CTA's work between two stores.
 struct Piece {
     int32_t b, head, row_tile, from, to;
+    __device__ __forceinline__ int64_t first_key() const { return static_cast<int64_t>(max(from - 1, 0)) * kKeys; }
+    __device__ __forceinline__ int64_t end_key() const { return static_cast<int64_t>(to - 1) * kKeys; }
 };
 
 // A CTA's walk through its share: sequence b, `at` stages into it, `left` to go.
@@ -373,7 +379,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             const Seq<kRows> q(C, P.b, A.group);
             const int last_row = min(q.rows, (P.row_tile + 1) * kRows) - 1;
             const int64_t seen = min(static_cast<int64_t>(q.len), q.s.start + last_row / A.group + 1);
-            const int64_t j0 = static_cast<int64_t>(P.from) * kKeys, j1 = min(seen, static_cast<int64_t>(P.to) * kKeys);
+            const int64_t j0 = P.first_key(), j1 = min(seen, P.end_key());
             if (j1 > j0) ok = feed.keys(&kmap, &vmap, C, P.b, P.head, j0, j1, flags);
         }
         if (!feed.drain() || !ok) iqq::raise_flags(flags, IQQ_FLAG_WAIT_TIMEOUT);
@@ -390,7 +396,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const int64_t len = Q.len;
     const int32_t last_row = min(rows, first_row + kRows) - 1;
     const int64_t seen = min(len, s.start + last_row / A.group + 1);  // keys this tile's rows can see at all
-    const int64_t j0 = static_cast<int64_t>(P.from) * kKeys, j1 = min(seen, static_cast<int64_t>(P.to) * kKeys);
+    const int64_t j0 = P.first_key(), j1 = min(seen, P.end_key());
 
     // the rows of q this lane feeds (row g of each 8), as binary16 times 2^-e
     uint32_t bq[NT][kK][2];
@@ -714,19 +720,21 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 
 // Joins the parts of a tile that shares c-1, c, c+1 .. cut: CTA c takes it when its share is the
 // first to begin inside the tile.  Share c-1's part is its last piece (its first, if it begins with
-// the tile); the others begin inside, so it is their first.  Two warps a row, eight parts in
-// flight each.
+// the tile); the others begin inside, so it is their first.  Four warps a row, eight
+// parts in flight each, and two rows a CTA: a long sequence leaves a hundred parts of few tiles,
+// and one SM would take several microseconds to read them.
 template <class T, int D, int ROWS>
-__global__ void __launch_bounds__(ROWS * 64)
+__global__ void __launch_bounds__(256)
 combine_kernel(const Args A, const int ctas)
 {
     constexpr int kE = D / 32, kFlight = 8;
-    __shared__ float s_m[ROWS][2], s_l[ROWS][2], s_o[ROWS][D];
-    const int lane = threadIdx.x & 31, r = threadIdx.x >> 6, half = (threadIdx.x >> 5) & 1, c = blockIdx.x + 1;
+    __shared__ float s_m[2][4], s_l[2][4], s_o[2][4][D];
+    const int lane = threadIdx.x & 31, half = threadIdx.x >> 7, warp = (threadIdx.x >> 5) & 3, c = blockIdx.x + 1;
+    const int r = blockIdx.y * 2 + half;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Mark M = A.marks[c];
-    if (M.t0 == M.t1) return;
+    if (M.t0 == M.t1 || static_cast<int>(blockIdx.y) * 2 >= M.rows) return;
     const int64_t prev = M.shares.start(c - 1);
     if (M.shares.start(c) <= M.t0 || prev > M.t0) return;
     // the shares c-1 .. end-1 have parts
@@ -741,33 +749,36 @@ combine_kernel(const Args A, const int ctas)
         end = hi;
     }
     const int parts = end - c + 1;
-    float m = -INFINITY, l = 0.0f, o[kE] = {};
+    float m = kNone, l = 0.0f, o[kE] = {};
     if (r < M.rows) {
-        for (int p0 = half; p0 < parts; p0 += 2 * kFlight) {
+        for (int p0 = warp; p0 < parts; p0 += 4 * kFlight) {
             float x[kFlight], v[kFlight][kE];
 #pragma unroll
-            for (int i = 0; i < kFlight; ++i) {
-                const int p = p0 + 2 * i;
-                x[i] = -INFINITY;
-                if (p < parts && !M.shares.empty(c - 1 + p)) {
-                    const int64_t at = (static_cast<int64_t>(c - 1 + p) * 2 + (p == 0 && prev < M.t0)) * ROWS + r;
-                    x[i] = A.part_lse[at];
-#pragma unroll
-                    for (int e = 0; e < kE; ++e) v[i][e] = A.part[at * D + lane * kE + e];
+            for (int i = 0; i < kFlight; ++i) {  // (loads without a branch, so that they overlap)
+                const int p = min(p0 + 4 * i, parts - 1), from = c - 1 + p;
+                const int at = (from * 2 + (p == 0 && prev < M.t0)) * ROWS + r;
+                x[i] = A.part_lse[at];
+                if (p0 + 4 * i >= parts || M.shares.empty(from)) x[i] = -INFINITY;
+                if constexpr (D == 128) {
+                    const float4 w = *reinterpret_cast<const float4*>(A.part + static_cast<int64_t>(at) * D + lane * 4);
+                    v[i][0] = w.x; v[i][1] = w.y; v[i][2] = w.z; v[i][3] = w.w;
+                } else {
+                    const float2 w = *reinterpret_cast<const float2*>(A.part + static_cast<int64_t>(at) * D + lane * 2);
+                    v[i][0] = w.x; v[i][1] = w.y;
                 }
             }
             float top = m;
 #pragma unroll
             for (int i = 0; i < kFlight; ++i) top = fmaxf(top, x[i]);  // (skips NaN, whose part makes everything NaN)
-            const float mu = top == -INFINITY ? 0.0f : top, keep = ex2(m - mu);
+            const float keep = ex2(m - top);
             m = top;
             l *= keep;
 #pragma unroll
             for (int e = 0; e < kE; ++e) o[e] *= keep;
 #pragma unroll
             for (int i = 0; i < kFlight; ++i) {
-                if (x[i] == -INFINITY) continue;
-                const float w = ex2(x[i] - mu);
+                if (x[i] == -INFINITY) continue;  // (its values may be anything)
+                const float w = ex2(x[i] - top);
                 l += w;
 #pragma unroll
                 for (int e = 0; e < kE; ++e) o[e] = fmaf(w, v[i][e], o[e]);
@@ -775,25 +786,29 @@ combine_kernel(const Args A, const int ctas)
         }
     }
     if (lane == 0) {
-        s_m[r][half] = m;
-        s_l[r][half] = l;
+        s_m[half][warp] = m;
+        s_l[half][warp] = l;
     }
-    if (half == 1) {
 #pragma unroll
-        for (int e = 0; e < kE; ++e) s_o[r][lane * kE + e] = o[e];
-    }
+    for (int e = 0; e < kE; ++e) s_o[half][warp][lane * kE + e] = o[e];
     __syncthreads();
-    if (half == 1 || r >= M.rows) return;
-    const float top = fmaxf(m, s_m[r][1]), mu = top == -INFINITY ? 0.0f : top;
-    const float f0 = ex2(m - mu), f1 = ex2(s_m[r][1] - mu), sum = fmaf(l, f0, s_l[r][1] * f1);
-    const bool none = top == -INFINITY && sum == 0.0f;
+    const int d = threadIdx.x & 127;
+    if (d >= D || r >= M.rows) return;
+    float top = s_m[half][0];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) top = fmaxf(top, s_m[half][w]);
+    float sum = 0.0f, acc = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float f = ex2(s_m[half][w] - top);
+        sum = fmaf(s_l[half][w], f, sum);
+        acc = fmaf(s_o[half][w][d], f, acc);
+    }
+    const bool none = top == kNone && sum == 0.0f;
     const int32_t row = M.row0 + r, token = row / A.group;
     const int64_t at = static_cast<int64_t>(M.token + token) * A.heads + M.head * A.group + row - token * A.group;
-    const float inv = none ? 0.0f : __fdiv_rn(1.0f, sum);
-    T* out = static_cast<T*>(A.out) + at * D + lane * kE;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) out[e] = iqq::from_f32<T>(none ? 0.0f : fmaf(o[e], f0, s_o[r][lane * kE + e] * f1) * inv);
-    if (A.lse != nullptr && lane == 0) A.lse[at] = none ? -INFINITY : (top + log2f(sum)) / kLog2e;
+    static_cast<T*>(A.out)[at * D + d] = iqq::from_f32<T>(none ? 0.0f : __fdiv_rn(acc, sum));
+    if (A.lse != nullptr && d == 0) A.lse[at] = none ? -INFINITY : (top + log2f(sum)) / kLog2e;
 }
 
 struct Plan {
@@ -812,7 +827,7 @@ Plan plan_of(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int64_t n_hea
     const int64_t each = (n_tokens + seqs->n_seqs - 1) / seqs->n_seqs * group;
     p.row_tile = each <= 8 ? 8 : 16;
     const int64_t tiles = (n_tokens * group / p.row_tile + seqs->n_seqs) * cache->n_kv_heads;
-    const int64_t stages = std::max<int64_t>(1, (seqs->table_width * cache->page_size + kKeys - 1) / kKeys);
+    const int64_t stages = 1 + (seqs->table_width * cache->page_size + kKeys - 1) / kKeys;
     const int64_t most = std::min<int64_t>(kMaxCtas, (p.row_tile == 8 ? 3 : 2) * iqq::sm_count());
     p.ctas = tiles >= most ? most : std::min<int64_t>(most, tiles * std::min<int64_t>(stages, most));
     p.marks = (static_cast<size_t>(p.ctas) * sizeof(Mark) + 15) / 16 * 16;
@@ -855,7 +870,7 @@ iqq_status launch(const Kv8& C, const Args& A, const Plan& p, cudaStream_t st, u
     }
     s = start(decode_kernel<T, D, NT>, dim3(static_cast<unsigned>(p.ctas)), kThreads + 32, smem, st, maps[0], maps[1], C, A, flags);
     if (s != IQQ_OK || p.ctas == 1) return s;
-    return start(combine_kernel<T, D, 8 * NT>, dim3(static_cast<unsigned>(p.ctas - 1)), 8 * NT * 64, 0, st, A,
+    return start(combine_kernel<T, D, 8 * NT>, dim3(static_cast<unsigned>(p.ctas - 1), 4 * NT), 256, 0, st, A,
                  static_cast<int>(p.ctas));
 }
 
