@@ -79,6 +79,50 @@ __device__ __forceinline__ int page_at(const Kv8& C, int b, int64_t index)
     return p >= 0 && p < C.n_pages ? p : -1;
 }
 
+// What both attention kernels take: q, the outputs, and n_heads = group * key/value heads.
+struct Attend {
+    const void* q;
+    void* out;
+    float* lse;
+    int64_t q_token_stride, q_head_stride;
+    int32_t heads, group;
+    float scale;
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNone = -3.4028234663852886e38f;  // the maximum of no score: below every finite one
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t sub_h2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi)
+{
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+// A row of q becomes binary16 exactly when it is multiplied by a power of two that brings its
+// largest magnitude `top` near 2^14 (values below 2^-38 of it round, which is beyond the binary32
+// sums): the exponent of the power's reciprocal, kept where both are normal.
+__device__ __forceinline__ int row_exponent(float top)
+{
+    return max(-110, min(110, static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14));
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// Many rows a sequence (kv8_prompt.cu).
+iqq_status launch_prompt(const iqq_kv8_cache* cache, const Kv8& C, const Attend& A, int dtype, uint32_t* flags,
+                         cudaStream_t st);
+
 // Host checks shared by the entry points; fills C.
 iqq_status kv8_check(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int64_t n_tokens, Kv8& C);
 

@@ -35,23 +35,20 @@
 
 namespace {
 
+using iqq::ex2;
+using iqq::kLog2e;
+using iqq::kNone;
 using iqq::Kv8;
+using iqq::pack_h2;
 using iqq::Span;
+using iqq::sub_h2;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;       // that compute; one more warp loads
 constexpr int kKeys = 128;                  // keys of a stage: 32 a warp
 constexpr int kMaxCtas = 1024;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNone = -3.4028234663852886e38f;  // the maximum of no score: below every finite one
 
-struct Args {
-    const void* q;
-    void* out;
-    float* lse;
-    int64_t q_token_stride, q_head_stride;
-    int32_t heads, group;
-    float scale;
+struct Args : iqq::Attend {
     struct Mark* marks;  // [gridDim.x]
     float* part;         // [gridDim.x][2][row tile][head_dim], then the log-sums [..][2][row tile]
     float* part_lse;
@@ -115,29 +112,10 @@ struct Seq {
     }
 };
 
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t sub_h2(uint32_t a, uint32_t b)
-{
-    uint32_t d;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
 // Bytes 0 and 2, and bytes 1 and 3, of four codes as binary16 pairs.
 __device__ __forceinline__ uint32_t codes_even(uint32_t w) { return sub_h2((w & 0x00ff00ffu) ^ 0x64806480u, 0x64806480u); }
 __device__ __forceinline__ uint32_t codes_odd(uint32_t w) { return codes_even(w >> 8); }
 
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi)
-{
-    uint32_t d;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
 __device__ __forceinline__ uint32_t transpose8(uint32_t a)
 {
     uint32_t d;
@@ -428,11 +406,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(v[i]));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // e = exponent of top - 14, kept where 2^e and 2^-e are normal
-        int e = static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14;
-        e = max(-110, min(110, e));
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        const int e = iqq::row_exponent(top);
+        const float down = iqq::power_of_two(-e), up = iqq::power_of_two(e);
 #pragma unroll
         for (int j = 0; j < kK; ++j) {
             // dimensions D/4 t + 4 j + {0, 2} and {1, 3}: as codes_even and codes_odd
@@ -811,7 +786,11 @@ combine_kernel(const Args A, const int ctas)
     if (A.lse != nullptr && d == 0) A.lse[at] = none ? -INFINITY : (top + log2f(sum)) / kLog2e;
 }
 
+// Rows a sequence (its share of the tokens, times the group) from which the prompt kernel is taken.
+constexpr int64_t kPromptRows = 64;
+
 struct Plan {
+    bool prompt;
     int row_tile;     // rows a CTA
     int64_t ctas;     // shares
     size_t marks, part, lse;  // bytes of the workspace's parts
@@ -822,9 +801,11 @@ struct Plan {
 // leave less than a stage each.
 Plan plan_of(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int64_t n_heads, int64_t n_tokens)
 {
-    Plan p;
+    Plan p = {};
     const int64_t group = n_heads / cache->n_kv_heads;
     const int64_t each = (n_tokens + seqs->n_seqs - 1) / seqs->n_seqs * group;
+    p.prompt = each >= kPromptRows;
+    if (p.prompt) return p;
     p.row_tile = each <= 8 ? 8 : 16;
     const int64_t tiles = (n_tokens * group / p.row_tile + seqs->n_seqs) * cache->n_kv_heads;
     const int64_t stages = 1 + (seqs->table_width * cache->page_size + kKeys - 1) / kKeys;
@@ -928,6 +909,7 @@ extern "C" iqq_status iqq_kv8_attention(const iqq_kv8_cache* cache, const iqq_kv
     A.part = reinterpret_cast<float*>(ws + p.marks);
     A.part_lse = reinterpret_cast<float*>(ws + p.marks + p.part);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (p.prompt) return iqq::launch_prompt(cache, C, A, dtype, d_flags, st);
     const auto go = [&](auto zero) {
         using T = decltype(zero);
         if (cache->head_dim == 128)

@@ -1,0 +1,479 @@
+// kv8_prompt.cu -- causal attention over the paged int8 key/value cache for many rows a sequence
+// (prompts and their chunks), on sm_100a.
+//
+// out = sum_j p_j v_j / sum_j p_j, p_j = exp(s_j - m), s_j = scale * q . k_j, one pass with the
+// running maximum m.  A CTA takes 256 rows of one sequence and key/value head (row r is token
+// r / group, head r % group of the group) as two tiles of 128, over 128 keys at a time:
+//     S = Q K^T and O += P V on tcgen05 (binary16 operands, binary32 sums in tensor memory).
+// While one tile's scores go through the softmax, the other's products run.  Four warps make the
+// operands: codes become binary16 exactly (the byte b of a code c, in the low byte of 0x6400, is
+// the binary16 1152 + c after b ^= 0x80), rows of q by a power of two for each row.  Four warps a
+// tile do the softmax, a thread a row, so maximum and sum need no other thread.
+//
+// The scales stay out of the operands: with f = (the row's and the page's key scale) and the page's
+// value scale vs, the thread computes y = s f + log2(vs) for 16 keys at a time, P = 2^(y - m) with
+// m the running maximum of y, in binary16 (2^-11, as fine as the output's type or finer), and the
+// denominator as sum P / vs in binary32.  m moves only when a y passes it by 8, and only then O is
+// rescaled.  Bound by the tensor cores and, as nearly, by the exponentials (16 an SM and clock).
+#include <math.h>
+
+#include "kv8.cuh"
+#include "sm100.cuh"
+
+namespace {
+
+using iqq::Attend;
+using iqq::ex2;
+using iqq::kLog2e;
+using iqq::kNone;
+using iqq::Kv8;
+using iqq::pack_h2;
+using iqq::Span;
+using iqq::sub_h2;
+
+constexpr int kRows = 128, kTiles = 2, kKeys = 128, kStages = 2, kScales = 4;
+constexpr int kMakers = 8, kMma = 12;             // first warp that makes operands, the warp that multiplies
+constexpr int kThreads = 32 * 13;
+constexpr float kTinyScale = 7.888609052210118e-31f;  // 2^-100: a value scale below it counts as 0
+
+// Operands in rows of 64 dimensions (128 bytes), 128-byte swizzle: block b of 64 dimensions of a
+// tile is 128 rows at b * 16384.
+template <int D>
+struct Smem {
+    static constexpr int kOperand = 128 * D * 2;
+    uint8_t v[kStages][kOperand];
+    uint8_t k[kStages][kOperand];
+    uint8_t q[kTiles][kOperand];
+    // of each 16 keys: the key scale, log2 of the value scale and its reciprocal
+    float ks[kScales][kKeys / 16], lv[kScales][kKeys / 16], rv[kScales][kKeys / 16];
+    uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
+    uint64_t scaled[kScales], qfull[kTiles], sfull[kTiles], pfull[kTiles], ofull[kTiles], done;
+    uint32_t tmem;
+};
+
+// 16-byte unit u (of 8) of row r of a 64-dimension block.
+__device__ __forceinline__ uint32_t unit(int r, int u) { return static_cast<uint32_t>(r * 128 + ((u ^ (r & 7)) << 4)); }
+
+// Four codes as two binary16 pairs, in order.
+__device__ __forceinline__ uint2 codes4(uint32_t w)
+{
+    w ^= 0x80808080u;
+    return make_uint2(sub_h2(__byte_perm(w, 0x64646464u, 0x4140), 0x64806480u),
+                      sub_h2(__byte_perm(w, 0x64646464u, 0x4342), 0x64806480u));
+}
+
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// A warp's arrival, after its threads' writes to an operand.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar)
+{
+    proxy_fence();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) iqq::bar_arrive(iqq::smem_u32(bar));
+}
+
+// The work of a CTA.
+struct Work {
+    int32_t b, head, row0, rows;  // sequence, key/value head, first row, rows of the sequence
+    int64_t start, len;           // position of the sequence's first token here, its keys
+    int32_t first;                // its first packed row
+    int32_t tiles[kTiles];        // key tiles that the row tile sees
+    __device__ __forceinline__ int64_t sees(int row, int group) const { return min(len, start + row / group + 1); }
+};
+
+// ---- the warps that make K and V ----
+
+template <int D>
+struct Maker {
+    static constexpr int kChunks = D / 16, kEach = kChunks;  // 16-byte pieces of a token; a thread's pieces of a tile
+    const Kv8& C;
+    const Work& W;
+    int tid, group[kEach];
+    uint4 w[2][kEach];
+
+    __device__ __forceinline__ Maker(const Kv8& c, const Work& x, int t) : C(c), W(x), tid(t) {}
+    __device__ __forceinline__ int key(int i) const { return (i * 128 + tid) / kChunks; }
+    __device__ __forceinline__ int page(int tile, int key, int64_t end) const
+    {
+        const int64_t at = static_cast<int64_t>(tile) * kKeys + key;
+        return at < end ? iqq::page_at(C, W.b, at >> C.page_log2) : -2;
+    }
+    __device__ __forceinline__ void look(int tile, int64_t end)
+    {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) group[i] = page(tile, key(i) & ~15, end);
+    }
+    __device__ __forceinline__ void load(int which, int tile, uint4 (&v)[kEach]) const
+    {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (group[i] >= 0) {
+                const int64_t at = static_cast<int64_t>(tile) * kKeys + key(i);
+                const int64_t cell = static_cast<int64_t>(group[i]) * C.heads + W.head;
+                v[i] = __ldg(reinterpret_cast<const uint4*>(
+                    C.codes[which] + ((cell << C.page_log2) + (at & ((1 << C.page_log2) - 1))) * D + (tid % kChunks) * 16));
+            }
+        }
+    }
+    __device__ __forceinline__ void store(const uint4 (&v)[kEach], uint8_t* to) const
+    {
+        const int c = tid % kChunks, block = c >> 2, u = 2 * (c & 3), swap = block & 1;
+        to += block * 16384;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const uint2 a = codes4(v[i].x), b = codes4(v[i].y), d = codes4(v[i].z), e = codes4(v[i].w);
+            const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, e.x, e.y);
+            // the two blocks' threads write their halves in opposite order, so they meet no bank
+            *reinterpret_cast<uint4*>(to + unit(key(i), u + swap)) = swap ? hi : lo;
+            *reinterpret_cast<uint4*>(to + unit(key(i), u + 1 - swap)) = swap ? lo : hi;
+        }
+    }
+};
+
+template <int D>
+__device__ __forceinline__ bool make_operands(Smem<D>& S, const Kv8& C, const Work& W, int n, int64_t end, uint32_t* flags)
+{
+    using M = Maker<D>;
+    const int tid = threadIdx.x - 32 * kMakers;
+    M m(C, W, tid);
+    uint4 kw[M::kEach], vw[M::kEach];
+    m.look(0, end);
+    m.load(0, 0, kw);
+    float lv = 0.0f;  // log2 of the last value scale that was not 0
+    for (int j = 0; j < n; ++j) {
+        const int s = j % kStages, c = j % kScales;
+        const uint32_t ph = (j / kStages) & 1;
+        m.load(1, j, vw);
+        // the scales of this tile: 8 threads, 16 keys each
+        if (tid < kKeys / 16) {
+            const int p = m.page(j, 16 * tid, end);
+            if (p == -1) iqq::raise_flags(flags, IQQ_FLAG_BAD_INDEX);
+            const int64_t cell = static_cast<int64_t>(p) * C.heads + W.head;
+            const float ks = p < 0 ? 0.0f : __ldg(C.scales[0] + cell), vs = p < 0 ? 0.0f : __ldg(C.scales[1] + cell);
+            if (vs >= kTinyScale) lv = log2f(vs);  // (below, the codes count as 0: any scale will do in the weights)
+            const float here = vs == vs ? lv : vs;
+            S.ks[c][tid] = ks;
+            S.lv[c][tid] = p < 0 ? -INFINITY : here;  // no page: hidden
+            S.rv[c][tid] = p < 0 ? 0.0f : (vs == vs ? ex2(-here) : 1.0f);  // (0 weights of NaN pages stay 0)
+        }
+        if (tid < 32) {
+            __syncwarp();
+            if (tid == 0) iqq::bar_arrive(iqq::smem_u32(&S.scaled[c]));
+        }
+        bool late = !iqq::bar_wait(iqq::smem_u32(&S.kempty[s]), ph ^ 1u);
+        if (__any_sync(0xffffffffu, late)) return false;
+        m.store(kw, S.k[s]);
+        warp_arrive(&S.kfull[s]);
+        // codes of a page whose value scale is 0 do not count
+#pragma unroll
+        for (int i = 0; i < M::kEach; ++i)
+            if (m.group[i] >= 0 && __ldg(C.scales[1] + static_cast<int64_t>(m.group[i]) * C.heads + W.head) < kTinyScale)
+                vw[i] = make_uint4(0, 0, 0, 0);
+        if (j + 1 < n) {
+            m.look(j + 1, end);
+            m.load(0, j + 1, kw);
+        }
+        late = !iqq::bar_wait(iqq::smem_u32(&S.vempty[s]), ph ^ 1u);
+        if (__any_sync(0xffffffffu, late)) return false;
+        m.store(vw, S.v[s]);
+        warp_arrive(&S.vfull[s]);
+    }
+    return true;
+}
+
+// ---- the warp that multiplies (one thread) ----
+
+template <int D>
+__device__ __forceinline__ bool multiply(Smem<D>& S, const Work& W, uint32_t tmem)
+{
+    constexpr uint32_t kQk = iqq::idesc_f16(kRows, kKeys, false), kPv = iqq::idesc_f16(kRows, D, true);
+    const auto scores = [&](int t, int j) {
+        const uint32_t q = iqq::smem_u32(S.q[t]), k = iqq::smem_u32(S.k[j % kStages]);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            const uint32_t at = (i >> 2) * 16384 + (i & 3) * 32;
+            iqq::mma_f16(tmem + t * kKeys, iqq::desc_k128(q + at), iqq::desc_k128(k + at), kQk, i > 0);
+        }
+        iqq::tc_commit<1>(iqq::smem_u32(&S.sfull[t]));
+    };
+    const int n = max(W.tiles[0], W.tiles[1]);
+    for (int t = 0; t < kTiles; ++t) {
+        if (W.tiles[t] == 0) continue;
+        if (!iqq::bar_wait(iqq::smem_u32(&S.qfull[t]), 0)) return false;
+    }
+    for (int j = -1; j < n; ++j) {
+        for (int t = 0; t < kTiles; ++t) {
+            if (j >= 0 && j < W.tiles[t]) {
+                if (!iqq::bar_wait(iqq::smem_u32(&S.pfull[t]), j & 1)) return false;
+                if (!iqq::bar_wait(iqq::smem_u32(&S.vfull[j % kStages]), (j / kStages) & 1)) return false;
+                iqq::tc_fence_after();
+                const uint32_t v = iqq::smem_u32(S.v[j % kStages]), p = tmem + t * kKeys, o = tmem + kTiles * kKeys + t * 128;
+#pragma unroll
+                for (int i = 0; i < kKeys / 16; ++i)
+                    iqq::mma_f16_t(o, p + 8 * i, iqq::desc_n128(v + i * 2048, 16384), kPv, j > 0 || i > 0);
+                if (j + 1 == W.tiles[t]) iqq::tc_commit<1>(iqq::smem_u32(&S.ofull[t]));
+            }
+            // the next scores overwrite this tile's weights: the products run in order
+            if (j + 1 < W.tiles[t]) {
+                if (!iqq::bar_wait(iqq::smem_u32(&S.kfull[(j + 1) % kStages]), ((j + 1) / kStages) & 1)) return false;
+                iqq::tc_fence_after();
+                scores(t, j + 1);
+            }
+        }
+        if (j + 1 < n) iqq::tc_commit<1>(iqq::smem_u32(&S.kempty[(j + 1) % kStages]));
+        if (j >= 0) iqq::tc_commit<1>(iqq::smem_u32(&S.vempty[j % kStages]));
+    }
+    return true;
+}
+
+// ---- the warps of a row tile (a thread a row) ----
+
+template <class T, int D>
+__device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& W, uint32_t tmem, int t)
+{
+    const int r = threadIdx.x & 127, row = W.row0 + t * kRows + r;
+    const bool real = row < W.rows;
+    const int token = row / A.group;
+    const int64_t at = static_cast<int64_t>(W.first + token) * A.heads + W.head * A.group + row - token * A.group;
+    const int n = W.tiles[t];
+    if (n == 0) {  // nothing to see: zeros
+        if (real) {
+            uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(A.out) + at * D);
+            for (int i = 0; i < D / 8; ++i) out[i] = make_uint4(0, 0, 0, 0);
+            if (A.lse != nullptr) A.lse[at] = -INFINITY;
+        }
+        return true;
+    }
+    // the row of q, read twice: its largest value, then the operand
+    float unscale;
+    {
+        const T* q = static_cast<const T*>(A.q) + (W.first + token) * A.q_token_stride +
+                     (W.head * A.group + row - token * A.group) * A.q_head_stride;
+        float top = 0.0f, v[8];
+        for (int i = 0; i < D / 8 && real; ++i) {
+            iqq::load8(q + 8 * i, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+        }
+        const int e = iqq::row_exponent(top);
+        // the scale's sign goes with q, so that the largest score is the largest product
+        const float down = A.scale < 0.0f ? -iqq::power_of_two(-e) : iqq::power_of_two(-e);
+        unscale = iqq::power_of_two(e) * fabsf(A.scale) * kLog2e;
+        for (int i = 0; i < D / 8; ++i) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) v[x] = 0.0f;
+            if (real) iqq::load8(q + 8 * i, v);
+            *reinterpret_cast<uint4*>(S.q[t] + (i >> 3) * 16384 + unit(r, i & 7)) =
+                make_uint4(pack_h2(v[0] * down, v[1] * down), pack_h2(v[2] * down, v[3] * down),
+                           pack_h2(v[4] * down, v[5] * down), pack_h2(v[6] * down, v[7] * down));
+        }
+        warp_arrive(&S.qfull[t]);
+    }
+    // keys below `limit` are seen by this row, below `clear` by every row of the tile
+    const int64_t limit64 = real ? W.sees(row, A.group) : W.len, clear64 = W.sees(W.row0 + t * kRows, A.group);
+    const uint32_t lanes = static_cast<uint32_t>((threadIdx.x >> 5) & 3) * 32 << 16;
+    const uint32_t s_at = tmem + lanes + t * kKeys, o_at = tmem + lanes + kTiles * kKeys + t * 128;
+    float m = kNone, l = 0.0f;
+    for (int j = 0; j < n; ++j) {
+        const int c = j % kScales;
+        bool late = !iqq::bar_wait(iqq::smem_u32(&S.scaled[c]), (j / kScales) & 1);
+        late |= !iqq::bar_wait(iqq::smem_u32(&S.sfull[t]), j & 1);
+        if (__any_sync(0xffffffffu, late)) return false;
+        iqq::tc_fence_after();
+        const bool masked = clear64 < static_cast<int64_t>(j + 1) * kKeys;
+        const int limit = static_cast<int>(max(int64_t{0}, min(limit64 - static_cast<int64_t>(j) * kKeys, int64_t{kKeys})));
+        float top = kNone;
+#pragma unroll
+        for (int i = 0; i < kKeys / 32; ++i) {
+            uint32_t x[32];
+            iqq::tmem_ld32(s_at + 32 * i, x);
+            iqq::tmem_wait_ld();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float most = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float v = __uint_as_float(x[16 * h + e]);
+                    if (masked && 32 * i + 16 * h + e >= limit) v = -INFINITY;
+                    most = fmaxf(most, v);
+                }
+                // (a NaN, of a hidden run whose factor is 0 or of a page whose scale is NaN, is passed over)
+                top = fmaxf(top, fmaf(most, unscale * S.ks[c][2 * i + h], S.lv[c][2 * i + h]));
+            }
+        }
+        if (j == 0) {
+            m = top;
+        } else if (__any_sync(0xffffffffu, top > m + 8.0f)) {
+            const float next = top > m + 8.0f ? top : m, f = ex2(m - next);
+            m = next;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                uint32_t x[32];
+                iqq::tmem_ld32(o_at + 32 * i, x);
+                iqq::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                iqq::tmem_st32(o_at + 32 * i, x);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kKeys / 32; ++i) {
+            uint32_t x[32], p[16];
+            iqq::tmem_ld32(s_at + 32 * i, x);
+            iqq::tmem_wait_ld();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float f = unscale * S.ks[c][2 * i + h], b = S.lv[c][2 * i + h] - m;
+                float sum = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    float y0 = fmaf(__uint_as_float(x[16 * h + e]), f, b), y1 = fmaf(__uint_as_float(x[16 * h + e + 1]), f, b);
+                    if (masked) {
+                        if (32 * i + 16 * h + e >= limit) y0 = -INFINITY;
+                        if (32 * i + 16 * h + e + 1 >= limit) y1 = -INFINITY;
+                    }
+                    const float p0 = ex2(y0), p1 = ex2(y1);
+                    sum += p0 + p1;
+                    p[8 * h + e / 2] = pack_h2(p0, p1);
+                }
+                l = fmaf(sum, S.rv[c][2 * i + h], l);
+            }
+            iqq::tmem_st16(s_at + 16 * i, p);  // over scores that have been read
+        }
+        iqq::tmem_wait_st();
+        iqq::tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) iqq::bar_arrive(iqq::smem_u32(&S.pfull[t]));
+    }
+    const bool late = !iqq::bar_wait(iqq::smem_u32(&S.ofull[t]), 0);
+    if (__any_sync(0xffffffffu, late)) return false;
+    iqq::tc_fence_after();
+    const bool none = m == kNone && l == 0.0f;
+    const float inv = none ? 0.0f : __fdiv_rn(1.0f, l);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        uint32_t x[32];
+        iqq::tmem_ld32(o_at + 32 * i, x);
+        iqq::tmem_wait_ld();
+        if (real) {
+            __align__(16) T v[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = iqq::from_f32<T>(none ? 0.0f : __uint_as_float(x[e]) * inv);
+            uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(A.out) + at * D + 32 * i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) out[e] = reinterpret_cast<const uint4*>(v)[e];
+        }
+    }
+    if (real && A.lse != nullptr) A.lse[at] = none ? -INFINITY : (m + log2f(l)) / kLog2e;
+    return true;
+}
+
+template <class T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_kernel(const Kv8 C, const Attend A, uint32_t* __restrict__ flags)
+{
+    extern __shared__ __align__(1024) uint8_t raw[];
+    Smem<D>& S = *reinterpret_cast<Smem<D>*>(raw);
+    const int warp = threadIdx.x >> 5;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    iqq::check_spans(C, false, flags);
+
+    // later slots first: the last rows of a sequence see the most keys
+    const int64_t slot = gridDim.x - 1 - blockIdx.x;
+    Work W;
+    W.b = iqq::seq_of_slot(C, slot, A.group, kTiles * kRows, 1);
+    W.head = blockIdx.y;
+    const Span s = iqq::span_of(C, W.b);
+    const int64_t row0 = (slot - iqq::slot_base(C, W.b, A.group, kTiles * kRows, 1)) * (kTiles * kRows);
+    W.rows = s.n * A.group;  // 0 for a bad span
+    if (row0 >= W.rows) return;
+    W.row0 = static_cast<int32_t>(row0);
+    W.first = s.first;
+    W.start = s.start;
+    W.len = s.len < C.capacity ? s.len : C.capacity;
+    int64_t end = 0;  // keys that some row sees
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+        const int first = W.row0 + t * kRows, last = min(W.rows, first + kRows) - 1;
+        const int64_t sees = first < W.rows ? max(int64_t{0}, W.sees(last, A.group)) : 0;
+        W.tiles[t] = static_cast<int32_t>((sees + kKeys - 1) / kKeys);
+        end = max(end, sees);
+    }
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            iqq::bar_init(iqq::smem_u32(&S.kfull[i]), 4);
+            iqq::bar_init(iqq::smem_u32(&S.vfull[i]), 4);
+            iqq::bar_init(iqq::smem_u32(&S.kempty[i]), 1);
+            iqq::bar_init(iqq::smem_u32(&S.vempty[i]), 1);
+        }
+        for (int i = 0; i < kScales; ++i) iqq::bar_init(iqq::smem_u32(&S.scaled[i]), 1);
+        for (int i = 0; i < kTiles; ++i) {
+            iqq::bar_init(iqq::smem_u32(&S.qfull[i]), 4);
+            iqq::bar_init(iqq::smem_u32(&S.sfull[i]), 1);
+            iqq::bar_init(iqq::smem_u32(&S.pfull[i]), 4);
+            iqq::bar_init(iqq::smem_u32(&S.ofull[i]), 1);
+        }
+        iqq::bar_init(iqq::smem_u32(&S.done), 1);
+        iqq::bar_init_fence();
+    }
+    if (warp == kMma) iqq::tmem_alloc<1>(iqq::smem_u32(&S.tmem), 512);
+    iqq::tc_fence_before();
+    __syncthreads();
+    iqq::tc_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const uint32_t tmem = S.tmem;
+
+    bool ok = true;
+    if (warp < kMakers) {
+        ok = attend<T, D>(S, A, W, tmem, warp >> 2);
+    } else if (warp < kMma) {
+        ok = make_operands<D>(S, C, W, max(W.tiles[0], W.tiles[1]), end, flags);
+    } else if ((threadIdx.x & 31) == 0) {
+        ok = multiply<D>(S, W, tmem);
+        // nothing is left running when the tensor memory goes
+        iqq::tc_commit<1>(iqq::smem_u32(&S.done));
+        ok &= iqq::bar_wait(iqq::smem_u32(&S.done), 0);
+    }
+    if (!ok) iqq::raise_flags(flags, IQQ_FLAG_WAIT_TIMEOUT);
+    __syncwarp();
+    iqq::tc_fence_before();
+    __syncthreads();
+    iqq::tc_fence_after();
+    if (warp == kMma) iqq::tmem_free<1>(tmem, 512);
+}
+
+template <class T, int D>
+iqq_status launch(const Kv8& C, const Attend& A, uint32_t* flags, cudaStream_t st)
+{
+    static std::atomic<uint64_t> done{0};
+    constexpr size_t smem = 226 * 1024;  // the whole SM's: it takes the whole tensor memory
+    static_assert(sizeof(Smem<D>) <= smem, "shared memory");
+    const iqq_status s = iqq::opt_in_smem(reinterpret_cast<const void*>(prompt_kernel<T, D>), smem, done);
+    if (s != IQQ_OK) return s;
+    const int64_t slots = static_cast<int64_t>(C.n_tokens) * A.group / (kTiles * kRows) + C.n_seqs;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(slots), static_cast<unsigned>(C.heads));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, prompt_kernel<T, D>, C, A, flags);
+    return iqq::launch_status();
+}
+
+}  // namespace
+
+iqq_status iqq::launch_prompt(const iqq_kv8_cache* cache, const Kv8& C, const Attend& A, int dtype, uint32_t* flags,
+                              cudaStream_t st)
+{
+    if (dtype == IQQ_BF16)
+        return cache->head_dim == 128 ? launch<__nv_bfloat16, 128>(C, A, flags, st) : launch<__nv_bfloat16, 64>(C, A, flags, st);
+    return cache->head_dim == 128 ? launch<__half, 128>(C, A, flags, st) : launch<__half, 64>(C, A, flags, st);
+}
