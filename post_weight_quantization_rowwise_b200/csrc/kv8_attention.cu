@@ -178,15 +178,6 @@ struct Walk {
     }
 };
 
-__device__ __forceinline__ void async_load4(uint32_t dst, const void* src)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-// Arrives on the barrier when this thread's cp.async so far are done.
-__device__ __forceinline__ void async_arrive(uint32_t bar)
-{
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
 
 // The loading warp's ring, over all pieces of its share.
 template <int D, int NT>
@@ -239,11 +230,11 @@ struct Feed {
                     iqq::tma_load(to, kmap, 0, row, bar);
                     iqq::tma_load(to + Smem<D, NT>::kHalf, vmap, 0, row, bar);
                     for (int k = 0; k < piece / 16; ++k) {
-                        async_load4(iqq::smem_u32(&S.ks[s][u * (piece / 16) + k]), C.scales[0] + cell);
-                        async_load4(iqq::smem_u32(&S.vs[s][u * (piece / 16) + k]), C.scales[1] + cell);
+                        iqq::async_load4(iqq::smem_u32(&S.ks[s][u * (piece / 16) + k]), C.scales[0] + cell);
+                        iqq::async_load4(iqq::smem_u32(&S.vs[s][u * (piece / 16) + k]), C.scales[1] + cell);
                     }
                 }
-                async_arrive(bar);
+                iqq::async_arrive(bar);
                 ++issued;
                 if (++s == kStages) {
                     s = 0;

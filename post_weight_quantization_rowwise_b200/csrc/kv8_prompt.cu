@@ -32,8 +32,8 @@ using iqq::Span;
 using iqq::sub_h2;
 
 constexpr int kRows = 128, kTiles = 2, kKeys = 128, kStages = 2, kScales = 4;
-constexpr int kMakers = 8, kMma = 12;             // first warp that makes operands, the warp that multiplies
-constexpr int kThreads = 32 * 13;
+constexpr int kMakers = 8, kMma = 12, kLoader = 13;  // first warp that makes operands; the ones that multiply and load
+constexpr int kThreads = 32 * 14;
 constexpr float kTinyScale = 7.888609052210118e-31f;  // 2^-100: a value scale below it counts as 0
 
 // Operands in rows of 64 dimensions (128 bytes), 128-byte swizzle: block b of 64 dimensions of a
@@ -44,8 +44,12 @@ struct Smem {
     uint8_t v[kStages][kOperand];
     uint8_t k[kStages][kOperand];
     uint8_t q[kTiles][kOperand];
+    uint8_t raw[2][128 * D];                    // the codes of a tile of keys, and of values
+    float rawks[kKeys / 16], rawvs[kKeys / 16];  // their scales, beside the keys
+    int live[2];                                // which 16 keys have a page, a bit each
     // of each 16 keys: the key scale, log2 of the value scale and its reciprocal
     float ks[kScales][kKeys / 16], lv[kScales][kKeys / 16], rv[kScales][kKeys / 16];
+    uint64_t rfull[2], rempty[2];
     uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
     uint64_t scaled[kScales], qfull[kTiles], sfull[kTiles], pfull[kTiles], ofull[kTiles], done;
     uint32_t tmem;
@@ -81,103 +85,133 @@ struct Work {
     __device__ __forceinline__ int64_t sees(int row, int group) const { return min(len, start + row / group + 1); }
 };
 
-// ---- the warps that make K and V ----
+// ---- the warp that loads ----
 
+// Key tiles 0 .. n-1 into `raw`, keys and values in turn.  A lane takes what a tile has of one page
+// (all or page_size of its keys, whichever is less); 32 of these are looked up at a time.
 template <int D>
-struct Maker {
-    static constexpr int kChunks = D / 16, kEach = kChunks;  // 16-byte pieces of a token; a thread's pieces of a tile
-    const Kv8& C;
-    const Work& W;
-    int tid, group[kEach];
-    uint4 w[2][kEach];
-
-    __device__ __forceinline__ Maker(const Kv8& c, const Work& x, int t) : C(c), W(x), tid(t) {}
-    __device__ __forceinline__ int key(int i) const { return (i * 128 + tid) / kChunks; }
-    __device__ __forceinline__ int page(int tile, int key, int64_t end) const
-    {
-        const int64_t at = static_cast<int64_t>(tile) * kKeys + key;
-        return at < end ? iqq::page_at(C, W.b, at >> C.page_log2) : -2;
-    }
-    __device__ __forceinline__ void look(int tile, int64_t end)
-    {
+__device__ __forceinline__ bool load(Smem<D>& S, const Kv8& C, const Work& W, int n, int64_t end, uint32_t* flags)
+{
+    const int lane = threadIdx.x & 31;
+    const int piece = min(kKeys, 1 << C.page_log2), per = kKeys / piece, batch = 32 / per;
+    const auto page_of = [&](int j) {
+        const int64_t key = static_cast<int64_t>(j) * kKeys + lane * piece;
+        return key < end ? iqq::page_at(C, W.b, key >> C.page_log2) : -2;
+    };
+    bool ok = true;
+    int page = page_of(0), j = 0;
+    for (int j0 = 0; j0 < n && ok; j0 += batch) {
+        const int here = page;
+        if (j0 + batch < n) page = page_of(j0 + batch);
+        if (here == -1) iqq::raise_flags(flags, IQQ_FLAG_BAD_INDEX);
+        const uint32_t live = __ballot_sync(0xffffffffu, here >= 0);
+        for (int i = 0; i < batch && j < n && ok; ++i, ++j) {
+            const uint32_t mine = (live >> (i * per)) & ((1u << per) - 1u);
+            const int u = lane - i * per;
+            const bool my = u >= 0 && u < per && here >= 0;
+            const int64_t cell = static_cast<int64_t>(here) * C.heads + W.head;
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) group[i] = page(tile, key(i) & ~15, end);
-    }
-    __device__ __forceinline__ void load(int which, int tile, uint4 (&v)[kEach]) const
-    {
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (group[i] >= 0) {
-                const int64_t at = static_cast<int64_t>(tile) * kKeys + key(i);
-                const int64_t cell = static_cast<int64_t>(group[i]) * C.heads + W.head;
-                v[i] = __ldg(reinterpret_cast<const uint4*>(
-                    C.codes[which] + ((cell << C.page_log2) + (at & ((1 << C.page_log2) - 1))) * D + (tid % kChunks) * 16));
+            for (int which = 0; which < 2; ++which) {
+                const bool late = !iqq::bar_wait(iqq::smem_u32(&S.rempty[which]), (j & 1) ^ 1u);
+                if (__any_sync(0xffffffffu, late)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t bar = iqq::smem_u32(&S.rfull[which]);
+                if (lane == 0) {
+                    uint32_t with = 0;
+                    for (int x = 0; x < per; ++x)
+                        if (mine >> x & 1u) with |= ((1u << (piece / 16)) - 1u) << (x * (piece / 16));
+                    S.live[which] = static_cast<int>(with);
+                    iqq::bar_expect(bar, static_cast<uint32_t>(__popc(mine)) * piece * D);
+                }
+                __syncwarp();
+                if (my) {
+                    const int64_t key = static_cast<int64_t>(j) * kKeys + u * piece;
+                    iqq::bulk_load(iqq::smem_u32(S.raw[which]) + u * piece * D,
+                                   C.codes[which] + ((cell << C.page_log2) + (key & ((1 << C.page_log2) - 1))) * D, piece * D, bar);
+                    if (which == 0)
+                        for (int x = 0; x < piece / 16; ++x) {
+                            iqq::async_load4(iqq::smem_u32(&S.rawks[u * (piece / 16) + x]), C.scales[0] + cell);
+                            iqq::async_load4(iqq::smem_u32(&S.rawvs[u * (piece / 16) + x]), C.scales[1] + cell);
+                        }
+                }
+                iqq::async_arrive(bar);
             }
         }
     }
-    __device__ __forceinline__ void store(const uint4 (&v)[kEach], uint8_t* to) const
-    {
-        const int c = tid % kChunks, block = c >> 2, u = 2 * (c & 3), swap = block & 1;
-        to += block * 16384;
+    // every copy has landed (the makers waited for it) unless a wait ran out
+    for (int which = 0; which < 2; ++which)
+        if (j > 0) ok &= iqq::bar_wait(iqq::smem_u32(&S.rfull[which]), (j - 1) & 1);
+    return ok;
+}
+
+// ---- the warps that make the operands ----
+
+// This thread's pieces of a raw tile, to binary16, swizzled.
+template <int D>
+__device__ __forceinline__ void convert(const uint4 (&w)[D / 16], int tid, uint8_t* to)
+{
+    constexpr int kChunks = D / 16;
+    const int c = tid % kChunks, block = c >> 2, u = 2 * (c & 3), swap = block & 1;
+    to += block * 16384;
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const uint2 a = codes4(v[i].x), b = codes4(v[i].y), d = codes4(v[i].z), e = codes4(v[i].w);
-            const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, e.x, e.y);
-            // the two blocks' threads write their halves in opposite order, so they meet no bank
-            *reinterpret_cast<uint4*>(to + unit(key(i), u + swap)) = swap ? hi : lo;
-            *reinterpret_cast<uint4*>(to + unit(key(i), u + 1 - swap)) = swap ? lo : hi;
-        }
+    for (int i = 0; i < kChunks; ++i) {
+        const int key = (i * 128 + tid) / kChunks;
+        const uint2 a = codes4(w[i].x), b = codes4(w[i].y), d = codes4(w[i].z), e = codes4(w[i].w);
+        const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, e.x, e.y);
+        // the two blocks' threads write their halves in opposite order, so they meet no bank
+        *reinterpret_cast<uint4*>(to + unit(key, u + swap)) = swap ? hi : lo;
+        *reinterpret_cast<uint4*>(to + unit(key, u + 1 - swap)) = swap ? lo : hi;
     }
-};
+}
 
 template <int D>
-__device__ __forceinline__ bool make_operands(Smem<D>& S, const Kv8& C, const Work& W, int n, int64_t end, uint32_t* flags)
+__device__ __forceinline__ bool make_operands(Smem<D>& S, int n)
 {
-    using M = Maker<D>;
-    const int tid = threadIdx.x - 32 * kMakers;
-    M m(C, W, tid);
-    uint4 kw[M::kEach], vw[M::kEach];
-    m.look(0, end);
-    m.load(0, 0, kw);
+    constexpr int kChunks = D / 16;  // 16-byte pieces of a token, and a thread's of a tile
+    const int tid = threadIdx.x - 32 * kMakers, lane = tid & 31;
     float lv = 0.0f;  // log2 of the last value scale that was not 0
     for (int j = 0; j < n; ++j) {
         const int s = j % kStages, c = j % kScales;
         const uint32_t ph = (j / kStages) & 1;
-        m.load(1, j, vw);
-        // the scales of this tile: 8 threads, 16 keys each
-        if (tid < kKeys / 16) {
-            const int p = m.page(j, 16 * tid, end);
-            if (p == -1) iqq::raise_flags(flags, IQQ_FLAG_BAD_INDEX);
-            const int64_t cell = static_cast<int64_t>(p) * C.heads + W.head;
-            const float ks = p < 0 ? 0.0f : __ldg(C.scales[0] + cell), vs = p < 0 ? 0.0f : __ldg(C.scales[1] + cell);
-            if (vs >= kTinyScale) lv = log2f(vs);  // (below, the codes count as 0: any scale will do in the weights)
-            const float here = vs == vs ? lv : vs;
-            S.ks[c][tid] = ks;
-            S.lv[c][tid] = p < 0 ? -INFINITY : here;  // no page: hidden
-            S.rv[c][tid] = p < 0 ? 0.0f : (vs == vs ? ex2(-here) : 1.0f);  // (0 weights of NaN pages stay 0)
-        }
-        if (tid < 32) {
-            __syncwarp();
-            if (tid == 0) iqq::bar_arrive(iqq::smem_u32(&S.scaled[c]));
-        }
-        bool late = !iqq::bar_wait(iqq::smem_u32(&S.kempty[s]), ph ^ 1u);
-        if (__any_sync(0xffffffffu, late)) return false;
-        m.store(kw, S.k[s]);
-        warp_arrive(&S.kfull[s]);
-        // codes of a page whose value scale is 0 do not count
+        uint32_t zero = 0;  // the 16 keys whose value scale is 0
 #pragma unroll
-        for (int i = 0; i < M::kEach; ++i)
-            if (m.group[i] >= 0 && __ldg(C.scales[1] + static_cast<int64_t>(m.group[i]) * C.heads + W.head) < kTinyScale)
-                vw[i] = make_uint4(0, 0, 0, 0);
-        if (j + 1 < n) {
-            m.look(j + 1, end);
-            m.load(0, j + 1, kw);
+        for (int which = 0; which < 2; ++which) {
+            bool late = !iqq::bar_wait(iqq::smem_u32(&S.rfull[which]), j & 1);
+            if (__any_sync(0xffffffffu, late)) return false;
+            uint32_t live = S.live[which];
+            if (which == 0) {
+                zero = __ballot_sync(0xffffffffu, lane < kKeys / 16 && S.rawvs[lane & 7] < kTinyScale);
+                if (tid < kKeys / 16) {
+                    const bool has = live >> tid & 1;
+                    const float vs = has ? S.rawvs[tid] : 0.0f;
+                    if (vs >= kTinyScale) lv = log2f(vs);  // (below, the codes count as 0: any scale will do in the weights)
+                    const float here = vs == vs ? lv : vs;
+                    S.ks[c][tid] = has ? S.rawks[tid] : 0.0f;
+                    S.lv[c][tid] = has ? here : -INFINITY;  // no page: hidden
+                    S.rv[c][tid] = has ? (vs == vs ? ex2(-here) : 1.0f) : 0.0f;  // (0 weights of NaN pages stay 0)
+                }
+                __syncwarp();
+                if (tid == 0) iqq::bar_arrive(iqq::smem_u32(&S.scaled[c]));
+            } else {
+                live &= ~zero;
+            }
+            uint4 w[kChunks];
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) w[i] = *reinterpret_cast<const uint4*>(&S.raw[which][(i * 128 + tid) * 16]);
+            __syncwarp();
+            if (lane == 0) iqq::bar_arrive(iqq::smem_u32(&S.rempty[which]));
+            if (live != 0xffu) {
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i)
+                    if (!(live >> ((i * 128 + tid) / kChunks / 16) & 1)) w[i] = make_uint4(0, 0, 0, 0);
+            }
+            late = !iqq::bar_wait(iqq::smem_u32(which == 0 ? &S.kempty[s] : &S.vempty[s]), ph ^ 1u);
+            if (__any_sync(0xffffffffu, late)) return false;
+            convert<D>(w, tid, which == 0 ? S.k[s] : S.v[s]);
+            warp_arrive(which == 0 ? &S.kfull[s] : &S.vfull[s]);
         }
-        late = !iqq::bar_wait(iqq::smem_u32(&S.vempty[s]), ph ^ 1u);
-        if (__any_sync(0xffffffffu, late)) return false;
-        m.store(vw, S.v[s]);
-        warp_arrive(&S.vfull[s]);
     }
     return true;
 }
@@ -409,6 +443,10 @@ prompt_kernel(const Kv8 C, const Attend A, uint32_t* __restrict__ flags)
             iqq::bar_init(iqq::smem_u32(&S.kempty[i]), 1);
             iqq::bar_init(iqq::smem_u32(&S.vempty[i]), 1);
         }
+        for (int i = 0; i < 2; ++i) {
+            iqq::bar_init(iqq::smem_u32(&S.rfull[i]), 33);  // expect_tx, and the lanes' scales
+            iqq::bar_init(iqq::smem_u32(&S.rempty[i]), 4);
+        }
         for (int i = 0; i < kScales; ++i) iqq::bar_init(iqq::smem_u32(&S.scaled[i]), 1);
         for (int i = 0; i < kTiles; ++i) {
             iqq::bar_init(iqq::smem_u32(&S.qfull[i]), 4);
@@ -430,7 +468,9 @@ prompt_kernel(const Kv8 C, const Attend A, uint32_t* __restrict__ flags)
     if (warp < kMakers) {
         ok = attend<T, D>(S, A, W, tmem, warp >> 2);
     } else if (warp < kMma) {
-        ok = make_operands<D>(S, C, W, max(W.tiles[0], W.tiles[1]), end, flags);
+        ok = make_operands<D>(S, max(W.tiles[0], W.tiles[1]));
+    } else if (warp == kLoader) {
+        ok = load<D>(S, C, W, max(W.tiles[0], W.tiles[1]), end, flags);
     } else if ((threadIdx.x & 31) == 0) {
         ok = multiply<D>(S, W, tmem);
         // nothing is left running when the tensor memory goes
