@@ -263,6 +263,70 @@ __device__ __forceinline__ bool multiply(Smem<D>& S, const Work& W, uint32_t tme
 
 // ---- the warps of a row tile (a thread a row) ----
 
+// The largest y = s f + log2(vs) of this thread's row.  (A NaN, of a hidden run whose factor is 0 or
+// of a page whose scale is NaN, is passed over.)
+template <bool MASKED>
+__device__ __forceinline__ float row_top(uint32_t s_at, const float* ks, const float* lv, float unscale, int limit)
+{
+    float top = kNone;
+    uint32_t x[2][32];
+    iqq::tmem_ld32(s_at, x[0]);
+#pragma unroll
+    for (int i = 0; i < kKeys / 32; ++i) {
+        iqq::tmem_wait_ld();
+        if (i + 1 < kKeys / 32) iqq::tmem_ld32(s_at + 32 * (i + 1), x[(i + 1) & 1]);
+        float most[4];  // independent chains
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            float v = __uint_as_float(x[i & 1][e]);
+            if (MASKED && 32 * i + e >= limit) v = -INFINITY;
+            most[e >> 3] = (e & 7) == 0 ? v : fmaxf(most[e >> 3], v);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            top = fmaxf(top, fmaf(fmaxf(most[2 * h], most[2 * h + 1]), unscale * ks[2 * i + h], lv[2 * i + h]));
+    }
+    return top;
+}
+
+// P = 2^(y - m) over the scores, and the row's sum of P / vs.
+template <bool MASKED>
+__device__ __forceinline__ float row_weights(uint32_t s_at, const float* ks, const float* lv, const float* rv, float unscale,
+                                             float m, int limit)
+{
+    float l = 0.0f;
+    uint32_t x[2][32];
+    iqq::tmem_ld32(s_at, x[0]);
+#pragma unroll
+    for (int i = 0; i < kKeys / 32; ++i) {
+        iqq::tmem_wait_ld();
+        // (the weights of run i go to columns 16 i .., over scores that were read before)
+        if (i + 1 < kKeys / 32) iqq::tmem_ld32(s_at + 32 * (i + 1), x[(i + 1) & 1]);
+        uint32_t p[16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float f = unscale * ks[2 * i + h], b = lv[2 * i + h] - m;
+            float sum[2];
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+                float y0 = fmaf(__uint_as_float(x[i & 1][16 * h + e]), f, b);
+                float y1 = fmaf(__uint_as_float(x[i & 1][16 * h + e + 1]), f, b);
+                if (MASKED) {
+                    if (32 * i + 16 * h + e >= limit) y0 = -INFINITY;
+                    if (32 * i + 16 * h + e + 1 >= limit) y1 = -INFINITY;
+                }
+                const float p0 = ex2(y0), p1 = ex2(y1);
+                sum[0] = e == 0 ? p0 : sum[0] + p0;
+                sum[1] = e == 0 ? p1 : sum[1] + p1;
+                p[8 * h + e / 2] = pack_h2(p0, p1);
+            }
+            l = fmaf(sum[0] + sum[1], rv[2 * i + h], l);
+        }
+        iqq::tmem_st16(s_at + 16 * i, p);
+    }
+    return l;
+}
+
 template <class T, int D>
 __device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& W, uint32_t tmem, int t)
 {
@@ -317,25 +381,8 @@ __device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& 
         iqq::tc_fence_after();
         const bool masked = clear64 < static_cast<int64_t>(j + 1) * kKeys;
         const int limit = static_cast<int>(max(int64_t{0}, min(limit64 - static_cast<int64_t>(j) * kKeys, int64_t{kKeys})));
-        float top = kNone;
-#pragma unroll
-        for (int i = 0; i < kKeys / 32; ++i) {
-            uint32_t x[32];
-            iqq::tmem_ld32(s_at + 32 * i, x);
-            iqq::tmem_wait_ld();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float most = -INFINITY;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float v = __uint_as_float(x[16 * h + e]);
-                    if (masked && 32 * i + 16 * h + e >= limit) v = -INFINITY;
-                    most = fmaxf(most, v);
-                }
-                // (a NaN, of a hidden run whose factor is 0 or of a page whose scale is NaN, is passed over)
-                top = fmaxf(top, fmaf(most, unscale * S.ks[c][2 * i + h], S.lv[c][2 * i + h]));
-            }
-        }
+        const float top = masked ? row_top<true>(s_at, S.ks[c], S.lv[c], unscale, limit)
+                                 : row_top<false>(s_at, S.ks[c], S.lv[c], unscale, limit);
         if (j == 0) {
             m = top;
         } else if (__any_sync(0xffffffffu, top > m + 8.0f)) {
@@ -352,30 +399,8 @@ __device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& 
                 iqq::tmem_st32(o_at + 32 * i, x);
             }
         }
-#pragma unroll
-        for (int i = 0; i < kKeys / 32; ++i) {
-            uint32_t x[32], p[16];
-            iqq::tmem_ld32(s_at + 32 * i, x);
-            iqq::tmem_wait_ld();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float f = unscale * S.ks[c][2 * i + h], b = S.lv[c][2 * i + h] - m;
-                float sum = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    float y0 = fmaf(__uint_as_float(x[16 * h + e]), f, b), y1 = fmaf(__uint_as_float(x[16 * h + e + 1]), f, b);
-                    if (masked) {
-                        if (32 * i + 16 * h + e >= limit) y0 = -INFINITY;
-                        if (32 * i + 16 * h + e + 1 >= limit) y1 = -INFINITY;
-                    }
-                    const float p0 = ex2(y0), p1 = ex2(y1);
-                    sum += p0 + p1;
-                    p[8 * h + e / 2] = pack_h2(p0, p1);
-                }
-                l = fmaf(sum, S.rv[c][2 * i + h], l);
-            }
-            iqq::tmem_st16(s_at + 16 * i, p);  // over scores that have been read
-        }
+        l += masked ? row_weights<true>(s_at, S.ks[c], S.lv[c], S.rv[c], unscale, m, limit)
+                    : row_weights<false>(s_at, S.ks[c], S.lv[c], S.rv[c], unscale, m, limit);
         iqq::tmem_wait_st();
         iqq::tc_fence_before();
         __syncwarp();
