@@ -33,7 +33,11 @@ using iqq::sub_h2;
 
 constexpr int kRows = 128, kTiles = 2, kKeys = 128, kStages = 2, kScales = 4;
 constexpr int kMakers = 8, kMma = 12, kLoader = 13;  // first warp that makes operands; the ones that multiply and load
-constexpr int kThreads = 32 * 14;
+constexpr int kThreads = 32 * 16;
+// Registers a thread of the softmax, the makers and the rest (the launch's are shared out anew).
+constexpr int kSoftmaxRegs = 168, kMakerRegs = 96, kOtherRegs = 64;
+constexpr int kRegs = 128 * (2 * kSoftmaxRegs + kMakerRegs + kOtherRegs);
+
 constexpr float kTinyScale = 7.888609052210118e-31f;  // 2^-100: a value scale below it counts as 0
 
 // Operands in rows of 64 dimensions (128 bytes), 128-byte swizzle: block b of 64 dimensions of a
@@ -64,6 +68,17 @@ __device__ __forceinline__ uint2 codes4(uint32_t w)
     w ^= 0x80808080u;
     return make_uint2(sub_h2(__byte_perm(w, 0x64646464u, 0x4140), 0x64806480u),
                       sub_h2(__byte_perm(w, 0x64646464u, 0x4342), 0x64806480u));
+}
+
+template <int N>
+__device__ __forceinline__ void more_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -289,20 +304,19 @@ __device__ __forceinline__ float row_top(uint32_t s_at, const float* ks, const f
     return top;
 }
 
-// P = 2^(y - m) over the scores, and the row's sum of P / vs.
+// P = 2^(y - m), as binary16 pairs; returns the row's sum of P / vs and sets `over` to the largest
+// y - m.
 template <bool MASKED>
 __device__ __forceinline__ float row_weights(uint32_t s_at, const float* ks, const float* lv, const float* rv, float unscale,
-                                             float m, int limit)
+                                             float m, int limit, uint32_t (&p)[kKeys / 32][16], float& over)
 {
-    float l = 0.0f;
+    float l = 0.0f, most[4] = {kNone, kNone, kNone, kNone};
     uint32_t x[2][32];
     iqq::tmem_ld32(s_at, x[0]);
 #pragma unroll
     for (int i = 0; i < kKeys / 32; ++i) {
         iqq::tmem_wait_ld();
-        // (the weights of run i go to columns 16 i .., over scores that were read before)
         if (i + 1 < kKeys / 32) iqq::tmem_ld32(s_at + 32 * (i + 1), x[(i + 1) & 1]);
-        uint32_t p[16];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const float f = unscale * ks[2 * i + h], b = lv[2 * i + h] - m;
@@ -315,15 +329,16 @@ __device__ __forceinline__ float row_weights(uint32_t s_at, const float* ks, con
                     if (32 * i + 16 * h + e >= limit) y0 = -INFINITY;
                     if (32 * i + 16 * h + e + 1 >= limit) y1 = -INFINITY;
                 }
+                most[e / 2 & 3] = fmaxf(most[e / 2 & 3], fmaxf(y0, y1));
                 const float p0 = ex2(y0), p1 = ex2(y1);
                 sum[0] = e == 0 ? p0 : sum[0] + p0;
                 sum[1] = e == 0 ? p1 : sum[1] + p1;
-                p[8 * h + e / 2] = pack_h2(p0, p1);
+                p[i][8 * h + e / 2] = pack_h2(p0, p1);
             }
             l = fmaf(sum[0] + sum[1], rv[2 * i + h], l);
         }
-        iqq::tmem_st16(s_at + 16 * i, p);
     }
+    over = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
     return l;
 }
 
@@ -381,26 +396,43 @@ __device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& 
         iqq::tc_fence_after();
         const bool masked = clear64 < static_cast<int64_t>(j + 1) * kKeys;
         const int limit = static_cast<int>(max(int64_t{0}, min(limit64 - static_cast<int64_t>(j) * kKeys, int64_t{kKeys})));
-        const float top = masked ? row_top<true>(s_at, S.ks[c], S.lv[c], unscale, limit)
-                                 : row_top<false>(s_at, S.ks[c], S.lv[c], unscale, limit);
-        if (j == 0) {
-            m = top;
-        } else if (__any_sync(0xffffffffu, top > m + 8.0f)) {
-            const float next = top > m + 8.0f ? top : m, f = ex2(m - next);
+        // One pass with the maximum as it is; a second, rare after the first tiles, where a y passed it
+        // by 8.  (A row that has seen nothing yet has no maximum to start from.)
+        uint32_t p[kKeys / 32][16];
+        const float *ks = S.ks[c], *lv = S.lv[c], *rv = S.rv[c];
+        const auto weigh = [&](float& over) {
+            return masked ? row_weights<true>(s_at, ks, lv, rv, unscale, m, limit, p, over)
+                          : row_weights<false>(s_at, ks, lv, rv, unscale, m, limit, p, over);
+        };
+        float over = 0.0f, sum = 0.0f, next = m;
+        const bool fresh = __any_sync(0xffffffffu, m == kNone);
+        if (fresh) {
+            const float top = masked ? row_top<true>(s_at, ks, lv, unscale, limit) : row_top<false>(s_at, ks, lv, unscale, limit);
+            if (m == kNone || top > m + 8.0f) next = top;
+        } else {
+            sum = weigh(over);
+            if (over > 8.0f) next = m + over;
+        }
+        if (fresh || __any_sync(0xffffffffu, over > 8.0f)) {
+            const float f = ex2(m - next);
             m = next;
             l *= f;
+            if (j > 0) {
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                uint32_t x[32];
-                iqq::tmem_ld32(o_at + 32 * i, x);
-                iqq::tmem_wait_ld();
+                for (int i = 0; i < D / 32; ++i) {
+                    uint32_t x[32];
+                    iqq::tmem_ld32(o_at + 32 * i, x);
+                    iqq::tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-                iqq::tmem_st32(o_at + 32 * i, x);
+                    for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                    iqq::tmem_st32(o_at + 32 * i, x);
+                }
             }
+            sum = weigh(over);
         }
-        l += masked ? row_weights<true>(s_at, S.ks[c], S.lv[c], S.rv[c], unscale, m, limit)
-                    : row_weights<false>(s_at, S.ks[c], S.lv[c], S.rv[c], unscale, m, limit);
+        l += sum;
+#pragma unroll
+        for (int i = 0; i < kKeys / 32; ++i) iqq::tmem_st16(s_at + 16 * i, p[i]);
         iqq::tmem_wait_st();
         iqq::tc_fence_before();
         __syncwarp();
@@ -491,16 +523,21 @@ prompt_kernel(const Kv8 C, const Attend A, uint32_t* __restrict__ flags)
 
     bool ok = true;
     if (warp < kMakers) {
+        more_registers<kSoftmaxRegs>();
         ok = attend<T, D>(S, A, W, tmem, warp >> 2);
     } else if (warp < kMma) {
+        fewer_registers<kMakerRegs>();
         ok = make_operands<D>(S, max(W.tiles[0], W.tiles[1]));
-    } else if (warp == kLoader) {
-        ok = load<D>(S, C, W, max(W.tiles[0], W.tiles[1]), end, flags);
-    } else if ((threadIdx.x & 31) == 0) {
-        ok = multiply<D>(S, W, tmem);
-        // nothing is left running when the tensor memory goes
-        iqq::tc_commit<1>(iqq::smem_u32(&S.done));
-        ok &= iqq::bar_wait(iqq::smem_u32(&S.done), 0);
+    } else {
+        fewer_registers<kOtherRegs>();
+        if (warp == kLoader) {
+            ok = load<D>(S, C, W, max(W.tiles[0], W.tiles[1]), end, flags);
+        } else if (threadIdx.x == 32 * kMma) {
+            ok = multiply<D>(S, W, tmem);
+            // nothing is left running when the tensor memory goes
+            iqq::tc_commit<1>(iqq::smem_u32(&S.done));
+            ok &= iqq::bar_wait(iqq::smem_u32(&S.done), 0);
+        }
     }
     if (!ok) iqq::raise_flags(flags, IQQ_FLAG_WAIT_TIMEOUT);
     __syncwarp();
@@ -518,6 +555,15 @@ iqq_status launch(const Kv8& C, const Attend& A, uint32_t* flags, cudaStream_t s
     static_assert(sizeof(Smem<D>) <= smem, "shared memory");
     const iqq_status s = iqq::opt_in_smem(reinterpret_cast<const void*>(prompt_kernel<T, D>), smem, done);
     if (s != IQQ_OK) return s;
+    // The warps' shares have to fit what the launch gives, or they would wait for registers for good.
+    static const int regs = [] {
+        cudaFuncAttributes at = {};
+        return cudaFuncGetAttributes(&at, prompt_kernel<T, D>) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if (regs * kThreads < kRegs) {
+        iqq::set_last_cuda_error(cudaErrorLaunchOutOfResources);
+        return IQQ_ERR_CUDA;
+    }
     const int64_t slots = static_cast<int64_t>(C.n_tokens) * A.group / (kTiles * kRows) + C.n_seqs;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(slots), static_cast<unsigned>(C.heads));
