@@ -174,7 +174,7 @@ pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CU
             for (int c = 0; c < cols; c += 16) {
                 uint32_t v[16];
                 iqq::tmem_ld16(at + c, v);
-                iqq::tmem_wait_ld();
+                iqq::tmem_wait_ld(v);
                 put16<T>(P, v, t0 + c, r, dw, bias);
             }
             iqq::tc_fence_before();
@@ -294,7 +294,7 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
             for (int c = 0; c < cols; c += 16) {
                 uint32_t v[16];
                 iqq::tmem_ld16(lanes + c, v);
-                iqq::tmem_wait_ld();
+                iqq::tmem_wait_ld(v);
                 put16<T>(P, v, t0 + c, r, dw, bias);
             }
         }
@@ -307,7 +307,7 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
             for (int c = 0; c < cols; c += 16) {
                 uint32_t v[16];
                 iqq::tmem_ld16(lanes + c, v);
-                iqq::tmem_wait_ld();
+                iqq::tmem_wait_ld(v);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     if (c + i >= cols) break;

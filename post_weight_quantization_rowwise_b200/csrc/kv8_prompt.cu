@@ -35,7 +35,7 @@ constexpr int kRows = 128, kTiles = 2, kKeys = 128, kStages = 2, kScales = 4;
 constexpr int kMakers = 8, kMma = 12, kLoader = 13;  // first warp that makes operands; the ones that multiply and load
 constexpr int kThreads = 32 * 16;
 // Registers a thread of the softmax, the makers and the rest (the launch's are shared out anew).
-constexpr int kSoftmaxRegs = 168, kMakerRegs = 96, kOtherRegs = 64;
+constexpr int kSoftmaxRegs = 184, kMakerRegs = 88, kOtherRegs = 40;
 constexpr int kRegs = 128 * (2 * kSoftmaxRegs + kMakerRegs + kOtherRegs);
 
 constexpr float kTinyScale = 7.888609052210118e-31f;  // 2^-100: a value scale below it counts as 0
@@ -288,7 +288,7 @@ __device__ __forceinline__ float row_top(uint32_t s_at, const float* ks, const f
     iqq::tmem_ld32(s_at, x[0]);
 #pragma unroll
     for (int i = 0; i < kKeys / 32; ++i) {
-        iqq::tmem_wait_ld();
+        iqq::tmem_wait_ld(x[i & 1]);
         if (i + 1 < kKeys / 32) iqq::tmem_ld32(s_at + 32 * (i + 1), x[(i + 1) & 1]);
         float most[4];  // independent chains
 #pragma unroll
@@ -304,41 +304,46 @@ __device__ __forceinline__ float row_top(uint32_t s_at, const float* ks, const f
     return top;
 }
 
-// P = 2^(y - m), as binary16 pairs; returns the row's sum of P / vs and sets `over` to the largest
-// y - m.
+// P = 2^(y - m), as binary16 pairs; returns the row's sum of P / vs.  `over`: whether a weight is
+// above 2^8.
 template <bool MASKED>
 __device__ __forceinline__ float row_weights(uint32_t s_at, const float* ks, const float* lv, const float* rv, float unscale,
-                                             float m, int limit, uint32_t (&p)[kKeys / 32][16], float& over)
+                                             float m, int limit, uint32_t (&p)[kKeys / 32][16], bool& over)
 {
-    float l = 0.0f, most[4] = {kNone, kNone, kNone, kNone};
-    uint32_t x[2][32];
+    float l = 0.0f;
+    uint32_t x[2][32], most[2] = {0u, 0u};
     iqq::tmem_ld32(s_at, x[0]);
 #pragma unroll
     for (int i = 0; i < kKeys / 32; ++i) {
-        iqq::tmem_wait_ld();
+        iqq::tmem_wait_ld(x[i & 1]);
         if (i + 1 < kKeys / 32) iqq::tmem_ld32(s_at + 32 * (i + 1), x[(i + 1) & 1]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const float f = unscale * ks[2 * i + h], b = lv[2 * i + h] - m;
-            float sum[2];
+            const uint64_t f2 = iqq::pack_f2(f, f), b2 = iqq::pack_f2(b, b);
+            uint64_t sum[2];
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
-                float y0 = fmaf(__uint_as_float(x[i & 1][16 * h + e]), f, b);
-                float y1 = fmaf(__uint_as_float(x[i & 1][16 * h + e + 1]), f, b);
+                float y0, y1;
+                iqq::unpack_f2(iqq::fma_f2(iqq::pack_f2(__uint_as_float(x[i & 1][16 * h + e]), __uint_as_float(x[i & 1][16 * h + e + 1])),
+                                           f2, b2), y0, y1);
                 if (MASKED) {
                     if (32 * i + 16 * h + e >= limit) y0 = -INFINITY;
                     if (32 * i + 16 * h + e + 1 >= limit) y1 = -INFINITY;
                 }
-                most[e / 2 & 3] = fmaxf(most[e / 2 & 3], fmaxf(y0, y1));
                 const float p0 = ex2(y0), p1 = ex2(y1);
-                sum[0] = e == 0 ? p0 : sum[0] + p0;
-                sum[1] = e == 0 ? p1 : sum[1] + p1;
+                const uint64_t p2 = iqq::pack_f2(p0, p1);
+                sum[e / 2 & 1] = e < 4 ? p2 : iqq::add_f2(sum[e / 2 & 1], p2);
                 p[i][8 * h + e / 2] = pack_h2(p0, p1);
+                most[e / 2 & 1] = iqq::max_h2(most[e / 2 & 1], p[i][8 * h + e / 2]);
             }
-            l = fmaf(sum[0] + sum[1], rv[2 * i + h], l);
+            float s0, s1;
+            iqq::unpack_f2(iqq::add_f2(sum[0], sum[1]), s0, s1);
+            l = fmaf(s0 + s1, rv[2 * i + h], l);
         }
     }
-    over = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+    const uint32_t top = iqq::max_h2(most[0], most[1]);
+    over = max(top & 0xffffu, top >> 16) > 0x5c00u;  // 2^8 (the weights are not negative; a NaN was passed over)
     return l;
 }
 
@@ -396,39 +401,34 @@ __device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& 
         iqq::tc_fence_after();
         const bool masked = clear64 < static_cast<int64_t>(j + 1) * kKeys;
         const int limit = static_cast<int>(max(int64_t{0}, min(limit64 - static_cast<int64_t>(j) * kKeys, int64_t{kKeys})));
-        // One pass with the maximum as it is; a second, rare after the first tiles, where a y passed it
-        // by 8.  (A row that has seen nothing yet has no maximum to start from.)
+        // One pass with the maximum as it is; where a weight came out above 2^8 (rare after the first
+        // tiles), or a row has seen nothing yet, the maximum is taken and the weights anew.
         uint32_t p[kKeys / 32][16];
         const float *ks = S.ks[c], *lv = S.lv[c], *rv = S.rv[c];
-        const auto weigh = [&](float& over) {
-            return masked ? row_weights<true>(s_at, ks, lv, rv, unscale, m, limit, p, over)
-                          : row_weights<false>(s_at, ks, lv, rv, unscale, m, limit, p, over);
-        };
-        float over = 0.0f, sum = 0.0f, next = m;
-        const bool fresh = __any_sync(0xffffffffu, m == kNone);
-        if (fresh) {
-            const float top = masked ? row_top<true>(s_at, ks, lv, unscale, limit) : row_top<false>(s_at, ks, lv, unscale, limit);
-            if (m == kNone || top > m + 8.0f) next = top;
-        } else {
-            sum = weigh(over);
-            if (over > 8.0f) next = m + over;
-        }
-        if (fresh || __any_sync(0xffffffffu, over > 8.0f)) {
-            const float f = ex2(m - next);
-            m = next;
-            l *= f;
-            if (j > 0) {
+        bool over = m == kNone;
+        float sum = 0.0f;
+        for (int turn = __any_sync(0xffffffffu, over) ? 1 : 0; turn < 3; ++turn) {
+            if (turn == 1) {
+                if (!__any_sync(0xffffffffu, over)) break;
+                const float top = masked ? row_top<true>(s_at, ks, lv, unscale, limit) : row_top<false>(s_at, ks, lv, unscale, limit);
+                const float next = over ? fmaxf(m, top) : m, f = ex2(m - next);
+                m = next;
+                l *= f;
+                if (j > 0) {
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    uint32_t x[32];
-                    iqq::tmem_ld32(o_at + 32 * i, x);
-                    iqq::tmem_wait_ld();
+                    for (int i = 0; i < D / 32; ++i) {
+                        uint32_t x[32];
+                        iqq::tmem_ld32(o_at + 32 * i, x);
+                        iqq::tmem_wait_ld(x);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-                    iqq::tmem_st32(o_at + 32 * i, x);
+                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                        iqq::tmem_st32(o_at + 32 * i, x);
+                    }
                 }
+            } else {
+                sum = masked ? row_weights<true>(s_at, ks, lv, rv, unscale, m, limit, p, over)
+                             : row_weights<false>(s_at, ks, lv, rv, unscale, m, limit, p, over);
             }
-            sum = weigh(over);
         }
         l += sum;
 #pragma unroll
@@ -447,7 +447,7 @@ __device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& 
     for (int i = 0; i < D / 32; ++i) {
         uint32_t x[32];
         iqq::tmem_ld32(o_at + 32 * i, x);
-        iqq::tmem_wait_ld();
+        iqq::tmem_wait_ld(x);
         if (real) {
             __align__(16) T v[32];
 #pragma unroll
