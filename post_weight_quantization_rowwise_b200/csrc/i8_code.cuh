@@ -53,16 +53,9 @@ template <> __device__ __forceinline__ float from_f32<float>(float v) { return v
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-// Eight values from a 16-byte boundary, widened to binary32 (exact).
-__device__ __forceinline__ void load8(const float* p, float (&v)[8])
+// Eight 16-bit values in four words, widened to binary32 (exact).
+__device__ __forceinline__ void widen8(const __nv_bfloat16*, uint4 a, float (&v)[8])
 {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8])
-{
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -70,15 +63,26 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8])
         v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
 }
-__device__ __forceinline__ void load8(const __half* p, float (&v)[8])
+__device__ __forceinline__ void widen8(const __half*, uint4 a, float (&v)[8])
 {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         v[2 * i] = __half2float(__ushort_as_half(static_cast<unsigned short>(w[i] & 0xffffu)));
         v[2 * i + 1] = __half2float(__ushort_as_half(static_cast<unsigned short>(w[i] >> 16)));
     }
+}
+// Eight values from a 16-byte boundary.
+__device__ __forceinline__ void load8(const float* p, float (&v)[8])
+{
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+template <class T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8])
+{
+    widen8(p, __ldg(reinterpret_cast<const uint4*>(p)), v);
 }
 
 inline int64_t dtype_bytes(int dtype) { return dtype == IQQ_F32 ? 4 : 2; }

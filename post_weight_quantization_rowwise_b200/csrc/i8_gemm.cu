@@ -113,7 +113,7 @@ pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CU
             const int m0 = static_cast<int>(i / P.t_tiles) * 2 * kRows + static_cast<int>(rank) * kRows;
             const int t0 = static_cast<int>(i % P.t_tiles) * P.tn + static_cast<int>(rank) * half;
             for (int kb = 0; kb < P.kblocks; ++kb) {
-                if (!iqq::bar_wait(iqq::smem_u32(&S.empty[s]), ph ^ 1u)) {
+                if (!iqq::bar_wait_long<true>(iqq::smem_u32(&S.empty[s]), ph ^ 1u)) {
                     late = true;
                     break;
                 }
@@ -131,17 +131,17 @@ pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CU
         // every copy has landed (the products waited for them) unless a wait ran out
         if (rank == 0)
             for (int64_t i = issued > P.stages ? issued - P.stages : 0; i < issued; ++i)
-                late |= !iqq::bar_wait(iqq::smem_u32(&S.full[i % P.stages]), static_cast<uint32_t>(i / P.stages) & 1u);
+                late |= !iqq::bar_wait_long<true>(iqq::smem_u32(&S.full[i % P.stages]), static_cast<uint32_t>(i / P.stages) & 1u);
     } else if (warp == 1 && lane == 0 && rank == 0) {
         const uint32_t idesc = iqq::idesc_i8(2 * kRows, P.tn);
         int s = 0, turn = 0;
         uint32_t ph = 0;
         for (int64_t i = pair; i < tiles && !late; i += pairs, ++turn) {
             const int buf = turn & 1;
-            late = !iqq::bar_wait(iqq::smem_u32(&S.taken[buf]), (static_cast<uint32_t>(turn >> 1) & 1u) ^ 1u);
+            late = !iqq::bar_wait_long<true>(iqq::smem_u32(&S.taken[buf]), (static_cast<uint32_t>(turn >> 1) & 1u) ^ 1u);
             iqq::tc_fence_after();
             for (int kb = 0; kb < P.kblocks && !late; ++kb) {
-                if (!iqq::bar_wait(iqq::smem_u32(&S.full[s]), ph)) {
+                if (!iqq::bar_wait_long<true>(iqq::smem_u32(&S.full[s]), ph)) {
                     late = true;
                     break;
                 }
@@ -166,7 +166,7 @@ pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CU
             const int buf = turn & 1;
             const int64_t r = (i / P.t_tiles) * 2 * kRows + rank * kRows + quad * 32 + lane, t0 = (i % P.t_tiles) * P.tn;
             const float dw = r < P.n_out ? __ldg(P.ws + r) : 0.0f, bias = bias_of(P, r);
-            late = !iqq::bar_wait(iqq::smem_u32(&S.done[buf]), static_cast<uint32_t>(turn >> 1) & 1u);
+            late = !iqq::bar_wait_long<true>(iqq::smem_u32(&S.done[buf]), static_cast<uint32_t>(turn >> 1) & 1u);
             if (__any_sync(0xffffffffu, late)) break;
             iqq::tc_fence_after();
             const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * 256;
@@ -235,7 +235,7 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
             uint32_t ph = 0;
             int issued = 0;
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!iqq::bar_wait(iqq::smem_u32(&S.empty[s]), ph ^ 1u)) {
+                if (!iqq::bar_wait_long(iqq::smem_u32(&S.empty[s]), ph ^ 1u)) {
                     late = true;
                     break;
                 }
@@ -251,7 +251,7 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
             }
             // every copy has landed (the products waited for them) unless a wait ran out
             for (int i = issued > P.stages ? issued - P.stages : 0; i < issued; ++i)
-                late |= !iqq::bar_wait(iqq::smem_u32(&S.full[i % P.stages]), static_cast<uint32_t>(i / P.stages) & 1u);
+                late |= !iqq::bar_wait_long(iqq::smem_u32(&S.full[i % P.stages]), static_cast<uint32_t>(i / P.stages) & 1u);
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -259,7 +259,7 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
             int s = 0;
             uint32_t ph = 0;
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!iqq::bar_wait(iqq::smem_u32(&S.full[s]), ph)) {
+                if (!iqq::bar_wait_long(iqq::smem_u32(&S.full[s]), ph)) {
                     late = true;
                     break;
                 }
@@ -280,7 +280,7 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
     }
     __syncwarp();
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    late |= !iqq::bar_wait(iqq::smem_u32(&S.done[0]), 0);
+    late |= !iqq::bar_wait_long(iqq::smem_u32(&S.done[0]), 0);
     __syncwarp();
     iqq::tc_fence_after();
 

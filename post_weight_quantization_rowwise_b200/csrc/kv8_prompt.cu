@@ -363,14 +363,18 @@ __device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& 
         }
         return true;
     }
-    // the row of q, read twice: its largest value, then the operand
+    // the row of q: all of it in flight at once, then its largest value, then the operand
     float unscale;
     {
         const T* q = static_cast<const T*>(A.q) + (W.first + token) * A.q_token_stride +
                      (W.head * A.group + row - token * A.group) * A.q_head_stride;
+        uint4 raw[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) raw[i] = real ? __ldg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0, 0, 0, 0);
         float top = 0.0f, v[8];
-        for (int i = 0; i < D / 8 && real; ++i) {
-            iqq::load8(q + 8 * i, v);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            iqq::widen8(q, raw[i], v);
 #pragma unroll
             for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
         }
@@ -378,10 +382,9 @@ __device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& 
         // the scale's sign goes with q, so that the largest score is the largest product
         const float down = A.scale < 0.0f ? -iqq::power_of_two(-e) : iqq::power_of_two(-e);
         unscale = iqq::power_of_two(e) * fabsf(A.scale) * kLog2e;
-        for (int i = 0; i < D / 8; ++i) {
 #pragma unroll
-            for (int x = 0; x < 8; ++x) v[x] = 0.0f;
-            if (real) iqq::load8(q + 8 * i, v);
+        for (int i = 0; i < D / 8; ++i) {
+            iqq::widen8(q, raw[i], v);
             *reinterpret_cast<uint4*>(S.q[t] + (i >> 3) * 16384 + unit(r, i & 7)) =
                 make_uint4(pack_h2(v[0] * down, v[1] * down), pack_h2(v[2] * down, v[3] * down),
                            pack_h2(v[4] * down, v[5] * down), pack_h2(v[6] * down, v[7] * down));
@@ -471,11 +474,11 @@ prompt_kernel(const Kv8 C, const Attend A, uint32_t* __restrict__ flags)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     iqq::check_spans(C, false, flags);
 
-    // later slots first: the last rows of a sequence see the most keys
-    const int64_t slot = gridDim.x - 1 - blockIdx.x;
+    // later slots first, in all heads: the last rows of a sequence see the most keys
+    const int64_t slot = (gridDim.x - 1 - blockIdx.x) / static_cast<uint32_t>(C.heads);
     Work W;
     W.b = iqq::seq_of_slot(C, slot, A.group, kTiles * kRows, 1);
-    W.head = blockIdx.y;
+    W.head = static_cast<int32_t>(blockIdx.x % static_cast<uint32_t>(C.heads));
     const Span s = iqq::span_of(C, W.b);
     const int64_t row0 = (slot - iqq::slot_base(C, W.b, A.group, kTiles * kRows, 1)) * (kTiles * kRows);
     W.rows = s.n * A.group;  // 0 for a bad span
@@ -566,7 +569,8 @@ iqq_status launch(const Kv8& C, const Attend& A, uint32_t* flags, cudaStream_t s
     }
     const int64_t slots = static_cast<int64_t>(C.n_tokens) * A.group / (kTiles * kRows) + C.n_seqs;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(slots), static_cast<unsigned>(C.heads));
+    if (slots * C.heads > 0x7fffffffLL) return IQQ_ERR_SHAPE;
+    cfg.gridDim = dim3(static_cast<unsigned>(slots * C.heads));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;

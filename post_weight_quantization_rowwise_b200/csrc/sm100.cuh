@@ -37,24 +37,69 @@ __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// CLUSTER: another CTA's arrivals count, and what it wrote before them is to be seen.
+template <bool CLUSTER>
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(100000u)
-        : "memory");
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    return ok != 0u;
+}
+// The same, asleep for up to 0.1 ms at a time: wakes a little later, and leaves the SM to the others.
+// (The products gain 3 to 15% by it, whose waits are long; the prompt kernel's softmax loses 10%.)
+template <bool CLUSTER>
+__device__ __forceinline__ bool bar_try_long(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(100000u)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(100000u)
+            : "memory");
     return ok != 0u;
 }
 // Waits for the phase of this parity, at most about 2 s; false when it did not complete.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity)
 {
-    if (bar_try(bar, parity)) return true;
+    if (bar_try<CLUSTER>(bar, parity)) return true;
     const long long t0 = clock64();
-    while (!bar_try(bar, parity))
+    while (!bar_try<CLUSTER>(bar, parity))
+        if (clock64() - t0 > kWaitClocks) return false;
+    return true;
+}
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool bar_wait_long(uint32_t bar, uint32_t parity)
+{
+    if (bar_try_long<CLUSTER>(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!bar_try_long<CLUSTER>(bar, parity))
         if (clock64() - t0 > kWaitClocks) return false;
     return true;
 }
