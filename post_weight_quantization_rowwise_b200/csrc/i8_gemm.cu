@@ -52,16 +52,44 @@ __device__ __forceinline__ float finish(int sum, float da, float dw, float bias)
     return __fadd_rn(__fmul_rn(__fmul_rn(static_cast<float>(sum), da), dw), bias);
 }
 
-// Sixteen columns (tokens t ..) of this lane's channel r.
+// 32 sums of this lane's channel, of n tokens (lane i has the i-th one's scale), from y on.
 template <class T>
-__device__ __forceinline__ void put16(const Args& P, const uint32_t (&v)[16], int64_t t, int64_t r, float dw, float bias)
+__device__ __forceinline__ void put32(const uint32_t (&x)[32], float da, float dw, float bias, T* y, int64_t ldy, int n, bool real)
 {
-    T* y = static_cast<T*>(P.y) + t * P.ldy + r;
-    const int n = P.n_tok - t < 16 ? static_cast<int>(P.n_tok - t) : 16;
-    if (r >= P.n_out) return;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (i < n) y[i * P.ldy] = iqq::from_f32<T>(finish(static_cast<int>(v[i]), __ldg(P.as + t + i), dw, bias));
+    for (int i = 0; i < 32; ++i) {
+        const float o = finish(static_cast<int>(x[i]), __shfl_sync(0xffffffffu, da, i), dw, bias);
+        if (real && i < n) y[i * ldy] = iqq::from_f32<T>(o);
+    }
+}
+
+// This lane's channel r of tokens t0 .. t0 + cols - 1, from the tensor memory's columns at `at`: 32 at
+// a time, the next ones (and their tokens' scales, a lane each) on the way while these are finished.
+template <class T>
+__device__ __forceinline__ void put(const Args& P, uint32_t at, int64_t t0, int cols, int64_t r, float dw, float bias)
+{
+    const int lane = threadIdx.x & 31;
+    const bool real = r < P.n_out;
+    const auto scale = [&](int c) { return c + lane < cols ? __ldg(P.as + t0 + c + lane) : 0.0f; };
+    T* y = static_cast<T*>(P.y) + t0 * P.ldy + r;
+    uint32_t v0[32], v1[32];
+    float d0 = scale(0), d1 = 0.0f;
+    iqq::tmem_ld32(at, v0);
+    for (int c = 0; c < cols; c += 64) {
+        iqq::tmem_wait_ld(v0);
+        if (c + 32 < cols) {
+            iqq::tmem_ld32(at + c + 32, v1);
+            d1 = scale(c + 32);
+        }
+        put32<T>(v0, d0, dw, bias, y + c * P.ldy, P.ldy, cols - c, real);
+        if (c + 32 >= cols) break;
+        iqq::tmem_wait_ld(v1);
+        if (c + 64 < cols) {
+            iqq::tmem_ld32(at + c + 64, v0);
+            d0 = scale(c + 64);
+        }
+        put32<T>(v1, d1, dw, bias, y + (c + 32) * P.ldy, P.ldy, cols - c - 32, real);
+    }
 }
 
 // (0 + bias and no bias differ for no value but -0, which the product of a zero sum may have)
@@ -171,12 +199,7 @@ pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CU
             iqq::tc_fence_after();
             const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * 256;
             const int cols = P.n_tok - t0 < P.tn ? static_cast<int>(P.n_tok - t0) : P.tn;
-            for (int c = 0; c < cols; c += 16) {
-                uint32_t v[16];
-                iqq::tmem_ld16(at + c, v);
-                iqq::tmem_wait_ld(v);
-                put16<T>(P, v, t0 + c, r, dw, bias);
-            }
+            put<T>(P, at, t0, cols, r, dw, bias);
             iqq::tc_fence_before();
             __syncwarp();
             if (lane == 0) iqq::bar_arrive_cluster(iqq::map_rank(iqq::smem_u32(&S.taken[buf]), 0));
@@ -291,19 +314,16 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
         if (warp >= 2) {
             const int64_t r = m0 + row;
             const float dw = r < P.n_out ? __ldg(P.ws + r) : 0.0f, bias = bias_of(P, r);
-            for (int c = 0; c < cols; c += 16) {
-                uint32_t v[16];
-                iqq::tmem_ld16(lanes + c, v);
-                iqq::tmem_wait_ld(v);
-                put16<T>(P, v, t0 + c, r, dw, bias);
-            }
+            put<T>(P, lanes, t0, cols, r, dw, bias);
         }
     } else {
-        // Column c belongs to the cluster's CTA floor(c * split / cols): everybody sends it its
-        // part, into the stages' memory (free once every CTA's products are done).
+        // Columns per * o .. belong to the cluster's CTA o: everybody sends it its part, into the
+        // stages' memory (free once every CTA's products are done).
         const int per = (cols + P.split - 1) / P.split;
         iqq::cluster_sync();
         if (warp >= 2) {
+            int owner = 0, local = 0;
+            uint32_t to = iqq::map_rank(base + ((rank * per * kRows + row) << 2), 0);
             for (int c = 0; c < cols; c += 16) {
                 uint32_t v[16];
                 iqq::tmem_ld16(lanes + c, v);
@@ -311,19 +331,19 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     if (c + i >= cols) break;
-                    const int owner = (c + i) * P.split / cols;
-                    const int first = (owner * cols + P.split - 1) / P.split;
-                    const uint32_t at = base + (((rank * per + (c + i - first)) * kRows + row) << 2);
-                    iqq::st_cluster(iqq::map_rank(at, static_cast<uint32_t>(owner)), v[i]);
+                    iqq::st_cluster(to + (local * kRows << 2), v[i]);
+                    if (++local == per && c + i + 1 < cols) {
+                        local = 0;
+                        to = iqq::map_rank(base + ((rank * per * kRows + row) << 2), static_cast<uint32_t>(++owner));
+                    }
                 }
             }
         }
         __syncwarp();
         iqq::cluster_sync();
-        const int first = (static_cast<int>(rank) * cols + P.split - 1) / P.split;
-        const int end = ((static_cast<int>(rank) + 1) * cols + P.split - 1) / P.split;
+        const int first = static_cast<int>(rank) * per, mine = min(per, cols - first);
         const uint32_t* part = reinterpret_cast<const uint32_t*>(raw + (base - iqq::smem_u32(raw)));
-        for (int i = threadIdx.x; i < (end - first) * kRows; i += kThreads) {
+        for (int i = threadIdx.x; i < mine * kRows; i += kThreads) {
             uint32_t sum = 0;
             for (int src = 0; src < P.split; ++src) sum += part[src * per * kRows + i];
             const int64_t t = t0 + first + i / kRows, r = m0 + i % kRows;
