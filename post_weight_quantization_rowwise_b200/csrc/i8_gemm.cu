@@ -28,6 +28,7 @@ constexpr int kStep = 128;           // bytes of k a stage: one swizzle row
 constexpr int kRows = 128;           // channels a CTA
 constexpr int kABytes = kRows * kStep;
 constexpr int kMaxStages = 12;
+constexpr int kScales = 4 * 256 * 4;      // shared memory for the tokens' scales, a copy a finishing warp
 constexpr int kSmem = 227 * 1024 - 1024;  // beside the static shared memory
 constexpr int kSmemHalf = 112 * 1024;     // two CTAs an SM
 
@@ -52,43 +53,54 @@ __device__ __forceinline__ float finish(int sum, float da, float dw, float bias)
     return __fadd_rn(__fmul_rn(__fmul_rn(static_cast<float>(sum), da), dw), bias);
 }
 
-// 32 sums of this lane's channel, of n tokens (lane i has the i-th one's scale), from y on.
+// 32 sums of this lane's channel, of n tokens with the scales da, from y on.
 template <class T>
-__device__ __forceinline__ void put32(const uint32_t (&x)[32], float da, float dw, float bias, T* y, int64_t ldy, int n, bool real)
+__device__ __forceinline__ void put32(const uint32_t (&x)[32], const float* da, float dw, float bias, T* y, int64_t ldy, int n)
 {
+    if (n >= 32) {  // (checked apart: a test a token took as long as its arithmetic)
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const float o = finish(static_cast<int>(x[i]), __shfl_sync(0xffffffffu, da, i), dw, bias);
-        if (real && i < n) y[i * ldy] = iqq::from_f32<T>(o);
+        for (int i = 0; i < 32; i += 4) {
+            const float4 d = *reinterpret_cast<const float4*>(da + i);
+            y[0] = iqq::from_f32<T>(finish(static_cast<int>(x[i]), d.x, dw, bias));
+            y += ldy;
+            y[0] = iqq::from_f32<T>(finish(static_cast<int>(x[i + 1]), d.y, dw, bias));
+            y += ldy;
+            y[0] = iqq::from_f32<T>(finish(static_cast<int>(x[i + 2]), d.z, dw, bias));
+            y += ldy;
+            y[0] = iqq::from_f32<T>(finish(static_cast<int>(x[i + 3]), d.w, dw, bias));
+            y += ldy;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < n) y[i * ldy] = iqq::from_f32<T>(finish(static_cast<int>(x[i]), da[i], dw, bias));
     }
 }
 
 // This lane's channel r of tokens t0 .. t0 + cols - 1, from the tensor memory's columns at `at`: 32 at
-// a time, the next ones (and their tokens' scales, a lane each) on the way while these are finished.
+// a time, the next ones on the way while these are finished.  `da`: the warp's own 256 floats of
+// shared memory, for the tokens' scales.
 template <class T>
-__device__ __forceinline__ void put(const Args& P, uint32_t at, int64_t t0, int cols, int64_t r, float dw, float bias)
+__device__ __forceinline__ void put(const Args& P, uint32_t at, int64_t t0, int cols, int64_t r, float dw, float bias, float* da)
 {
     const int lane = threadIdx.x & 31;
     const bool real = r < P.n_out;
-    const auto scale = [&](int c) { return c + lane < cols ? __ldg(P.as + t0 + c + lane) : 0.0f; };
     T* y = static_cast<T*>(P.y) + t0 * P.ldy + r;
     uint32_t v0[32], v1[32];
-    float d0 = scale(0), d1 = 0.0f;
     iqq::tmem_ld32(at, v0);
+    __syncwarp();
+    for (int c = lane; c < cols; c += 32) da[c] = __ldg(P.as + t0 + c);
+    __syncwarp();
     for (int c = 0; c < cols; c += 64) {
         iqq::tmem_wait_ld(v0);
-        if (c + 32 < cols) {
-            iqq::tmem_ld32(at + c + 32, v1);
-            d1 = scale(c + 32);
-        }
-        put32<T>(v0, d0, dw, bias, y + c * P.ldy, P.ldy, cols - c, real);
+        if (c + 32 < cols) iqq::tmem_ld32(at + c + 32, v1);
+        if (real) put32<T>(v0, da + c, dw, bias, y + c * P.ldy, P.ldy, cols - c);
         if (c + 32 >= cols) break;
+        __syncwarp();
         iqq::tmem_wait_ld(v1);
-        if (c + 64 < cols) {
-            iqq::tmem_ld32(at + c + 64, v0);
-            d0 = scale(c + 64);
-        }
-        put32<T>(v1, d1, dw, bias, y + (c + 32) * P.ldy, P.ldy, cols - c - 32, real);
+        if (c + 64 < cols) iqq::tmem_ld32(at + c + 64, v0);
+        if (real) put32<T>(v1, da + c + 32, dw, bias, y + (c + 32) * P.ldy, P.ldy, cols - c - 32);
+        __syncwarp();
     }
 }
 
@@ -189,6 +201,7 @@ pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CU
         }
     } else if (warp >= 2) {
         const int quad = warp & 3;
+        float* scales = reinterpret_cast<float*>(raw + (base - iqq::smem_u32(raw)) + P.stages * stage_bytes) + (warp - 2) * 256;
         int turn = 0;
         for (int64_t i = pair; i < tiles; i += pairs, ++turn) {
             const int buf = turn & 1;
@@ -199,7 +212,7 @@ pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CU
             iqq::tc_fence_after();
             const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * 256;
             const int cols = P.n_tok - t0 < P.tn ? static_cast<int>(P.n_tok - t0) : P.tn;
-            put<T>(P, at, t0, cols, r, dw, bias);
+            put<T>(P, at, t0, cols, r, dw, bias, scales);
             iqq::tc_fence_before();
             __syncwarp();
             if (lane == 0) iqq::bar_arrive_cluster(iqq::map_rank(iqq::smem_u32(&S.taken[buf]), 0));
@@ -312,9 +325,10 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     if (P.split == 1) {
         if (warp >= 2) {
+            float* scales = reinterpret_cast<float*>(raw + (base - iqq::smem_u32(raw))) + (warp - 2) * 256;  // (the stages are free)
             const int64_t r = m0 + row;
             const float dw = r < P.n_out ? __ldg(P.ws + r) : 0.0f, bias = bias_of(P, r);
-            put<T>(P, lanes, t0, cols, r, dw, bias);
+            put<T>(P, lanes, t0, cols, r, dw, bias, scales);
         }
     } else {
         // Columns per * o .. belong to the cluster's CTA o: everybody sends it its part, into the
@@ -413,7 +427,7 @@ iqq_status launch(Args P, const int8_t* a, int64_t lda, const int8_t* w, int64_t
         s = iqq::byte_map(&amap, a, k, P.n_tok, lda, P.tn / 2);
         if (s == IQQ_OK) s = iqq::opt_in_smem(reinterpret_cast<const void*>(pair_kernel<T>), kSmem, pair_done);
         if (s != IQQ_OK) return s;
-        P.stages = std::min<int>(kMaxStages, (kSmem - 1024 - static_cast<int>(sizeof(Bars))) / (kABytes + P.tn / 2 * kStep));
+        P.stages = std::min<int>(kMaxStages, (kSmem - 1024 - kScales - static_cast<int>(sizeof(Bars))) / (kABytes + P.tn / 2 * kStep));
         const int64_t pairs = std::min<int64_t>(P.m_tiles * P.t_tiles, sms / 2);
         cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
         cfg.dynamicSmemBytes = kSmem - sizeof(Bars);  // the whole SM's: it takes the whole tensor memory
