@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 
 namespace iqq {
 
@@ -20,22 +21,53 @@ __device__ __forceinline__ float i8_scale(uint32_t amax_bits)
     return amax_bits < kTinyBits ? 0.0f : __fdiv_rn(__uint_as_float(amax_bits), 127.0f);
 }
 
-// rint(t / d) for t = num * mul, decided exactly.  The binary32 estimate p = t * fl(1/d) is
-// within 127 * 2^-22 of the quotient (three roundings), so it decides except next to a half;
-// there 2|t| is compared with (2m+1) d in binary64, where both are exact (|num| <= 24 bits,
-// |mul| <= 7 bits, 2m+1 <= 8 bits).
-__device__ __forceinline__ int i8_code(float num, int mul, float d, float inv)
+// rint(num * mul / d), decided exactly: 2 |num mul| is compared with (2m+1) d in binary64, where both
+// are exact (|num| <= 24 bits, |mul| <= 8 bits, 2m+1 <= 9 bits), m the quotient's floor or, where p is
+// next to a whole number, either side of it.  p: an estimate of the quotient within 127 * 2^-21.
+__device__ __forceinline__ int exact_code(float num, int mul, float d, float p)
 {
-    const float p = __fmul_rn(__fmul_rn(num, static_cast<float>(mul)), inv);
+    const int m = static_cast<int>(fabsf(p));
+    const double t2 = 2.0 * fabs(static_cast<double>(num) * mul), mid = (2 * m + 1) * static_cast<double>(d);
+    const int a = t2 > mid ? m + 1 : (t2 < mid ? m : m + (m & 1));
+    return p < 0.0f ? -a : a;
+}
+
+__device__ __forceinline__ int rint_code(float num, int mul, float d, float p)
+{
     const float r = rintf(p);
-    int q = static_cast<int>(r);
-    if (fabsf(p - r) > 0.5f - 6e-5f) {
-        const int m = static_cast<int>(fabsf(p));
-        const double t2 = 2.0 * fabs(static_cast<double>(num) * mul), mid = (2 * m + 1) * static_cast<double>(d);
-        const int a = t2 > mid ? m + 1 : (t2 < mid ? m : m + (m & 1));
-        q = p < 0.0f ? -a : a;
+    return fabsf(p - r) > 0.5f - 6e-5f ? exact_code(num, mul, d, p) : static_cast<int>(r);
+}
+
+// Eight codes rint(v / d), packed; inv = fl(1/d), |v / d| < 2^8.  The binary32 product p = v * inv is
+// within 127 * 2^-22 of the quotient, so it decides a code unless it is next to a half.  Adding
+// 1.5 * 2^23 rounds p to the nearest integer, ties to even, and leaves the integer's two's complement
+// in the sum's low bits; two values go through an instruction.
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float d, float inv)
+{
+    constexpr float kMagic = 12582912.0f;
+    uint32_t q[8];
+    float far = 0.0f, p[8];
+    const uint64_t inv2 = pack_f2(inv, inv), up = pack_f2(kMagic, kMagic), down = pack_f2(-kMagic, -kMagic);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const uint64_t p2 = mul_f2(pack_f2(v[i], v[i + 1]), inv2), r2 = add_f2(p2, up);
+        const uint64_t n2 = add_f2(r2, down);                       // exact
+        const uint64_t off = fma_f2(n2, pack_f2(-1.0f, -1.0f), p2);  // p - n, exact
+        float r0, r1, o0, o1;
+        unpack_f2(p2, p[i], p[i + 1]);
+        unpack_f2(r2, r0, r1);
+        unpack_f2(off, o0, o1);
+        q[i] = __float_as_uint(r0);
+        q[i + 1] = __float_as_uint(r1);
+        far = fmaxf(far, fmaxf(fabsf(o0), fabsf(o1)));
     }
-    return max(-127, min(127, q));
+    if (far > 0.5f - 6e-5f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = static_cast<uint32_t>(rint_code(v[i], 1, d, p[i]));
+    }
+    const uint32_t a = __byte_perm(q[0], q[1], 0x0040), b = __byte_perm(q[2], q[3], 0x0040);
+    const uint32_t c = __byte_perm(q[4], q[5], 0x0040), e = __byte_perm(q[6], q[7], 0x0040);
+    return make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(c, e, 0x5410));
 }
 
 __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d)

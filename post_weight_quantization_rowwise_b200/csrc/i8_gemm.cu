@@ -16,6 +16,8 @@
 //  split kernel  tiles of 128 channels x up to 256 tokens, the k axis split over a cluster of up
 //                to 8 CTAs whose partial sums meet in shared memory: when tokens are few, the
 //                weights' bytes bound the product and every SM has to read its share of them.
+#include <math.h>
+
 #include <algorithm>
 
 #include "i8_code.cuh"
@@ -227,7 +229,7 @@ pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CU
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap, const Args P,
              const uint32_t columns)
 {
@@ -331,39 +333,48 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
             put<T>(P, lanes, t0, cols, r, dw, bias, scales);
         }
     } else {
-        // Columns per * o .. belong to the cluster's CTA o: everybody sends it its part, into the
-        // stages' memory (free once every CTA's products are done).
-        const int per = (cols + P.split - 1) / P.split;
+        // Groups of four columns per * o .. belong to the cluster's CTA o: everybody sends it its part,
+        // 16 bytes a lane, into the stages' memory (free once every CTA's products are done).
+        const int groups = (cols + 3) / 4, per = (groups + P.split - 1) / P.split;
         iqq::cluster_sync();
         if (warp >= 2) {
+            const uint32_t mine = base + ((rank * per * kRows + row) << 4);
             int owner = 0, local = 0;
-            uint32_t to = iqq::map_rank(base + ((rank * per * kRows + row) << 2), 0);
-            for (int c = 0; c < cols; c += 16) {
+            uint32_t to = iqq::map_rank(mine, 0);
+            for (int q = 0; q < groups; q += 4) {
                 uint32_t v[16];
-                iqq::tmem_ld16(lanes + c, v);
+                iqq::tmem_ld16(lanes + 4 * q, v);
                 iqq::tmem_wait_ld(v);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    if (c + i >= cols) break;
-                    iqq::st_cluster(to + (local * kRows << 2), v[i]);
-                    if (++local == per && c + i + 1 < cols) {
+                for (int i = 0; i < 4; ++i) {
+                    if (q + i >= groups) break;
+                    iqq::st_cluster(to + ((local * kRows) << 4), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    if (++local == per && q + i + 1 < groups) {
                         local = 0;
-                        to = iqq::map_rank(base + ((rank * per * kRows + row) << 2), static_cast<uint32_t>(++owner));
+                        to = iqq::map_rank(mine, static_cast<uint32_t>(++owner));
                     }
                 }
             }
         }
         __syncwarp();
         iqq::cluster_sync();
-        const int first = static_cast<int>(rank) * per, mine = min(per, cols - first);
-        const uint32_t* part = reinterpret_cast<const uint32_t*>(raw + (base - iqq::smem_u32(raw)));
+        const int first = static_cast<int>(rank) * per, mine = min(per, groups - first);
+        const uint4* part = reinterpret_cast<const uint4*>(raw + (base - iqq::smem_u32(raw)));
         for (int i = threadIdx.x; i < mine * kRows; i += kThreads) {
-            uint32_t sum = 0;
-            for (int src = 0; src < P.split; ++src) sum += part[src * per * kRows + i];
-            const int64_t t = t0 + first + i / kRows, r = m0 + i % kRows;
-            if (r < P.n_out)
-                static_cast<T*>(P.y)[t * P.ldy + r] =
-                    iqq::from_f32<T>(finish(static_cast<int>(sum), __ldg(P.as + t), __ldg(P.ws + r), bias_of(P, r)));
+            uint4 sum = make_uint4(0, 0, 0, 0);
+            for (int src = 0; src < P.split; ++src) {
+                const uint4 v = part[src * per * kRows + i];
+                sum = make_uint4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+            }
+            const int64_t t = t0 + 4 * (first + i / kRows), r = m0 + i % kRows;
+            if (r >= P.n_out) continue;
+            const float dw = __ldg(P.ws + r), bias = bias_of(P, r);
+            T* y = static_cast<T*>(P.y) + t * P.ldy + r;
+            const uint32_t each[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (t + u < P.n_tok)
+                    y[u * P.ldy] = iqq::from_f32<T>(finish(static_cast<int>(each[u]), __ldg(P.as + t + u), dw, bias));
         }
     }
     if (late) iqq::raise_flags(P.flags, IQQ_FLAG_WAIT_TIMEOUT);
@@ -386,21 +397,52 @@ __global__ void __launch_bounds__(256) empty_kernel(const Args P)
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Where the pair kernel runs (else the split kernel), and its token tile.
-bool plan_pair(Args& P, int sms)
+// The launch is the one that this estimate of its time (in microseconds, from measurements on one
+// B200) finds shortest: which kernel, its token tile and its parts of the k axis.
+//   An SM takes in 0.14 MB of operands a microsecond, 0.1 MB when most SMs do; HBM gives 6 MB, and
+//   0.057 MB an SM when few ask; tensor cores take tn/256 * 0.27 a 128-byte step; a launch has 3.3,
+//   its finish 0.008 a token, joining parts 0.5 + 0.012 a token.
+// Both sides of its turns, tokens x channels x k: 192 x 11008 x 4096: pairs with 192 tokens 14.9 us,
+// with 64 tokens 20.1, split kernel 15.7; 16 x 11008 x 4096: 3 parts 11.2, 2 parts 13.0, 1 part 12.6;
+// 192 x 4096 x 14336: 4 parts of 192 tokens 21.1, one part of 128 tokens 29.5, pairs 31.0;
+// 64 x 11008 x 4096: pairs 12.8, 3 parts 13.6; 200 x 512 x 8192: 8 parts of 64 tokens 7.9, pairs 12.1.
+struct Choice {
+    double us = 1e300;
+    bool pair = false;
+    int tn = 0, split = 1;
+};
+
+Choice choose(int64_t n_tok, int64_t n_out, int64_t k, int kblocks, int sms)
 {
-    const int64_t m = ceil_div(P.n_out, 2 * kRows), pairs = sms / 2;
-    int64_t best = INT64_MAX;
-    for (int tn = 32; tn <= 256; tn += 32) {
-        const int64_t cost = ceil_div(m * ceil_div(P.n_tok, tn), pairs) * (tn + 24);
-        if (cost <= best) {
-            best = cost;
-            P.tn = tn;
+    const double bytes = (static_cast<double>(n_out) + static_cast<double>(n_tok)) * static_cast<double>(k) / 1e6;
+    Choice best;
+    const auto consider = [&](bool pair, int tn, int split) {
+        const int64_t tiles = ceil_div(n_out, pair ? 2 * kRows : kRows) * ceil_div(n_tok, tn);
+        const int64_t ctas = tiles * (pair ? 2 : split), per = ceil_div(kblocks, split);
+        if (split > 1 && ctas > (tn <= 64 ? 2 : 1) * sms) return;  // the parts of a tile run at once
+        const double stage = (kABytes + tn / (pair ? 2 : 1) * kStep) / 1e6;
+        // steps of the SM that has most; CTAs of up to 64 tokens run two an SM, but share what it takes in
+        const double steps = static_cast<double>(ceil_div(ctas, sms) * per);
+        const double use = static_cast<double>(ctas) / static_cast<double>(ceil_div(ctas, sms) * sms);
+        const double hbm = ctas <= sms ? std::min(6.0, 0.057 * static_cast<double>(ctas)) : 6.0 * std::sqrt(use);
+        double us = std::max(steps * stage / (ctas > 64 || pair ? 0.1 : 0.14), std::max(bytes / hbm, steps * tn * 0.00105));
+        us += 3.3 + 0.008 * tn + (split > 1 ? 0.5 + 0.012 * tn : 0.0);
+        if (us < best.us) {
+            best.us = us;
+            best.pair = pair;
+            best.tn = tn;
+            best.split = split;
         }
+    };
+    const int most = n_tok >= 256 ? 256 : static_cast<int>(ceil_div(n_tok, 16) * 16);
+    for (int split = std::min(8, kblocks); split >= 1; --split) {
+        consider(false, most, split);
+        if (most > 128) consider(false, 128, split);
+        if (most > 64) consider(false, 64, split);
     }
-    P.m_tiles = m;
-    P.t_tiles = ceil_div(P.n_tok, P.tn);
-    return m * P.t_tiles * 2 > pairs && P.n_tok > 64;
+    if (n_tok > 32)
+        for (int tn = 32; tn <= 256 && tn < n_tok + 32; tn += 32) consider(true, tn, 1);
+    return best;
 }
 
 template <class T>
@@ -423,7 +465,12 @@ iqq_status launch(Args P, const int8_t* a, int64_t lda, const int8_t* w, int64_t
     CUtensorMap wmap, amap;
     iqq_status s = iqq::byte_map(&wmap, w, k, P.n_out, ldw, kRows);
     if (s != IQQ_OK) return s;
-    if (plan_pair(P, sms)) {
+    const Choice plan = choose(P.n_tok, P.n_out, k, P.kblocks, sms);
+    P.tn = plan.tn;
+    P.split = plan.split;
+    P.m_tiles = ceil_div(P.n_out, plan.pair ? 2 * kRows : kRows);
+    P.t_tiles = ceil_div(P.n_tok, P.tn);
+    if (plan.pair) {
         s = iqq::byte_map(&amap, a, k, P.n_tok, lda, P.tn / 2);
         if (s == IQQ_OK) s = iqq::opt_in_smem(reinterpret_cast<const void*>(pair_kernel<T>), kSmem, pair_done);
         if (s != IQQ_OK) return s;
@@ -434,13 +481,13 @@ iqq_status launch(Args P, const int8_t* a, int64_t lda, const int8_t* w, int64_t
         cudaLaunchKernelEx(&cfg, pair_kernel<T>, wmap, amap, P);
         return iqq::launch_status();
     }
-    P.tn = P.n_tok >= 256 ? 256 : static_cast<int>(ceil_div(P.n_tok, 16) * 16);
-    P.m_tiles = ceil_div(P.n_out, kRows);
-    P.t_tiles = ceil_div(P.n_tok, P.tn);
-    const int64_t tiles = P.m_tiles * P.t_tiles, slots = P.tn <= 64 ? 2 * sms : sms;
-    P.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, slots / tiles, static_cast<int64_t>(P.kblocks)})));
+    const int64_t tiles = P.m_tiles * P.t_tiles;
     if (tiles * P.split > 0x7fffffffLL) return IQQ_ERR_SHAPE;
-    const int stage = kABytes + P.tn * kStep, room = (P.tn <= 64 ? kSmemHalf : kSmem - static_cast<int>(sizeof(Bars))) - 1024;
+    // Small stages: two CTAs an SM where there are so many, and where a CTA has few steps anyway (16 x
+    // 4096 x 4096 in 4 parts: 6.9 us, with an SM's memory each 7.6; clusters of 8 then find room as
+    // well); else all of an SM's memory for stages (64 x 11008 x 4096 in one part: 12.9, with half 16.4).
+    const bool two = P.tn <= 64 && (tiles * P.split > sms || ceil_div(P.kblocks, P.split) <= 8);
+    const int stage = kABytes + P.tn * kStep, room = (two ? kSmemHalf : kSmem - static_cast<int>(sizeof(Bars))) - 1024;
     P.stages = std::min(kMaxStages, room / stage);
     uint32_t columns = 32;
     while (columns < static_cast<uint32_t>(P.tn)) columns *= 2;

@@ -35,16 +35,14 @@ __device__ __forceinline__ uint32_t amax8(const float (&v)[8], uint32_t m)
 
 __device__ __forceinline__ void store_unit(int8_t* row, int64_t j, int64_t n, const float (&v)[8], float d, float inv)
 {
-    int q[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = d > 0.0f ? iqq::i8_code(v[i], 1, d, inv) : 0;  // (NaN > 0 is false)
+    uint2 q = make_uint2(0u, 0u);
+    if (d > 0.0f) q = iqq::codes8(v, d, inv);  // (NaN > 0 is false)
     if (j + 8 <= n) {
-        *reinterpret_cast<uint2*>(row + j) =
-            make_uint2(iqq::pack4(q[0], q[1], q[2], q[3]), iqq::pack4(q[4], q[5], q[6], q[7]));
+        *reinterpret_cast<uint2*>(row + j) = q;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (j + i < n) row[j + i] = static_cast<int8_t>(q[i]);
+            if (j + i < n) row[j + i] = static_cast<int8_t>((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
     }
 }
 

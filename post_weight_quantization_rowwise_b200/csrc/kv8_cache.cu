@@ -90,11 +90,7 @@ append_kernel(const Kv8 C, const New N, uint32_t* __restrict__ flags)
     }
     int8_t* tile = C.codes[which] + ((static_cast<int64_t>(p) * C.heads + head) << C.page_log2) * D;
     auto store = [&](int u, const float(&t)[8]) {
-        int q[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = d > 0.0f ? iqq::i8_code(t[i], 1, d, inv) : 0;
-        *reinterpret_cast<uint2*>(tile + lo * D + u * 8) =
-            make_uint2(iqq::pack4(q[0], q[1], q[2], q[3]), iqq::pack4(q[4], q[5], q[6], q[7]));
+        *reinterpret_cast<uint2*>(tile + lo * D + u * 8) = d > 0.0f ? iqq::codes8(t, d, inv) : make_uint2(0u, 0u);
     };
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
@@ -107,6 +103,7 @@ append_kernel(const Kv8 C, const New N, uint32_t* __restrict__ flags)
         store(u, t);
     }
     if (d > held) {  // the tokens already in the page, to the new scale
+        const float ratio = held * inv;
         for (int u = tid; u < lo * kRow; u += kThreads) {
             uint2* at = reinterpret_cast<uint2*>(tile + u * 8);
             const uint2 w = *at;
@@ -114,7 +111,7 @@ append_kernel(const Kv8 C, const New N, uint32_t* __restrict__ flags)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int c = static_cast<int8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
-                q[i] = iqq::i8_code(held, c, d, inv);
+                q[i] = iqq::rint_code(held, c, d, ratio * static_cast<float>(c));
             }
             *at = make_uint2(iqq::pack4(q[0], q[1], q[2], q[3]), iqq::pack4(q[4], q[5], q[6], q[7]));
         }
