@@ -38,32 +38,32 @@ __device__ __forceinline__ int rint_code(float num, int mul, float d, float p)
     return fabsf(p - r) > 0.5f - 6e-5f ? exact_code(num, mul, d, p) : static_cast<int>(r);
 }
 
-// Eight codes rint(v / d), packed; inv = fl(1/d), |v / d| < 2^8.  The binary32 product p = v * inv is
-// within 127 * 2^-22 of the quotient, so it decides a code unless it is next to a half.  Adding
-// 1.5 * 2^23 rounds p to the nearest integer, ties to even, and leaves the integer's two's complement
-// in the sum's low bits; two values go through an instruction.
+// Eight codes rint(v / d), packed; inv = fl(1/d), |v / d| < 2^8.  v * inv is within 127 * 2^-23 of the
+// quotient, so it decides a code unless it is next to a half.  Adding 1.5 * 2^23 to the product, in
+// one rounding, gives the nearest integer, ties to even, as the sum's low bits (two's complement);
+// two values go through an instruction.
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], float d, float inv)
 {
     constexpr float kMagic = 12582912.0f;
     uint32_t q[8];
-    float far = 0.0f, p[8];
-    const uint64_t inv2 = pack_f2(inv, inv), up = pack_f2(kMagic, kMagic), down = pack_f2(-kMagic, -kMagic);
+    float far = 0.0f, near[8], off[8];
+    const uint64_t inv2 = pack_f2(inv, inv), up = pack_f2(kMagic, kMagic), minus = pack_f2(-1.0f, -1.0f);
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-        const uint64_t p2 = mul_f2(pack_f2(v[i], v[i + 1]), inv2), r2 = add_f2(p2, up);
-        const uint64_t n2 = add_f2(r2, down);                       // exact
-        const uint64_t off = fma_f2(n2, pack_f2(-1.0f, -1.0f), p2);  // p - n, exact
-        float r0, r1, o0, o1;
-        unpack_f2(p2, p[i], p[i + 1]);
+        const uint64_t v2 = pack_f2(v[i], v[i + 1]), r2 = fma_f2(v2, inv2, up);
+        const uint64_t n2 = fma_f2(r2, minus, up);                 // less the integer, exact
+        float r0, r1;
         unpack_f2(r2, r0, r1);
-        unpack_f2(off, o0, o1);
+        unpack_f2(n2, near[i], near[i + 1]);
+        unpack_f2(fma_f2(v2, inv2, n2), off[i], off[i + 1]);       // what is left
         q[i] = __float_as_uint(r0);
         q[i + 1] = __float_as_uint(r1);
-        far = fmaxf(far, fmaxf(fabsf(o0), fabsf(o1)));
+        far = fmaxf(far, fmaxf(fabsf(off[i]), fabsf(off[i + 1])));
     }
     if (far > 0.5f - 6e-5f) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = static_cast<uint32_t>(rint_code(v[i], 1, d, p[i]));
+        for (int i = 0; i < 8; ++i)
+            if (fabsf(off[i]) > 0.5f - 6e-5f) q[i] = static_cast<uint32_t>(exact_code(v[i], 1, d, off[i] - near[i]));
     }
     const uint32_t a = __byte_perm(q[0], q[1], 0x0040), b = __byte_perm(q[2], q[3], 0x0040);
     const uint32_t c = __byte_perm(q[4], q[5], 0x0040), e = __byte_perm(q[6], q[7], 0x0040);

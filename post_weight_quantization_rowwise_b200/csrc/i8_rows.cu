@@ -15,62 +15,81 @@ namespace {
 
 constexpr int kMaxWarps = 32;
 
-template <class T, bool VEC>
-__device__ __forceinline__ void load_unit(const T* row, int64_t j, int64_t n, float (&v)[8])
-{
-    if (VEC && j + 8 <= n) {
-        iqq::load8(row + j, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = j + i < n ? iqq::to_f32(row[j + i]) : 0.0f;
-    }
-}
+// Eight values as they are in memory, so that a row of 16-bit values waits in half the registers.
+struct Wide {
+    float4 a, b;
+};
+template <class T> struct Raw { using type = uint4; };
+template <> struct Raw<float> { using type = Wide; };
 
-__device__ __forceinline__ uint32_t amax8(const float (&v)[8], uint32_t m)
+__device__ __forceinline__ void fetch(const float* p, Wide& r)
 {
+    r.a = __ldg(reinterpret_cast<const float4*>(p));
+    r.b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+}
+template <class T> __device__ __forceinline__ void fetch(const T* p, uint4& r) { r = __ldg(reinterpret_cast<const uint4*>(p)); }
+
+__device__ __forceinline__ void widen(const float*, const Wide& r, float (&v)[8])
+{
+    v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
+    v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
+}
+template <class T> __device__ __forceinline__ void widen(const T* p, const uint4& r, float (&v)[8]) { iqq::widen8(p, r, v); }
+
+// Largest magnitude's bits so far: of binary32 values, or of two 16-bit values in a word (magnitudes
+// order as their bits do, NaN above Inf above all else).
+__device__ __forceinline__ uint32_t amax8(const float*, const Wide& r, uint32_t m)
+{
+    const float v[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
     return m;
 }
-
-__device__ __forceinline__ void store_unit(int8_t* row, int64_t j, int64_t n, const float (&v)[8], float d, float inv)
+template <class T>
+__device__ __forceinline__ uint32_t amax8(const T*, const uint4& r, uint32_t m)
 {
-    uint2 q = make_uint2(0u, 0u);
-    if (d > 0.0f) q = iqq::codes8(v, d, inv);  // (NaN > 0 is false)
-    if (j + 8 <= n) {
-        *reinterpret_cast<uint2*>(row + j) = q;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (j + i < n) row[j + i] = static_cast<int8_t>((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
-    }
+    m = __vmaxu2(m, r.x & 0x7fff7fffu);
+    m = __vmaxu2(m, r.y & 0x7fff7fffu);
+    m = __vmaxu2(m, r.z & 0x7fff7fffu);
+    return __vmaxu2(m, r.w & 0x7fff7fffu);
+}
+// The same as the bits of one binary32 magnitude.
+__device__ __forceinline__ uint32_t amax_bits(const float*, uint32_t m) { return m; }
+__device__ __forceinline__ uint32_t amax_bits(const __nv_bfloat16*, uint32_t m) { return max(m & 0xffffu, m >> 16) << 16; }
+__device__ __forceinline__ uint32_t amax_bits(const __half*, uint32_t m)
+{
+    return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(max(m & 0xffffu, m >> 16))))) & 0x7fffffffu;
 }
 
-template <class T, int NV, bool VEC>
+// Rows of whole units of eight values on 16-byte boundaries.
+template <class T, int NV>
 __global__ void __launch_bounds__(1024)
 i8_rows_kernel(const T* __restrict__ x, int64_t ldx, int8_t* __restrict__ codes, int64_t ldc,
                float* __restrict__ scales, int64_t nrows, int64_t n, uint32_t* __restrict__ flags)
 {
     __shared__ uint32_t part[2][kMaxWarps];
     const int tid = threadIdx.x, lane = tid & 31, warps = blockDim.x >> 5;
+    const int64_t units = n / 8, beyond = static_cast<int64_t>(NV) * blockDim.x;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t step = 8LL * blockDim.x;
     int turn = 0;
     for (int64_t r = blockIdx.x; r < nrows; r += gridDim.x, turn ^= 1) {
         const T* row = x + r * ldx;
-        float v[NV][8];
+        typename Raw<T>::type v[NV];
         uint32_t m = 0u;
 #pragma unroll
-        for (int u = 0; u < NV; ++u) load_unit<T, VEC>(row, 8LL * tid + u * step, n, v[u]);
-#pragma unroll
-        for (int u = 0; u < NV; ++u) m = amax8(v[u], m);
-        for (int64_t j = 8LL * tid + NV * step; j < n; j += step) {
-            float t[8];
-            load_unit<T, VEC>(row, j, n, t);
-            m = amax8(t, m);
+        for (int u = 0; u < NV; ++u) {
+            v[u] = {};
+            if (tid + u * static_cast<int>(blockDim.x) < units) fetch(row + 8 * (tid + u * blockDim.x), v[u]);
         }
-        m = __reduce_max_sync(0xffffffffu, m);
+#pragma unroll
+        for (int u = 0; u < NV; ++u) m = amax8(row, v[u], m);
+        for (int64_t u = tid + beyond; u < units; u += blockDim.x) {
+            typename Raw<T>::type t;
+            fetch(row + 8 * u, t);
+            m = amax8(row, t, m);
+        }
+        m = __reduce_max_sync(0xffffffffu, amax_bits(row, m));
         // two sets of slots in turn: a warp can be at most one row ahead of another
         if (lane == 0) part[turn][tid >> 5] = m;
         __syncthreads();
@@ -81,25 +100,76 @@ i8_rows_kernel(const T* __restrict__ x, int64_t ldx, int8_t* __restrict__ codes,
             scales[r] = d;
             if (m >= iqq::kInfBits) iqq::raise_flags(flags, IQQ_FLAG_NONFINITE_INPUT);
         }
-        int8_t* out = codes + r * ldc;
+        uint2* out = reinterpret_cast<uint2*>(codes + r * ldc);
+        if (d > 0.0f) {  // (NaN > 0 is false)
 #pragma unroll
-        for (int u = 0; u < NV; ++u) {
-            const int64_t j = 8LL * tid + u * step;
-            if (j < n) store_unit(out, j, n, v[u], d, inv);
-        }
-        for (int64_t j = 8LL * tid + NV * step; j < n; j += step) {
-            float t[8];
-            load_unit<T, VEC>(row, j, n, t);
-            store_unit(out, j, n, t, d, inv);
+            for (int u = 0; u < NV; ++u) {
+                float w[8];
+                widen(row, v[u], w);
+                if (tid + u * static_cast<int>(blockDim.x) < units) out[tid + u * blockDim.x] = iqq::codes8(w, d, inv);
+            }
+            for (int64_t u = tid + beyond; u < units; u += blockDim.x) {
+                typename Raw<T>::type t;
+                float w[8];
+                fetch(row + 8 * u, t);
+                widen(row, t, w);
+                out[u] = iqq::codes8(w, d, inv);
+            }
+        } else {
+            for (int64_t u = tid; u < units; u += blockDim.x) out[u] = make_uint2(0u, 0u);
         }
     }
 }
 
-template <class T, int NV, bool VEC>
-iqq_status launch(const void* x, int64_t ldx, int8_t* codes, int64_t ldc, float* scales, int64_t nrows, int64_t n,
-                  uint32_t* flags, cudaStream_t st)
+// Any rows, a value at a time; the second pass reads them again.
+template <class T>
+__global__ void __launch_bounds__(1024)
+i8_rows_any_kernel(const T* __restrict__ x, int64_t ldx, int8_t* __restrict__ codes, int64_t ldc,
+                   float* __restrict__ scales, int64_t nrows, int64_t n, uint32_t* __restrict__ flags)
 {
-    const int64_t units = (n + 7) / 8, per = (units + NV - 1) / NV;
+    __shared__ uint32_t part[2][kMaxWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warps = blockDim.x >> 5;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int turn = 0;
+    for (int64_t r = blockIdx.x; r < nrows; r += gridDim.x, turn ^= 1) {
+        const T* row = x + r * ldx;
+        uint32_t m = 0u;
+#pragma unroll 8
+        for (int64_t j = tid; j < n; j += blockDim.x) m = max(m, __float_as_uint(iqq::to_f32(row[j])) & 0x7fffffffu);
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) part[turn][tid >> 5] = m;
+        __syncthreads();
+        m = __reduce_max_sync(0xffffffffu, lane < warps ? part[turn][lane] : 0u);
+        const float d = iqq::i8_scale(m);
+        const float inv = d > 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
+        if (tid == 0) {
+            scales[r] = d;
+            if (m >= iqq::kInfBits) iqq::raise_flags(flags, IQQ_FLAG_NONFINITE_INPUT);
+        }
+        int8_t* out = codes + r * ldc;
+        // four codes a thread, a word where there are four (rows of codes begin on 16-byte boundaries)
+        for (int64_t j = 4LL * tid; j < n; j += 4LL * blockDim.x) {
+            int q[4] = {0, 0, 0, 0};
+            const int most = n - j < 4 ? static_cast<int>(n - j) : 4;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float v = i < most ? iqq::to_f32(row[j + i]) : 0.0f;
+                if (d > 0.0f) q[i] = iqq::rint_code(v, 1, d, v * inv);
+            }
+            if (most == 4) {
+                *reinterpret_cast<uint32_t*>(out + j) = iqq::pack4(q[0], q[1], q[2], q[3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    if (i < most) out[j + i] = static_cast<int8_t>(q[i]);
+            }
+        }
+    }
+}
+
+iqq_status start(void (*kernel)(), int64_t per, int64_t nrows, cudaStream_t st, void** args)
+{
     const int threads = static_cast<int>(per >= 1024 ? 1024 : (per <= 64 ? 64 : (per + 31) / 32 * 32));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(nrows < 0x7fffffffLL ? nrows : 0x7fffffffLL));
@@ -110,8 +180,7 @@ iqq_status launch(const void* x, int64_t ldx, int8_t* codes, int64_t ldc, float*
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, i8_rows_kernel<T, NV, VEC>, static_cast<const T*>(x), ldx, codes, ldc, scales, nrows, n,
-                       flags);
+    cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kernel), args);
     return iqq::launch_status();
 }
 
@@ -119,14 +188,16 @@ template <class T>
 iqq_status launch_type(const void* x, int64_t ldx, int8_t* codes, int64_t ldc, float* scales, int64_t nrows, int64_t n,
                        uint32_t* flags, cudaStream_t st)
 {
-    const bool vec = iqq::aligned(x, 16) && (ldx * static_cast<int64_t>(sizeof(T))) % 16 == 0;
-    // Few rows (less than two CTAs an SM): one unit a thread, the shortest chain.  Many rows:
-    // four units in flight a thread.
-    const bool few = nrows < 2LL * iqq::sm_count();
-    if (vec) return few ? launch<T, 1, true>(x, ldx, codes, ldc, scales, nrows, n, flags, st)
-                        : launch<T, 4, true>(x, ldx, codes, ldc, scales, nrows, n, flags, st);
-    return few ? launch<T, 1, false>(x, ldx, codes, ldc, scales, nrows, n, flags, st)
-               : launch<T, 4, false>(x, ldx, codes, ldc, scales, nrows, n, flags, st);
+    const T* from = static_cast<const T*>(x);
+    void* args[] = {&from, &ldx, &codes, &ldc, &scales, &nrows, &n, &flags};
+    const int64_t units = (n + 7) / 8;
+    if (n % 8 != 0 || !iqq::aligned(x, 16) || (ldx * static_cast<int64_t>(sizeof(T))) % 16 != 0)
+        return start(reinterpret_cast<void (*)()>(i8_rows_any_kernel<T>), units, nrows, st, args);
+    // Few rows (less than two CTAs an SM): one unit a thread, the shortest chain.  Many rows: four
+    // units in flight a thread.
+    if (nrows < 2LL * iqq::sm_count())
+        return start(reinterpret_cast<void (*)()>(i8_rows_kernel<T, 1>), units, nrows, st, args);
+    return start(reinterpret_cast<void (*)()>(i8_rows_kernel<T, 4>), (units + 3) / 4, nrows, st, args);
 }
 
 }  // namespace
