@@ -787,6 +787,7 @@ class Kv8Cache:
                                        v_scales.data_ptr(), self.n_pages, self.n_kv_heads, self.page_size,
                                        self.head_dim)
         self._ref = ctypes.byref(self._struct)
+        self._workspace = {}  # workspace bytes by a call's sizes
 
 
 def kv8_cache(n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, device="cuda"):
@@ -858,16 +859,24 @@ def kv8_gather(cache, block_tables, seq_lens, cu_tokens, n_tokens: int, dtype=No
     """Allocates and returns (k, v) of iqq_kv8_gather; n_tokens is cu_tokens' last value (rows that
     belong to no sequence are unspecified); dtype None: float32."""
     import torch
-    shape = (n_tokens, cache.n_kv_heads, cache.head_dim)
-    k = _empty(shape, dtype or torch.float32, cache.device, stream)
-    v = _empty(shape, dtype or torch.float32, cache.device, stream)
+    k, v = _empty((2, n_tokens, cache.n_kv_heads, cache.head_dim), dtype or torch.float32, cache.device,
+                  stream).unbind(0)
     return iqq_kv8_gather(cache, block_tables, seq_lens, cu_tokens, k, v, flags, stream)
 
 
 def kv8_attention_workspace_bytes(cache, n_seqs: int, table_width: int, n_heads: int, n_tokens: int) -> int:
-    """Device workspace iqq_kv8_attention needs (0: none)."""
-    seqs = _Kv8SeqsStruct(None, table_width, table_width, None, None, n_seqs)
-    return int(_lib.iqq_kv8_attention_workspace_bytes(cache._ref, ctypes.byref(seqs), n_heads, n_tokens))
+    """Device workspace iqq_kv8_attention needs (0: none), on the cache's device."""
+    import torch
+    key = (n_seqs, table_width, n_heads, n_tokens)
+    need = cache._workspace.get(key)  # the sizes alone decide: asked for once
+    if need is None:
+        seqs = _Kv8SeqsStruct(None, table_width, table_width, None, None, n_seqs)
+        with torch.cuda.device(cache.index):
+            need = int(_lib.iqq_kv8_attention_workspace_bytes(cache._ref, ctypes.byref(seqs), n_heads, n_tokens))
+        if len(cache._workspace) >= 4096:
+            cache._workspace.clear()
+        cache._workspace[key] = need
+    return need
 
 
 def iqq_kv8_attention(cache, q, block_tables, seq_lens, cu_tokens, out, lse=None, scale=None, workspace=None,

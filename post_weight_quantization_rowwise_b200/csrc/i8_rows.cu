@@ -15,52 +15,6 @@ namespace {
 
 constexpr int kMaxWarps = 32;
 
-// Eight values as they are in memory, so that a row of 16-bit values waits in half the registers.
-struct Wide {
-    float4 a, b;
-};
-template <class T> struct Raw { using type = uint4; };
-template <> struct Raw<float> { using type = Wide; };
-
-__device__ __forceinline__ void fetch(const float* p, Wide& r)
-{
-    r.a = __ldg(reinterpret_cast<const float4*>(p));
-    r.b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-}
-template <class T> __device__ __forceinline__ void fetch(const T* p, uint4& r) { r = __ldg(reinterpret_cast<const uint4*>(p)); }
-
-__device__ __forceinline__ void widen(const float*, const Wide& r, float (&v)[8])
-{
-    v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
-    v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
-}
-template <class T> __device__ __forceinline__ void widen(const T* p, const uint4& r, float (&v)[8]) { iqq::widen8(p, r, v); }
-
-// Largest magnitude's bits so far: of binary32 values, or of two 16-bit values in a word (magnitudes
-// order as their bits do, NaN above Inf above all else).
-__device__ __forceinline__ uint32_t amax8(const float*, const Wide& r, uint32_t m)
-{
-    const float v[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-    return m;
-}
-template <class T>
-__device__ __forceinline__ uint32_t amax8(const T*, const uint4& r, uint32_t m)
-{
-    m = __vmaxu2(m, r.x & 0x7fff7fffu);
-    m = __vmaxu2(m, r.y & 0x7fff7fffu);
-    m = __vmaxu2(m, r.z & 0x7fff7fffu);
-    return __vmaxu2(m, r.w & 0x7fff7fffu);
-}
-// The same as the bits of one binary32 magnitude.
-__device__ __forceinline__ uint32_t amax_bits(const float*, uint32_t m) { return m; }
-__device__ __forceinline__ uint32_t amax_bits(const __nv_bfloat16*, uint32_t m) { return max(m & 0xffffu, m >> 16) << 16; }
-__device__ __forceinline__ uint32_t amax_bits(const __half*, uint32_t m)
-{
-    return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(max(m & 0xffffu, m >> 16))))) & 0x7fffffffu;
-}
-
 // Rows of whole units of eight values on 16-byte boundaries.
 template <class T, int NV>
 __global__ void __launch_bounds__(1024)
@@ -75,21 +29,21 @@ i8_rows_kernel(const T* __restrict__ x, int64_t ldx, int8_t* __restrict__ codes,
     int turn = 0;
     for (int64_t r = blockIdx.x; r < nrows; r += gridDim.x, turn ^= 1) {
         const T* row = x + r * ldx;
-        typename Raw<T>::type v[NV];
+        typename iqq::Raw<T>::type v[NV];
         uint32_t m = 0u;
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             v[u] = {};
-            if (tid + u * static_cast<int>(blockDim.x) < units) fetch(row + 8 * (tid + u * blockDim.x), v[u]);
+            if (tid + u * static_cast<int>(blockDim.x) < units) iqq::fetch(row + 8 * (tid + u * blockDim.x), v[u]);
         }
 #pragma unroll
-        for (int u = 0; u < NV; ++u) m = amax8(row, v[u], m);
+        for (int u = 0; u < NV; ++u) m = iqq::amax8(row, v[u], m);
         for (int64_t u = tid + beyond; u < units; u += blockDim.x) {
-            typename Raw<T>::type t;
-            fetch(row + 8 * u, t);
-            m = amax8(row, t, m);
+            typename iqq::Raw<T>::type t;
+            iqq::fetch(row + 8 * u, t);
+            m = iqq::amax8(row, t, m);
         }
-        m = __reduce_max_sync(0xffffffffu, amax_bits(row, m));
+        m = __reduce_max_sync(0xffffffffu, iqq::amax_bits(row, m));
         // two sets of slots in turn: a warp can be at most one row ahead of another
         if (lane == 0) part[turn][tid >> 5] = m;
         __syncthreads();
@@ -105,14 +59,14 @@ i8_rows_kernel(const T* __restrict__ x, int64_t ldx, int8_t* __restrict__ codes,
 #pragma unroll
             for (int u = 0; u < NV; ++u) {
                 float w[8];
-                widen(row, v[u], w);
+                iqq::widen(row, v[u], w);
                 if (tid + u * static_cast<int>(blockDim.x) < units) out[tid + u * blockDim.x] = iqq::codes8(w, d, inv);
             }
             for (int64_t u = tid + beyond; u < units; u += blockDim.x) {
-                typename Raw<T>::type t;
+                typename iqq::Raw<T>::type t;
                 float w[8];
-                fetch(row + 8 * u, t);
-                widen(row, t, w);
+                iqq::fetch(row + 8 * u, t);
+                iqq::widen(row, t, w);
                 out[u] = iqq::codes8(w, d, inv);
             }
         } else {

@@ -53,7 +53,7 @@ __device__ __forceinline__ void check_spans(const Kv8& C, bool places, uint32_t*
 
 // Work laid out by sequence without a pass over the spans: sequence b's slots begin at
 // slot_base(b) = floor(cu[b] * per / unit) + extra * b, so slots of every sequence fit between its
-// base and the next one's, and the sequence of a slot is found by bisection over cu.  (cu is
+// base and the next one's, and the sequence of a slot is found by a search over cu.  (cu is
 // clamped, so arrays that are not monotone give some sequence in range, which span_of checks.)
 __device__ __forceinline__ int64_t slot_base(const Kv8& C, int b, int per, int unit, int extra)
 {
@@ -61,13 +61,16 @@ __device__ __forceinline__ int64_t slot_base(const Kv8& C, int b, int per, int u
     return static_cast<int64_t>(c) * per / unit + static_cast<int64_t>(extra) * b;
 }
 
+// All lanes of a warp together, 32 places of cu looked at each time.
 __device__ __forceinline__ int seq_of_slot(const Kv8& C, int64_t slot, int per, int unit, int extra)
 {
+    const int lane = threadIdx.x & 31;
     int lo = 0, hi = C.n_seqs;  // base(lo) <= slot < base(hi)
     while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (slot_base(C, mid, per, unit, extra) <= slot) lo = mid;
-        else hi = mid;
+        const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
+        const uint32_t past = __ballot_sync(0xffffffffu, at < hi && slot_base(C, at, per, unit, extra) <= slot);
+        lo += step * (past == 0xffffffffu ? 32 : __ffs(~past) - 1);
+        hi = min(hi, lo + step);
     }
     return lo;
 }

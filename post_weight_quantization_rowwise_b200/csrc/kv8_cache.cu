@@ -1,11 +1,12 @@
 // kv8_cache.cu -- writing and reading back the paged int8 key/value cache, on sm_100a.
 //
-// Append.  One CTA takes one (page, head) of the keys or of the values: the new tokens of the
-// page set its scale, so the CTA that quantizes them is the only one that reads the page's old
-// scale and rewrites its old codes, and no two CTAs meet.  d = max(d_old, fl32(amax/127)); the
-// new values stay in registers between the maximum and the rounding (what a page of 128 tokens
-// does not fit is read again, from L2).  HBM-bound on prompts (2 or 4 B in, 1 B out a value);
-// a decoding step is one token and, when the scale grows, the page's old codes.
+// Append.  One CTA (a warp, where a sequence has few new tokens) takes one (page, head) of the keys or
+// of the values: the new tokens of the page set its scale, so whoever quantizes them is the only one
+// that reads the page's old scale and rewrites its old codes.  d = max(d_old, fl32(amax/127)); the new
+// values wait in registers, as they were read, between the maximum and the rounding (what a page of
+// 128 tokens does not fit is read again, from L2).  HBM-bound on prompts (2 or 4 B in, 1 B out a
+// value); a decoding step is one token and, when the scale grows, the page's old codes, and takes the
+// five dependent reads (cu, the span, the table, the scale, the codes) that lead to its store.
 //
 // Gather.  One warp a packed row: fl32(d * q) of all heads, 8 codes in and 16 or 32 B out a lane.
 #include "kv8.cuh"
@@ -15,25 +16,30 @@ namespace {
 using iqq::Kv8;
 using iqq::Span;
 
-constexpr int kThreads = 256;
-constexpr int kUnits = 4;  // units of eight values a thread keeps
+constexpr int kThreads = 256;        // of a gathering CTA
+constexpr int kAppendThreads = 128;
 
 struct New {
     const void* p[2];
     int64_t token_stride[2], head_stride[2];
 };
 
-template <class T, int D>
-__global__ void __launch_bounds__(kThreads)
+// G threads (a warp, or the CTA) take slot, head and which (keys or values) together.
+template <class T, int D, int G>
+__global__ void __launch_bounds__(kAppendThreads, 8)
 append_kernel(const Kv8 C, const New N, uint32_t* __restrict__ flags)
 {
-    constexpr int kRow = D / 8;  // units of a token
-    __shared__ uint32_t part[kThreads / 32];
-    const int tid = threadIdx.x, head = blockIdx.y, which = blockIdx.z;
+    constexpr int kRow = D / 8;                        // units of eight values of a token
+    constexpr int kUnits = sizeof(T) == 2 ? 8 : 4;     // units a thread keeps
+    __shared__ uint32_t part[kAppendThreads / 32];
+    const int tid = threadIdx.x % G, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     iqq::check_spans(C, true, flags);
     const int page = 1 << C.page_log2;
+    const int item = (blockIdx.y * kAppendThreads + threadIdx.x) / G;  // head and which, which first
+    if (item >= 2 * C.heads) return;
+    const int head = item >> 1, which = item & 1;
     const int64_t slot = blockIdx.x;
     const int b = iqq::seq_of_slot(C, slot, 1, page, 2);
     const Span s = iqq::span_of(C, b);
@@ -42,45 +48,43 @@ append_kernel(const Kv8 C, const New N, uint32_t* __restrict__ flags)
     const int64_t index = (s.start >> C.page_log2) + j, t0 = index << C.page_log2;
     if (s.n == 0 || t0 >= s.len) return;
     const int p = t0 < C.capacity ? iqq::page_at(C, b, index) : -1;
-    if (p < 0) {
-        if (tid == 0 && head == 0 && which == 0) iqq::raise_flags(flags, IQQ_FLAG_BAD_INDEX);
-        return;
-    }
     // tokens lo .. hi-1 of the page are new
     const int lo = s.start > t0 ? static_cast<int>(s.start - t0) : 0;
     const int hi = s.len - t0 < page ? static_cast<int>(s.len - t0) : page;
     const int64_t row0 = s.first + (t0 + lo - s.start);
-    const T* x = static_cast<const T*>(N.p[which]) + row0 * N.token_stride[which] + head * N.head_stride[which];
     const int64_t ts = N.token_stride[which];
+    const T* x = static_cast<const T*>(N.p[which]) + row0 * ts + head * N.head_stride[which];
     const int units = (hi - lo) * kRow;
+    const auto at = [&](int u) { return x + (u / kRow) * ts + (u % kRow) * 8; };
 
-    float v[kUnits][8];
+    typename iqq::Raw<T>::type v[kUnits];
     uint32_t m = 0u;
-    auto amax = [&](const float(&t)[8]) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(t[i]) & 0x7fffffffu);
-    };
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
-        const int u = tid + k * kThreads;
-        if (u < units) {
-            iqq::load8(x + (u / kRow) * ts + (u % kRow) * 8, v[k]);
-            amax(v[k]);
-        }
+        v[k] = {};
+        if (tid + k * G < units) iqq::fetch(at(tid + k * G), v[k]);
     }
-    for (int u = tid + kUnits * kThreads; u < units; u += kThreads) {
-        float t[8];
-        iqq::load8(x + (u / kRow) * ts + (u % kRow) * 8, t);
-        amax(t);
+    if (p < 0) {
+        if (tid == 0) iqq::raise_flags(flags, IQQ_FLAG_BAD_INDEX);
+        return;
     }
     float* scale = C.scales[which] + static_cast<int64_t>(p) * C.heads + head;
     const float held = lo > 0 ? *scale : 0.0f;
-    m = __reduce_max_sync(0xffffffffu, m);
-    if ((tid & 31) == 0) part[tid >> 5] = m;
-    __syncthreads();  // every thread has read the old scale, too
-    m = 0u;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) m = max(m, part[i]);
+    for (int k = 0; k < kUnits; ++k) m = iqq::amax8(x, v[k], m);
+    for (int u = tid + kUnits * G; u < units; u += G) {
+        typename iqq::Raw<T>::type t;
+        iqq::fetch(at(u), t);
+        m = iqq::amax8(x, t, m);
+    }
+    m = __reduce_max_sync(0xffffffffu, iqq::amax_bits(x, m));
+    if constexpr (G > 32) {
+        if (lane == 0) part[threadIdx.x >> 5] = m;
+        __syncthreads();  // every thread has read the old scale, too
+        m = __reduce_max_sync(0xffffffffu, part[lane % (G / 32)]);
+    } else {
+        __syncwarp();
+    }
     const float need = iqq::i8_scale(m);
     const float d = need != need || held != held ? __uint_as_float(0x7fc00000u) : fmaxf(held, need);
     const float inv = d > 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
@@ -88,32 +92,33 @@ append_kernel(const Kv8 C, const New N, uint32_t* __restrict__ flags)
         *scale = d;
         if (m >= iqq::kInfBits) iqq::raise_flags(flags, IQQ_FLAG_NONFINITE_INPUT);
     }
-    int8_t* tile = C.codes[which] + ((static_cast<int64_t>(p) * C.heads + head) << C.page_log2) * D;
-    auto store = [&](int u, const float(&t)[8]) {
-        *reinterpret_cast<uint2*>(tile + lo * D + u * 8) = d > 0.0f ? iqq::codes8(t, d, inv) : make_uint2(0u, 0u);
+    uint2* tile = reinterpret_cast<uint2*>(C.codes[which] + ((static_cast<int64_t>(p) * C.heads + head) << C.page_log2) * D);
+    const auto store = [&](int u, const typename iqq::Raw<T>::type& r) {
+        float t[8];
+        iqq::widen(x, r, t);
+        tile[lo * kRow + u] = d > 0.0f ? iqq::codes8(t, d, inv) : make_uint2(0u, 0u);
     };
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-        const int u = tid + k * kThreads;
-        if (u < units) store(u, v[k]);
-    }
-    for (int u = tid + kUnits * kThreads; u < units; u += kThreads) {
-        float t[8];
-        iqq::load8(x + (u / kRow) * ts + (u % kRow) * 8, t);
+    for (int k = 0; k < kUnits; ++k)
+        if (tid + k * G < units) store(tid + k * G, v[k]);
+    for (int u = tid + kUnits * G; u < units; u += G) {
+        typename iqq::Raw<T>::type t;
+        iqq::fetch(at(u), t);
         store(u, t);
     }
     if (d > held) {  // the tokens already in the page, to the new scale
         const float ratio = held * inv;
-        for (int u = tid; u < lo * kRow; u += kThreads) {
-            uint2* at = reinterpret_cast<uint2*>(tile + u * 8);
-            const uint2 w = *at;
-            int q[8];
+#pragma unroll 4
+        for (int u = tid; u < lo * kRow; u += G) {
+            const uint2 w = tile[u];
+            int c[8];
+            float t[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int c = static_cast<int8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
-                q[i] = iqq::rint_code(held, c, d, ratio * static_cast<float>(c));
+                c[i] = static_cast<int8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+                t[i] = static_cast<float>(c[i]);
             }
-            *at = make_uint2(iqq::pack4(q[0], q[1], q[2], q[3]), iqq::pack4(q[4], q[5], q[6], q[7]));
+            tile[u] = iqq::codes8(t, ratio, [&](int i, float q) { return iqq::exact_code(held, c[i], d, q); });
         }
     }
 }
@@ -155,6 +160,7 @@ gather_kernel(const Kv8 C, T* __restrict__ ko, T* __restrict__ vo, uint32_t* __r
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         T* out = (which == 0 ? ko : vo) + row * units * 8;
+#pragma unroll 4
         for (int u = lane; u < units; u += 32) {
             const int h = u / kRow;
             float t[8] = {};
@@ -173,11 +179,11 @@ gather_kernel(const Kv8 C, T* __restrict__ ko, T* __restrict__ vo, uint32_t* __r
 }
 
 template <class K, class... A>
-iqq_status launch(K kernel, dim3 grid, cudaStream_t st, A... args)
+iqq_status launch(K kernel, dim3 grid, int threads, cudaStream_t st, A... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -251,14 +257,25 @@ extern "C" iqq_status iqq_kv8_append(const iqq_kv8_cache* cache, const iqq_kv8_s
     const New N = {{k, v}, {k_token_stride, v_token_stride}, {k_head_stride, v_head_stride}};
     // n tokens reach at most floor(n / page) + 2 pages of a sequence
     const int64_t slots = n_tokens / cache->page_size + 2LL * C.n_seqs;
-    const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(C.heads), 2);
+    // A warp a page and head while a sequence has up to four new tokens (96 sequences of one token, 8
+    // heads: 4.6 us; with a CTA of 256 threads each it took 27), else a CTA.
+    const bool few = n_tokens <= 4LL * C.n_seqs;
+    const int64_t items = 2LL * C.heads, held = few ? kAppendThreads / 32 : 1, groups = (items + held - 1) / held;
+    if (slots > 0x7fffffffLL || groups > 65535) return IQQ_ERR_SHAPE;
+    const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(groups));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool wide = cache->head_dim == 128;
+    const auto go = [&](auto zero) -> iqq_status {
+        using T = decltype(zero);
+        if (cache->head_dim == 128)
+            return few ? launch(append_kernel<T, 128, 32>, grid, kAppendThreads, st, C, N, d_flags)
+                       : launch(append_kernel<T, 128, kAppendThreads>, grid, kAppendThreads, st, C, N, d_flags);
+        return few ? launch(append_kernel<T, 64, 32>, grid, kAppendThreads, st, C, N, d_flags)
+                   : launch(append_kernel<T, 64, kAppendThreads>, grid, kAppendThreads, st, C, N, d_flags);
+    };
     switch (dtype) {
-    case IQQ_F32: return launch(wide ? append_kernel<float, 128> : append_kernel<float, 64>, grid, st, C, N, d_flags);
-    case IQQ_BF16:
-        return launch(wide ? append_kernel<__nv_bfloat16, 128> : append_kernel<__nv_bfloat16, 64>, grid, st, C, N, d_flags);
-    default: return launch(wide ? append_kernel<__half, 128> : append_kernel<__half, 64>, grid, st, C, N, d_flags);
+    case IQQ_F32: return go(float{});
+    case IQQ_BF16: return go(__nv_bfloat16{});
+    default: return go(__half{});
     }
 }
 
@@ -277,7 +294,7 @@ extern "C" iqq_status iqq_kv8_gather(const iqq_kv8_cache* cache, const iqq_kv8_s
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     auto go = [&](auto* k, auto* v) -> iqq_status {
         using T = std::remove_pointer_t<decltype(k)>;
-        return launch(cache->head_dim == 128 ? gather_kernel<T, 128> : gather_kernel<T, 64>, grid, st, C, k, v, d_flags);
+        return launch(cache->head_dim == 128 ? gather_kernel<T, 128> : gather_kernel<T, 64>, grid, kThreads, st, C, k, v, d_flags);
     };
     switch (dtype) {
     case IQQ_F32: return go(static_cast<float*>(k_out), static_cast<float*>(v_out));
