@@ -90,6 +90,10 @@ struct Attend {
     int64_t q_token_stride, q_head_stride;
     int32_t heads, group;
     float scale;
+    // Parts of rows, where the keys of a row are split over CTAs: normalized outputs, log-sums (base 2).
+    int32_t splits;
+    float* part;
+    float* part_lse;
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -122,7 +126,11 @@ __device__ __forceinline__ int row_exponent(float top)
 }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
-// Many rows a sequence (kv8_prompt.cu).
+// Many rows a sequence (kv8_prompt.cu): how many CTAs share the keys of 256 rows, the workspace's bytes
+// (0 for one), and the launch.
+int prompt_splits(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int64_t n_heads, int64_t n_tokens);
+size_t prompt_part_bytes(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int64_t n_heads, int64_t n_tokens,
+                         int splits, size_t* lse_bytes);
 iqq_status launch_prompt(const iqq_kv8_cache* cache, const Kv8& C, const Attend& A, int dtype, uint32_t* flags,
                          cudaStream_t st);
 

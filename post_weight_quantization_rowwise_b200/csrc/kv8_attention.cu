@@ -49,9 +49,7 @@ constexpr int kKeys = 128;                  // keys of a stage: 32 a warp
 constexpr int kMaxCtas = 1024;
 
 struct Args : iqq::Attend {
-    struct Mark* marks;  // [gridDim.x]
-    float* part;         // [gridDim.x][2][row tile][head_dim], then the log-sums [..][2][row tile]
-    float* part_lse;
+    struct Mark* marks;  // [gridDim.x]; parts are [gridDim.x][2][row tile][head_dim], log-sums [..][2][row tile]
 };
 
 // The launch's stages in equal shares: `each`, and one more for the first `more` CTAs.
@@ -782,6 +780,7 @@ constexpr int64_t kPromptRows = 64;
 
 struct Plan {
     bool prompt;
+    int splits;       // of the prompt kernel
     int row_tile;     // rows a CTA
     int64_t ctas;     // shares
     size_t marks, part, lse;  // bytes of the workspace's parts
@@ -796,7 +795,11 @@ Plan plan_of(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int64_t n_hea
     const int64_t group = n_heads / cache->n_kv_heads;
     const int64_t each = (n_tokens + seqs->n_seqs - 1) / seqs->n_seqs * group;
     p.prompt = each >= kPromptRows;
-    if (p.prompt) return p;
+    if (p.prompt) {
+        p.splits = iqq::prompt_splits(cache, seqs, n_heads, n_tokens);
+        p.part = iqq::prompt_part_bytes(cache, seqs, n_heads, n_tokens, p.splits, &p.lse);
+        return p;
+    }
     p.row_tile = each <= 8 ? 8 : 16;
     const int64_t tiles = (n_tokens * group / p.row_tile + seqs->n_seqs) * cache->n_kv_heads;
     const int64_t stages = 1 + (seqs->table_width * cache->page_size + kKeys - 1) / kKeys;
@@ -896,6 +899,7 @@ extern "C" iqq_status iqq_kv8_attention(const iqq_kv8_cache* cache, const iqq_kv
     A.group = static_cast<int32_t>(n_heads / C.heads);
     A.scale = scale;
     char* ws = static_cast<char*>(workspace);
+    A.splits = p.splits;
     A.marks = reinterpret_cast<Mark*>(ws);
     A.part = reinterpret_cast<float*>(ws + p.marks);
     A.part_lse = reinterpret_cast<float*>(ws + p.marks + p.part);

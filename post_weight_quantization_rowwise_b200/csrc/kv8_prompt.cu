@@ -17,6 +17,8 @@
 // rescaled.  Bound by the tensor cores and, as nearly, by the exponentials (16 an SM and clock).
 #include <math.h>
 
+#include <algorithm>
+
 #include "kv8.cuh"
 #include "sm100.cuh"
 
@@ -96,7 +98,10 @@ struct Work {
     int32_t b, head, row0, rows;  // sequence, key/value head, first row, rows of the sequence
     int64_t start, len;           // position of the sequence's first token here, its keys
     int32_t first;                // its first packed row
-    int32_t tiles[kTiles];        // key tiles that the row tile sees
+    int32_t tile0;                // the first key tile of this CTA's part
+    int64_t part;                 // where its rows' parts go
+    int32_t tiles[kTiles];        // key tiles of the part that the row tile sees
+    __device__ __forceinline__ int key_tiles() const { return max(tiles[0], tiles[1]); }
     __device__ __forceinline__ int64_t sees(int row, int group) const { return min(len, start + row / group + 1); }
 };
 
@@ -110,7 +115,7 @@ __device__ __forceinline__ bool load(Smem<D>& S, const Kv8& C, const Work& W, in
     const int lane = threadIdx.x & 31;
     const int piece = min(kKeys, 1 << C.page_log2), per = kKeys / piece, batch = 32 / per;
     const auto page_of = [&](int j) {
-        const int64_t key = static_cast<int64_t>(j) * kKeys + lane * piece;
+        const int64_t key = (static_cast<int64_t>(W.tile0) + j) * kKeys + lane * piece;
         return key < end ? iqq::page_at(C, W.b, key >> C.page_log2) : -2;
     };
     bool ok = true;
@@ -142,7 +147,7 @@ __device__ __forceinline__ bool load(Smem<D>& S, const Kv8& C, const Work& W, in
                 }
                 __syncwarp();
                 if (my) {
-                    const int64_t key = static_cast<int64_t>(j) * kKeys + u * piece;
+                    const int64_t key = (static_cast<int64_t>(W.tile0) + j) * kKeys + u * piece;
                     iqq::bulk_load(iqq::smem_u32(S.raw[which]) + u * piece * D,
                                    C.codes[which] + ((cell << C.page_log2) + (key & ((1 << C.page_log2) - 1))) * D, piece * D, bar);
                     if (which == 0)
@@ -246,7 +251,7 @@ __device__ __forceinline__ bool multiply(Smem<D>& S, const Work& W, uint32_t tme
         }
         iqq::tc_commit<1>(iqq::smem_u32(&S.sfull[t]));
     };
-    const int n = max(W.tiles[0], W.tiles[1]);
+    const int n = W.key_tiles();
     for (int t = 0; t < kTiles; ++t) {
         if (W.tiles[t] == 0) continue;
         if (!iqq::bar_wait(iqq::smem_u32(&S.qfull[t]), 0)) return false;
@@ -355,8 +360,11 @@ __device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& 
     const int token = row / A.group;
     const int64_t at = static_cast<int64_t>(W.first + token) * A.heads + W.head * A.group + row - token * A.group;
     const int n = W.tiles[t];
+    const int64_t part = W.part + t * kRows + r;
     if (n == 0) {  // nothing to see: zeros
-        if (real) {
+        if (real && A.splits > 1) {
+            A.part_lse[part] = -INFINITY;
+        } else if (real) {
             uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(A.out) + at * D);
             for (int i = 0; i < D / 8; ++i) out[i] = make_uint4(0, 0, 0, 0);
             if (A.lse != nullptr) A.lse[at] = -INFINITY;
@@ -402,8 +410,9 @@ __device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& 
         late |= !iqq::bar_wait(iqq::smem_u32(&S.sfull[t]), j & 1);
         if (__any_sync(0xffffffffu, late)) return false;
         iqq::tc_fence_after();
-        const bool masked = clear64 < static_cast<int64_t>(j + 1) * kKeys;
-        const int limit = static_cast<int>(max(int64_t{0}, min(limit64 - static_cast<int64_t>(j) * kKeys, int64_t{kKeys})));
+        const int64_t first_key = (static_cast<int64_t>(W.tile0) + j) * kKeys;
+        const bool masked = clear64 < first_key + kKeys;
+        const int limit = static_cast<int>(max(int64_t{0}, min(limit64 - first_key, int64_t{kKeys})));
         // One pass with the maximum as it is; where a weight came out above 2^8 (rare after the first
         // tiles), or a row has seen nothing yet, the maximum is taken and the weights anew.
         uint32_t p[kKeys / 32][16];
@@ -451,7 +460,13 @@ __device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& 
         uint32_t x[32];
         iqq::tmem_ld32(o_at + 32 * i, x);
         iqq::tmem_wait_ld(x);
-        if (real) {
+        if (real && A.splits > 1) {
+            float4* out = reinterpret_cast<float4*>(A.part + part * D + 32 * i);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                out[e] = make_float4(__uint_as_float(x[4 * e]) * inv, __uint_as_float(x[4 * e + 1]) * inv,
+                                     __uint_as_float(x[4 * e + 2]) * inv, __uint_as_float(x[4 * e + 3]) * inv);
+        } else if (real) {
             __align__(16) T v[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = iqq::from_f32<T>(none ? 0.0f : __uint_as_float(x[e]) * inv);
@@ -460,7 +475,9 @@ __device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& 
             for (int e = 0; e < 4; ++e) out[e] = reinterpret_cast<const uint4*>(v)[e];
         }
     }
-    if (real && A.lse != nullptr) A.lse[at] = none ? -INFINITY : (m + log2f(l)) / kLog2e;
+    const float lse = none ? -INFINITY : m + log2f(l);
+    if (real && A.splits > 1) A.part_lse[part] = lse;
+    else if (real && A.lse != nullptr) A.lse[at] = lse / kLog2e;
     return true;
 }
 
@@ -475,10 +492,11 @@ prompt_kernel(const Kv8 C, const Attend A, uint32_t* __restrict__ flags)
     iqq::check_spans(C, false, flags);
 
     // later slots first, in all heads: the last rows of a sequence see the most keys
-    const int64_t slot = (gridDim.x - 1 - blockIdx.x) / static_cast<uint32_t>(C.heads);
+    const uint32_t split = blockIdx.x % static_cast<uint32_t>(A.splits), item = (gridDim.x - 1 - blockIdx.x) / static_cast<uint32_t>(A.splits);
+    const int64_t slot = item / static_cast<uint32_t>(C.heads);
     Work W;
     W.b = iqq::seq_of_slot(C, slot, A.group, kTiles * kRows, 1);
-    W.head = static_cast<int32_t>(blockIdx.x % static_cast<uint32_t>(C.heads));
+    W.head = static_cast<int32_t>(item % static_cast<uint32_t>(C.heads));
     const Span s = iqq::span_of(C, W.b);
     const int64_t row0 = (slot - iqq::slot_base(C, W.b, A.group, kTiles * kRows, 1)) * (kTiles * kRows);
     W.rows = s.n * A.group;  // 0 for a bad span
@@ -487,6 +505,7 @@ prompt_kernel(const Kv8 C, const Attend A, uint32_t* __restrict__ flags)
     W.first = s.first;
     W.start = s.start;
     W.len = s.len < C.capacity ? s.len : C.capacity;
+    W.part = (static_cast<int64_t>(item) * A.splits + split) * (kTiles * kRows);
     int64_t end = 0;  // keys that some row sees
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
@@ -494,6 +513,12 @@ prompt_kernel(const Kv8 C, const Attend A, uint32_t* __restrict__ flags)
         const int64_t sees = first < W.rows ? max(int64_t{0}, W.sees(last, A.group)) : 0;
         W.tiles[t] = static_cast<int32_t>((sees + kKeys - 1) / kKeys);
         end = max(end, sees);
+    }
+    {  // this CTA's part of the key tiles
+        const int n = W.key_tiles(), to = static_cast<int>(static_cast<int64_t>(n) * (split + 1) / A.splits);
+        W.tile0 = static_cast<int32_t>(static_cast<int64_t>(n) * split / A.splits);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) W.tiles[t] = max(0, min(W.tiles[t], to) - W.tile0);
     }
 
     if (threadIdx.x == 0) {
@@ -530,11 +555,11 @@ prompt_kernel(const Kv8 C, const Attend A, uint32_t* __restrict__ flags)
         ok = attend<T, D>(S, A, W, tmem, warp >> 2);
     } else if (warp < kMma) {
         fewer_registers<kMakerRegs>();
-        ok = make_operands<D>(S, max(W.tiles[0], W.tiles[1]));
+        ok = make_operands<D>(S, W.key_tiles());
     } else {
         fewer_registers<kOtherRegs>();
         if (warp == kLoader) {
-            ok = load<D>(S, C, W, max(W.tiles[0], W.tiles[1]), end, flags);
+            ok = load<D>(S, C, W, W.key_tiles(), end, flags);
         } else if (threadIdx.x == 32 * kMma) {
             ok = multiply<D>(S, W, tmem);
             // nothing is left running when the tensor memory goes
@@ -550,13 +575,72 @@ prompt_kernel(const Kv8 C, const Attend A, uint32_t* __restrict__ flags)
     if (warp == kMma) iqq::tmem_free<1>(tmem, 512);
 }
 
+// Joins a row's parts: a warp a row.
+template <class T, int D>
+__global__ void __launch_bounds__(256)
+join_kernel(const Kv8 C, const Attend A)
+{
+    constexpr int kE = D / 32;
+    const int lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t item = id / (kTiles * kRows), slot = item / C.heads;
+    const int r = static_cast<int>(id % (kTiles * kRows)), head = static_cast<int>(item % C.heads);
+    const int b = iqq::seq_of_slot(C, slot, A.group, kTiles * kRows, 1);
+    const Span s = iqq::span_of(C, b);
+    const int64_t row = (slot - iqq::slot_base(C, b, A.group, kTiles * kRows, 1)) * (kTiles * kRows) + r;
+    if (row >= static_cast<int64_t>(s.n) * A.group) return;
+    const int64_t part = item * A.splits * (kTiles * kRows) + r;
+    float m = kNone, l = 0.0f, o[kE] = {};
+#pragma unroll 4
+    for (int p = 0; p < A.splits; ++p) {
+        const int64_t at = part + static_cast<int64_t>(p) * (kTiles * kRows);
+        const float x = A.part_lse[at];
+        float v[kE];
+#pragma unroll
+        for (int e = 0; e < kE; ++e) v[e] = A.part[at * D + lane * kE + e];
+        if (x == -INFINITY) continue;  // (its values may be anything)
+        const float top = fmaxf(m, x), keep = ex2(m - top), w = ex2(x - top);  // (a NaN part makes everything NaN)
+        m = top;
+        l = fmaf(l, keep, w);
+#pragma unroll
+        for (int e = 0; e < kE; ++e) o[e] = fmaf(o[e], keep, w * v[e]);
+    }
+    const bool none = m == kNone && l == 0.0f;
+    const int64_t token = row / A.group, at = (s.first + token) * A.heads + head * A.group + row - token * A.group;
+#pragma unroll
+    for (int e = 0; e < kE; ++e)
+        static_cast<T*>(A.out)[at * D + lane * kE + e] = iqq::from_f32<T>(none ? 0.0f : __fdiv_rn(o[e], l));
+    if (A.lse != nullptr && lane == 0) A.lse[at] = none ? -INFINITY : (m + log2f(l)) / kLog2e;
+}
+
+int64_t slots_of(int64_t n_tokens, int64_t group, int64_t n_seqs) { return n_tokens * group / (kTiles * kRows) + n_seqs; }
+
+template <class... P, class... A>
+iqq_status start(void (*kernel)(P...), int64_t grid, int threads, size_t smem, cudaStream_t st, const A&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, kernel, args...);
+    return iqq::launch_status();
+}
+
 template <class T, int D>
 iqq_status launch(const Kv8& C, const Attend& A, uint32_t* flags, cudaStream_t st)
 {
     static std::atomic<uint64_t> done{0};
     constexpr size_t smem = 226 * 1024;  // the whole SM's: it takes the whole tensor memory
     static_assert(sizeof(Smem<D>) <= smem, "shared memory");
-    const iqq_status s = iqq::opt_in_smem(reinterpret_cast<const void*>(prompt_kernel<T, D>), smem, done);
+    iqq_status s = iqq::opt_in_smem(reinterpret_cast<const void*>(prompt_kernel<T, D>), smem, done);
     if (s != IQQ_OK) return s;
     // The warps' shares have to fit what the launch gives, or they would wait for registers for good.
     static const int regs = [] {
@@ -567,23 +651,34 @@ iqq_status launch(const Kv8& C, const Attend& A, uint32_t* flags, cudaStream_t s
         iqq::set_last_cuda_error(cudaErrorLaunchOutOfResources);
         return IQQ_ERR_CUDA;
     }
-    const int64_t slots = static_cast<int64_t>(C.n_tokens) * A.group / (kTiles * kRows) + C.n_seqs;
-    cudaLaunchConfig_t cfg = {};
-    if (slots * C.heads > 0x7fffffffLL) return IQQ_ERR_SHAPE;
-    cfg.gridDim = dim3(static_cast<unsigned>(slots * C.heads));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, prompt_kernel<T, D>, C, A, flags);
-    return iqq::launch_status();
+    const int64_t items = slots_of(C.n_tokens, A.group, C.n_seqs) * C.heads;
+    if (items * A.splits > 0x7fffffffLL || items * kTiles * kRows / 8 > 0x7fffffffLL) return IQQ_ERR_SHAPE;
+    s = start(prompt_kernel<T, D>, items * A.splits, kThreads, smem, st, C, A, flags);
+    if (s != IQQ_OK || A.splits == 1) return s;
+    return start(join_kernel<T, D>, items * kTiles * kRows / 8, 256, 0, st, C, A);
 }
 
 }  // namespace
+
+// The keys of 256 rows are split while the row tiles alone leave SMs idle and a part keeps at least four
+// key tiles (50 tokens of 8 heads over one head of 64 dimensions, 100000 keys: two CTAs took 1650 us).
+int iqq::prompt_splits(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int64_t n_heads, int64_t n_tokens)
+{
+    const int64_t group = n_heads / cache->n_kv_heads, items = slots_of(n_tokens, group, seqs->n_seqs) * cache->n_kv_heads;
+    const int64_t most = seqs->table_width * cache->page_size / (4 * kKeys);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sm_count() / items, most, 128})));
+}
+
+size_t iqq::prompt_part_bytes(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int64_t n_heads, int64_t n_tokens,
+                              int splits, size_t* lse_bytes)
+{
+    *lse_bytes = 0;
+    if (splits == 1) return 0;
+    const int64_t group = n_heads / cache->n_kv_heads;
+    const size_t rows = static_cast<size_t>(slots_of(n_tokens, group, seqs->n_seqs) * cache->n_kv_heads) * splits * kTiles * kRows;
+    *lse_bytes = rows * sizeof(float);
+    return rows * cache->head_dim * sizeof(float);
+}
 
 iqq_status iqq::launch_prompt(const iqq_kv8_cache* cache, const Kv8& C, const Attend& A, int dtype, uint32_t* flags,
                               cudaStream_t st)

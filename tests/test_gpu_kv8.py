@@ -253,7 +253,9 @@ def test_attention_ragged_chunks(iqq, dtype, page, dim, kv, group):
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("lens,new,kv,group", [([9000], [1], 1, 4), ([40000], [1], 2, 8), ([5000, 3, 8111], [1, 1, 1], 1, 2),
-                                               ([3000], [1500], 1, 2), ([6100], [17], 2, 4)])
+                                               ([3000], [1500], 1, 2), ([6100], [17], 2, 4),
+                                               ([30000], [60], 1, 8), ([20000, 700, 70], [100, 64, 70], 1, 1),
+                                               ([9000, 0, 5], [200, 3, 9], 2, 4)])
 def test_attention_long(iqq, dtype, lens, new, kv, group):
     c = Case(iqq, lens, kv, 128, 64, 17)
     _check_attention(iqq, c, new, kv * group, dtype)
