@@ -711,39 +711,55 @@ def quantize_i8_rows(x, flags=None, stream=None):
     """Allocates and returns (codes, scales) of x: int8 [nrows, n], rows padded to a multiple of
     16 bytes in memory, and float32 [nrows]."""
     import torch
-    nrows, n = _shape2(x)
-    codes = _empty((nrows, (n + 15) // 16 * 16), torch.int8, x.device, stream)
-    if codes.shape[1] != n:
-        codes = codes[:, :n]
+    index = _device_index("x", x)
+    nrows, n, ldx = _rows("x", x, None, index)
+    code = _dtype_code("x", x.dtype)
+    _need_vector("flags", flags, 1, torch.int32, index)
+    pitch = (n + 15) // 16 * 16
+    codes = _empty((nrows, pitch), torch.int8, x.device, stream)
     scales = _empty((nrows,), torch.float32, x.device, stream)
-    return iqq_quantize_i8_rows(x, codes, scales, flags, stream)
+    _launch("iqq_quantize_i8_rows", index, stream, code, x.data_ptr(), ldx, codes.data_ptr(), pitch,
+            scales.data_ptr(), nrows, n, _at(flags))
+    return codes if pitch == n else codes[:, :n], scales
 
 
-def iqq_gemm_i8(a_codes, a_scales, w_codes, w_scales, y, bias=None, flags=None, stream=None):
-    """y [n_tok, n_out] (float32, bfloat16 or float16) = a_codes [n_tok, k] @ w_codes [n_out, k].T,
-    scaled by a_scales [n_tok] and w_scales [n_out], plus bias [n_out] (float32)."""
+def _gemm_i8(a_codes, a_scales, w_codes, w_scales, y, dtype, bias, flags, stream):
     import torch
     index = _device_index("a_codes", a_codes)
     n_tok, k, lda = _rows("a_codes", a_codes, torch.int8, index)
     n_out, kw, ldw = _rows("w_codes", w_codes, torch.int8, index)
-    ytok, yout, ldy = _rows("y", y, None, index)
-    code = _dtype_code("y", y.dtype)
-    if kw != k or ytok != n_tok or yout != n_out:
-        raise ValueError(f"a_codes {(n_tok, k)}, w_codes {(n_out, kw)} and y {(ytok, yout)} do not fit")
+    if kw != k:
+        raise ValueError(f"a_codes {(n_tok, k)} and w_codes {(n_out, kw)} do not fit")
     _need_vector("a_scales", a_scales, n_tok, torch.float32, index)
     _need_vector("w_scales", w_scales, n_out, torch.float32, index)
     _need_vector("bias", bias, n_out, torch.float32, index)
     _need_vector("flags", flags, 1, torch.int32, index)
+    if y is None:
+        code = _dtype_code("y", dtype)
+        y = _empty((n_tok, n_out), dtype, a_codes.device, stream)
+        ldy = n_out
+    else:
+        ytok, yout, ldy = _rows("y", y, None, index)
+        code = _dtype_code("y", y.dtype)
+        if ytok != n_tok or yout != n_out:
+            raise ValueError(f"y must be {(n_tok, n_out)}, got {(ytok, yout)}")
     _launch("iqq_gemm_i8", index, stream, a_codes.data_ptr(), lda, a_scales.data_ptr(), w_codes.data_ptr(), ldw,
             w_scales.data_ptr(), _at(bias), code, y.data_ptr(), ldy, n_tok, n_out, k, _at(flags))
     return y
 
 
+def iqq_gemm_i8(a_codes, a_scales, w_codes, w_scales, y, bias=None, flags=None, stream=None):
+    """y [n_tok, n_out] (float32, bfloat16 or float16) = a_codes [n_tok, k] @ w_codes [n_out, k].T,
+    scaled by a_scales [n_tok] and w_scales [n_out], plus bias [n_out] (float32)."""
+    if y is None:
+        raise ValueError("y is required")
+    return _gemm_i8(a_codes, a_scales, w_codes, w_scales, y, None, bias, flags, stream)
+
+
 def gemm_i8(a_codes, a_scales, w_codes, w_scales, bias=None, dtype=None, flags=None, stream=None):
     """Allocates and returns y [n_tok, n_out] of iqq_gemm_i8 (dtype None: float32)."""
     import torch
-    y = _empty((a_codes.shape[0], w_codes.shape[0]), dtype or torch.float32, a_codes.device, stream)
-    return iqq_gemm_i8(a_codes, a_scales, w_codes, w_scales, y, bias, flags, stream)
+    return _gemm_i8(a_codes, a_scales, w_codes, w_scales, None, dtype or torch.float32, bias, flags, stream)
 
 
 # ----------------------------------------------------------------------------
@@ -859,8 +875,9 @@ def kv8_gather(cache, block_tables, seq_lens, cu_tokens, n_tokens: int, dtype=No
     """Allocates and returns (k, v) of iqq_kv8_gather; n_tokens is cu_tokens' last value (rows that
     belong to no sequence are unspecified); dtype None: float32."""
     import torch
-    k, v = _empty((2, n_tokens, cache.n_kv_heads, cache.head_dim), dtype or torch.float32, cache.device,
-                  stream).unbind(0)
+    shape = (n_tokens, cache.n_kv_heads, cache.head_dim)
+    k = _empty(shape, dtype or torch.float32, cache.device, stream)
+    v = _empty(shape, dtype or torch.float32, cache.device, stream)
     return iqq_kv8_gather(cache, block_tables, seq_lens, cu_tokens, k, v, flags, stream)
 
 
