@@ -515,11 +515,10 @@ extern "C" iqq_status iqq_gemm_i8(const int8_t* a, int64_t lda, const float* a_s
     if (n_tok < 0 || n_out < 0 || k < 0 || k > IQQ_GEMM_I8_MAX_K) return IQQ_ERR_SHAPE;
     if (n_tok == 0 || n_out == 0) return IQQ_OK;
     const int64_t pitch = (k + 15) / 16 * 16;
-    if (n_tok == 1) {
-        lda = pitch;
-        ldy = n_out;
-    }
-    if (n_out == 1) ldw = pitch;
+    // the distance of rows is not looked at where there is one row, or nothing in them
+    if (n_tok == 1 || k == 0) lda = pitch;
+    if (n_tok == 1) ldy = n_out;
+    if (n_out == 1 || k == 0) ldw = pitch;
     constexpr int64_t kMost = 0x7fffffff - 1024, kFar = (1LL << 40) - 16;  // a tile's coordinates and pitch
     if (lda < k || ldw < k || ldy < n_out || n_tok > kMost || n_out > kMost || lda > kFar || ldw > kFar ||
         !iqq::size_ok(n_tok, lda > 0 ? lda : 1, 1) || !iqq::size_ok(n_out, ldw > 0 ? ldw : 1, 1) ||

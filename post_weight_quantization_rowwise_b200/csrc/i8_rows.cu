@@ -174,7 +174,14 @@ extern "C" iqq_status iqq_quantize_i8_rows(int dtype, const void* x, int64_t ldx
 {
     if (!iqq::dtype_ok(dtype)) return IQQ_ERR_ARG;
     if (!iqq::size_ok(nrows, n, 4)) return IQQ_ERR_SHAPE;
-    if (nrows == 0 || n == 0) return IQQ_OK;
+    if (nrows == 0) return IQQ_OK;
+    if (n == 0) {
+        if (!iqq::aligned(scales, 4)) return IQQ_ERR_ALIGN;
+        if (scales != nullptr &&
+            cudaMemsetAsync(scales, 0, static_cast<size_t>(nrows) * sizeof(float), static_cast<cudaStream_t>(stream)) != cudaSuccess)
+            return iqq::launch_status();
+        return IQQ_OK;
+    }
     if (nrows == 1) {
         ldx = (n + 15) / 16 * 16;
         ldc = ldx;

@@ -156,6 +156,15 @@ def test_gemm_leaves_the_rest_of_y(iqq, n_tok, n_out):
         assert (rest == 7.0).all()
 
 
+def test_rows_of_no_values(iqq):
+    """Rows of length 0 have the scale 0, and their product is the bias."""
+    a, da = iqq.quantize_i8_rows(torch.empty(3, 0, device="cuda"))
+    w, dw = iqq.quantize_i8_rows(torch.empty(40, 0, device="cuda"))
+    bias = torch.arange(40.0, device="cuda")
+    assert (da == 0).all() and a.shape == (3, 0)
+    assert torch.equal(iqq.gemm_i8(a, da, w, dw, bias=bias), bias.expand(3, 40))
+
+
 def test_gemm_empty_sum_and_nan_scale(iqq):
     a, w = _codes(3, 16, 1)[:, :0], _codes(40, 16, 2)[:, :0]
     one, bias = torch.ones(40, device="cuda"), torch.arange(40.0, device="cuda")
