@@ -1,7 +1,8 @@
 /*
  * iqq.h -- C ABI of the B200 (sm_100a) library for importance-matrix-weighted
  * Q4_0 weight quantization, Q8_K_128 activation quantization, Q4_0
- * dequantization and the round-trip weighted RMSE.
+ * dequantization and the round-trip weighted RMSE, and for 8-bit integer rows
+ * with their matrix product and a paged 8-bit key/value cache with its attention.
  *
  * Sources (page title, address, section):
  *  [W]   "ik_llama.cpp 量化权重之谜：weight[j] = qw[j] * sqrtf(sigma2 +
@@ -26,9 +27,10 @@
  *  - Data problems found on the device (NaN/Inf input, negative importance,
  *    a scale beyond binary16) are ORed as IQQ_FLAG_* bits into the optional
  *    caller-owned device word *d_flags (may be NULL).  Nothing on the device
- *    traps or asserts.  The only waits on the device are the GEMV kernel's
- *    waits for its own bulk copies: each is bounded (about 2 s), and on expiry
- *    the kernel sets IQQ_FLAG_WAIT_TIMEOUT, drains its copies and returns.
+ *    traps or asserts.  The only waits on the device are those of a kernel's
+ *    warps for its own copies, products and one another (the GEMV, the int8
+ *    product and the attention kernels): each is bounded (about 2 s), and on
+ *    expiry the kernel sets IQQ_FLAG_WAIT_TIMEOUT, drains its copies and returns.
  *  - Empty input (nrows == 0 or n_per_row == 0) is valid and enqueues
  *    nothing; pointers may then be NULL.
  *  - Layouts are row-major: element (r, j) of an [nrows, n_per_row] float
@@ -452,7 +454,7 @@ iqq_status iqq_weighted_rmse(const float* x, const void* blocks, const float* qw
  *  scales     nrows binary32 scales, 4-byte aligned.
  *  d_flags    optional; receives IQQ_FLAG_NONFINITE_INPUT.  A row that holds NaN or Inf gets
  *             d = NaN and codes 0, so every product with it is NaN; other rows are exact.
- * n == 0 with nrows > 0 is empty input: nothing is written.
+ * n == 0: every scale is 0 (scales may be NULL), so a product with such rows is its bias.
  */
 iqq_status iqq_quantize_i8_rows(int dtype, const void* x, int64_t ldx, int8_t* codes, int64_t ldc,
                                 float* scales, int64_t nrows, int64_t n, uint32_t* d_flags, void* stream);
@@ -490,7 +492,7 @@ iqq_status iqq_gemm_i8(const int8_t* a, int64_t lda, const float* a_scales, cons
  *
  *  k_codes, v_codes    int8 [n_pages][n_kv_heads][page_size][head_dim], 16-byte aligned: a
  *                      page's tokens of one head are one contiguous tile.
- *  k_scales, v_scales  binary32 [n_pages][n_kv_heads], 4-byte aligned.
+ *  k_scales, v_scales  binary32 [n_pages][n_kv_heads], 4-byte aligned, not negative.
  *  n_pages             at least 1 where a call has tokens.
  *  page_size           16, 32, 64 or 128.
  *  head_dim            64 or 128.
@@ -583,8 +585,12 @@ iqq_status iqq_kv8_gather(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, 
  *  d_flags     optional; IQQ_FLAG_BAD_INDEX (a page without a place, and tokens beyond
  *              table_width * page_size, are not attended to; the rows of a bad span are left as
  *              they are), IQQ_FLAG_WAIT_TIMEOUT.
- * Scores and sums are binary32.  A narrower view of the block tables (table_width) bounds the
- * lengths that the launch is laid out for.
+ * Scores, sums and the softmax's maximum are binary32; the weights p_j meet the codes in binary16
+ * (2^-11 of each, or 2^-31 of the largest), whatever the dtype.  A page whose scale is NaN makes the rows that see it NaN, and
+ * no others; a value scale below 2^-100 may count as 0.
+ * The launch is laid out for the average number of tokens a sequence: a batch of single tokens or
+ * drafts beside prompts is right in one call, but faster in two.  A narrower view of the block
+ * tables (table_width) bounds the lengths that are looked at, and the workspace.
  */
 size_t iqq_kv8_attention_workspace_bytes(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int64_t n_heads,
                                          int64_t n_tokens);

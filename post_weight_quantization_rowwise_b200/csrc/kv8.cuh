@@ -99,6 +99,12 @@ struct Attend {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -3.4028234663852886e38f;  // the maximum of no score: below every finite one
 
+// The weights 2^(y - m) go to the products in binary16, where a value below 2^-14 rounds by an
+// absolute 2^-25.  So the reference m is kept kLift below the largest y when it moves, and moves
+// only when a y comes kMove further: the largest weight is 2^7 to 2^15 (of 65504), and a weight
+// rounds by 2^-11 of itself or 2^-32 of the largest.
+constexpr float kLift = 7.0f, kMove = 8.0f;
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -122,7 +128,7 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi)
 // sums): the exponent of the power's reciprocal, kept where both are normal.
 __device__ __forceinline__ int row_exponent(float top)
 {
-    return max(-110, min(110, static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14));
+    return max(-126, min(126, static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14));
 }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 

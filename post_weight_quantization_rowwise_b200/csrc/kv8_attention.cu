@@ -18,7 +18,8 @@
 // that brings its largest value near 2^14 (values below 2^-38 of it round, which is beyond the
 // binary32 sums).  The weights p_j are rounded to binary16, times the page's value scale over a
 // power of two that follows the largest such scale: 2^-11 each, as fine as the output's type or
-// finer.  The running maximum moves only when a score passes it by 2^8, so a block costs one vote.
+// finer.  m is the running maximum less 7 (see kLift) and moves only when a weight passes 2^15, so
+// a block costs one vote.
 //
 // Every launch is one wave of CTAs, and each takes an equal share of the work: the stages of all
 // sequences, heads and row tiles laid end to end, in an order that every CTA works out from the
@@ -497,14 +498,14 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 top[n][h] = fmaxf(fmaxf(x[0][n][h], x[0][n][2 + h]), fmaxf(x[1][n][h], x[1][n][2 + h]));
-                moved |= top[n][h] > m[n][h] + 8.0f;
+                moved |= top[n][h] > m[n][h] + (iqq::kLift + iqq::kMove);
             }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float v = fmaxf(top[n][h], m[n][h]);
+                    float v = fmaxf(top[n][h] - iqq::kLift, m[n][h]);
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
@@ -856,7 +857,8 @@ bool shapes_ok(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int64_t n_h
 {
     return cache != nullptr && seqs != nullptr && cache->n_kv_heads >= 1 && n_heads >= 1 && n_heads <= 65535 &&
            n_heads % cache->n_kv_heads == 0 && n_tokens >= 1 && n_tokens <= 0x7fffffffLL / n_heads && seqs->n_seqs >= 1 &&
-           seqs->n_seqs <= (1LL << 24) && cache->page_size >= 1 && seqs->table_width >= 0;
+           seqs->n_seqs <= (1LL << 24) && cache->page_size >= 1 && cache->page_size <= 128 && seqs->table_width >= 0 &&
+           seqs->table_width <= 0x7fffffffLL;
 }
 
 }  // namespace

@@ -44,7 +44,7 @@ append_kernel(const Kv8 C, const New N, uint32_t* __restrict__ flags)
     const int b = iqq::seq_of_slot(C, slot, 1, page, 2);
     const Span s = iqq::span_of(C, b);
     const int64_t j = slot - iqq::slot_base(C, b, 1, page, 2);  // the sequence's j-th page reached
-    if (!s.ok || s.start < 0) return;
+    if (j < 0 || !s.ok || s.start < 0) return;  // (a slot before the first sequence's, where cu begins above 0)
     const int64_t index = (s.start >> C.page_log2) + j, t0 = index << C.page_log2;
     if (s.n == 0 || t0 >= s.len) return;
     const int p = t0 < C.capacity ? iqq::page_at(C, b, index) : -1;

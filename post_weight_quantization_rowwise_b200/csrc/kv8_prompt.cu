@@ -12,9 +12,9 @@
 //
 // The scales stay out of the operands: with f = (the row's and the page's key scale) and the page's
 // value scale vs, the thread computes y = s f + log2(vs) for 16 keys at a time, P = 2^(y - m) with
-// m the running maximum of y, in binary16 (2^-11, as fine as the output's type or finer), and the
-// denominator as sum P / vs in binary32.  m moves only when a y passes it by 8, and only then O is
-// rescaled.  Bound by the tensor cores and, as nearly, by the exponentials (16 an SM and clock).
+// m the running maximum of y less 7 (see kLift), in binary16 (2^-11, as fine as the output's type or
+// finer), and the denominator as sum P / vs in binary32.  m moves only when a P passes 2^15, and only
+// then O is rescaled.  Bound by the tensor cores and, as nearly, by the exponentials (16 an SM and clock).
 #include <math.h>
 
 #include <algorithm>
@@ -310,7 +310,7 @@ __device__ __forceinline__ float row_top(uint32_t s_at, const float* ks, const f
 }
 
 // P = 2^(y - m), as binary16 pairs; returns the row's sum of P / vs.  `over`: whether a weight is
-// above 2^8.
+// above 2^15.
 template <bool MASKED>
 __device__ __forceinline__ float row_weights(uint32_t s_at, const float* ks, const float* lv, const float* rv, float unscale,
                                              float m, int limit, uint32_t (&p)[kKeys / 32][16], bool& over)
@@ -348,7 +348,7 @@ __device__ __forceinline__ float row_weights(uint32_t s_at, const float* ks, con
         }
     }
     const uint32_t top = iqq::max_h2(most[0], most[1]);
-    over = max(top & 0xffffu, top >> 16) > 0x5c00u;  // 2^8 (the weights are not negative; a NaN was passed over)
+    over = max(top & 0xffffu, top >> 16) > 0x7800u;  // 2^15 (the weights are not negative; a NaN was passed over)
     return l;
 }
 
@@ -413,7 +413,7 @@ __device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& 
         const int64_t first_key = (static_cast<int64_t>(W.tile0) + j) * kKeys;
         const bool masked = clear64 < first_key + kKeys;
         const int limit = static_cast<int>(max(int64_t{0}, min(limit64 - first_key, int64_t{kKeys})));
-        // One pass with the maximum as it is; where a weight came out above 2^8 (rare after the first
+        // One pass with the maximum as it is; where a weight came out above 2^15 (rare after the first
         // tiles), or a row has seen nothing yet, the maximum is taken and the weights anew.
         uint32_t p[kKeys / 32][16];
         const float *ks = S.ks[c], *lv = S.lv[c], *rv = S.rv[c];
@@ -423,7 +423,7 @@ __device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& 
             if (turn == 1) {
                 if (!__any_sync(0xffffffffu, over)) break;
                 const float top = masked ? row_top<true>(s_at, ks, lv, unscale, limit) : row_top<false>(s_at, ks, lv, unscale, limit);
-                const float next = over ? fmaxf(m, top) : m, f = ex2(m - next);
+                const float to = top - iqq::kLift, next = over || to > m + iqq::kMove ? fmaxf(m, to) : m, f = ex2(m - next);
                 m = next;
                 l *= f;
                 if (j > 0) {
@@ -500,7 +500,7 @@ prompt_kernel(const Kv8 C, const Attend A, uint32_t* __restrict__ flags)
     const Span s = iqq::span_of(C, W.b);
     const int64_t row0 = (slot - iqq::slot_base(C, W.b, A.group, kTiles * kRows, 1)) * (kTiles * kRows);
     W.rows = s.n * A.group;  // 0 for a bad span
-    if (row0 >= W.rows) return;
+    if (row0 < 0 || row0 >= W.rows) return;  // (a slot before the first sequence's, where cu begins above 0)
     W.row0 = static_cast<int32_t>(row0);
     W.first = s.first;
     W.start = s.start;
@@ -590,7 +590,7 @@ join_kernel(const Kv8 C, const Attend A)
     const int b = iqq::seq_of_slot(C, slot, A.group, kTiles * kRows, 1);
     const Span s = iqq::span_of(C, b);
     const int64_t row = (slot - iqq::slot_base(C, b, A.group, kTiles * kRows, 1)) * (kTiles * kRows) + r;
-    if (row >= static_cast<int64_t>(s.n) * A.group) return;
+    if (row < 0 || row >= static_cast<int64_t>(s.n) * A.group) return;
     const int64_t part = item * A.splits * (kTiles * kRows) + r;
     float m = kNone, l = 0.0f, o[kE] = {};
 #pragma unroll 4

@@ -215,10 +215,15 @@ def _check_attention(iqq, c, new, heads, dtype, q=None, scale=None, pad=0):
             o, l, mass, big = _attention64(c, b, h, heads // c.kv, q[at:at + n, h], n, sc)
             keys = c.lens[b]
             bound = mass * (u + 2 * (c.dim + 8) * 2.0 ** -24 * big[:, None] + (keys + 64) * 2.0 ** -24)
+            # binary16 weights below 2^-14 round by an absolute 2^-25, where a row's largest is at least
+            # 2^7 and a code's unit at most twice the largest value scale: 2^-25 127 2 vs / 2^7 a key
+            bound = bound + keys * 127 * 2.0 ** -31 * float(c.cache.v_scales.max())
             bound = bound + u * o.abs() * (1 + u) + STEP[dtype]
-            got = out[at:at + n, h].double()
+            got, gl = out[at:at + n, h].double(), lse[at:at + n, h].double()
+            real = torch.isfinite(q[at:at + n, h]).all(1)  # a row of q that holds an infinity or NaN gives NaN
+            assert got[~real].isnan().all() and not torch.isfinite(gl[~real]).any()
+            got, gl, o, l, big, bound = (t[real] for t in (got, gl, o, l, big, bound))
             assert ((got - o).abs() <= bound).all(), (b, h, float(((got - o).abs() - bound).max()))
-            gl = lse[at:at + n, h].double()
             fine = torch.isfinite(l)
             assert torch.equal(fine, torch.isfinite(gl)) and (gl[~fine] == -math.inf).all()
             off = (gl - l).abs()[fine] - (2 * (c.dim + 8) * 2.0 ** -24 * big[fine] + (keys + 64) * 2.0 ** -24
@@ -327,6 +332,73 @@ def test_attention_bad_indices_are_left_out(iqq):
         iqq.iqq_kv8_attention(c.cache, q, c.tables, args[0], _i32(cu), out, workspace=ws, flags=flags)
         assert int(flags.item()) == iqq.FLAG_BAD_INDEX
         assert torch.isfinite(out).all()
+
+
+def test_rows_before_the_first_sequence(iqq):
+    """cu_tokens that begins above 0: the rows before belong to nobody, in append, gather and both
+    forms of attention."""
+    for new, lens in (([1, 1, 1], [40, 7, 130]), ([90, 60, 100], [90, 200, 140])):
+        c = Case(iqq, lens, 2, 64, 16, 51)
+        skip, total = 40, 40 + sum(new)
+        cu = _cu(new) + skip
+        k = c.randn(total, 2, 64)
+        want = [t.cpu().clone() for t in (c.cache.k_codes, c.cache.k_scales)]
+        at = skip
+        for b, n in enumerate(new):
+            _append64(want[0], want[1], k[at:at + n].cpu(), c.tables[b].tolist(), lens[b] - n, n, 16)
+            at += n
+        flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+        iqq.iqq_kv8_append(c.cache, k, k, c.tables, _i32(lens), cu, flags=flags)
+        assert torch.equal(c.cache.k_codes.cpu(), want[0]) and torch.equal(c.cache.k_scales.cpu(), want[1])
+        ko = torch.full((total, 2, 64), 7.0, device="cuda")
+        iqq.iqq_kv8_gather(c.cache, c.tables, _i32(lens), cu, ko, ko.clone(), flags=flags)
+        assert (ko[:skip] == 7.0).all() and torch.equal(ko[skip], c.values(0, 0, 0).float()[lens[0] - new[0]].new_tensor(
+            torch.stack([c.values(0, 0, h).float()[lens[0] - new[0]] for h in range(2)]).tolist()))
+        q = c.randn(total, 4, 64, dtype=BF16)
+        out = torch.full_like(q, 7.0)
+        need = iqq.kv8_attention_workspace_bytes(c.cache, 3, c.tables.shape[1], 4, total)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        iqq.iqq_kv8_attention(c.cache, q, c.tables, _i32(lens), cu, out, workspace=ws, flags=flags)
+        ref = iqq.kv8_attention(c.cache, q[skip:].contiguous(), c.tables, _i32(lens), _cu(new))
+        assert (out[:skip] == 7.0).all() and int(flags.item()) == 0
+        torch.testing.assert_close(out[skip:].float(), ref.float(), rtol=2.0 ** -7, atol=2e-3)
+
+
+def test_attention_rows_without_a_maximum_beside_rising_scores(iqq):
+    """A prompt whose first pages are left out: some rows never see a key, beside rows whose scores
+    rise steeply from tile to tile."""
+    c = Case(iqq, [900], 1, 128, 64, 53)
+    c.cache.k_scales.fill_(0.02)
+    c.cache.k_codes[c.tables[0, :15].long()] = (torch.arange(15, device="cuda") * 8)[:, None, None, None].to(torch.int8)
+    q = torch.full((880, 1, 128), 4.0, device="cuda").to(BF16)
+    bad = c.tables.clone()
+    bad[0, :4] = -1
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = iqq.kv8_attention(c.cache, q, bad, _i32([900]), _i32([0, 880]), flags=flags)
+    assert int(flags.item()) == iqq.FLAG_BAD_INDEX
+    k, v = c.values(0, 0, 0), c.values(0, 1, 0)
+    s = (q[:, 0].double() @ k.t()) * 128 ** -0.5
+    seen = torch.arange(900, device="cuda")[None] <= 20 + torch.arange(880, device="cuda")[:, None]
+    seen[:, :256] = False
+    p = torch.softmax(s.masked_fill(~seen, -math.inf), 1).nan_to_num(0.0)
+    ref, mass = p @ v, p @ v.abs()
+    # scores of one page are equal, so weights are equal up to binary32 and binary16 roundings
+    bound = mass * (2.0 ** -8 + 2.0 ** -10) + 2.0 ** -8 * ref.abs() + 2.0 ** -133
+    assert (out[:236] == 0).all()
+    assert ((out[:, 0].double() - ref).abs() <= bound).all()
+
+
+def test_attention_largest_and_smallest_q(iqq):
+    """Rows of q at the ends of bfloat16's range: the scores, brought back by the scale, are ordinary.
+    A drawn 4 times 2^126 is an infinity, whose row alone is NaN."""
+    c = Case(iqq, [200, 90], 1, 64, 16, 57)
+    for size in (2.0 ** 126, 2.0 ** -126):
+        base = c.randn(91, 2, 64, dtype=BF16)
+        q = (base.double() * size).to(BF16)
+        scale = 0.125 / size
+        if not 2.0 ** -126 <= scale <= 2.0 ** 127:
+            scale = 2.0 ** -126
+        _check_attention(iqq, c, [1, 90], 2, BF16, q=q, scale=scale)
 
 
 def test_attention_strided_q_and_offsets_past_32_bits(iqq):
