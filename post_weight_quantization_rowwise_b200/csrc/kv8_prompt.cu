@@ -36,8 +36,9 @@ using iqq::sub_h2;
 constexpr int kRows = 128, kTiles = 2, kKeys = 128, kStages = 2, kScales = 4;
 constexpr int kMakers = 8, kMma = 12, kLoader = 13;  // first warp that makes operands; the ones that multiply and load
 constexpr int kThreads = 32 * 16;
-// Registers a thread of the softmax, the makers and the rest (the launch's are shared out anew).
-constexpr int kSoftmaxRegs = 184, kMakerRegs = 88, kOtherRegs = 40;
+// Registers a thread of the softmax, the makers and the rest (the launch's are shared out anew); where
+// the rest spill, so does the time (8192 tokens of 32 heads over 8: 650 us with 40 for them).
+constexpr int kSoftmaxRegs = 192, kMakerRegs = 72, kOtherRegs = 56;
 constexpr int kRegs = 128 * (2 * kSoftmaxRegs + kMakerRegs + kOtherRegs);
 
 constexpr float kTinyScale = 7.888609052210118e-31f;  // 2^-100: a value scale below it counts as 0
@@ -196,7 +197,7 @@ __device__ __forceinline__ bool make_operands(Smem<D>& S, int n)
         const int s = j % kStages, c = j % kScales;
         const uint32_t ph = (j / kStages) & 1;
         uint32_t zero = 0;  // the 16 keys whose value scale is 0
-#pragma unroll
+#pragma unroll 1  // (the code of all roles together has to stay in the instruction caches)
         for (int which = 0; which < 2; ++which) {
             bool late = !iqq::bar_wait(iqq::smem_u32(&S.rfull[which]), j & 1);
             if (__any_sync(0xffffffffu, late)) return false;
@@ -237,17 +238,20 @@ __device__ __forceinline__ bool make_operands(Smem<D>& S, int n)
 }
 
 // ---- the warp that multiplies (one thread) ----
+// Its path from a tile's weights to the next products is every step's: it is one loop, not unrolled
+// over the tiles, within its registers, and descriptors are a 32-bit sum (8192 tokens of 32 heads
+// over 8: 590 us before, 541 us so).
 
 template <int D>
 __device__ __forceinline__ bool multiply(Smem<D>& S, const Work& W, uint32_t tmem)
 {
     constexpr uint32_t kQk = iqq::idesc_f16(kRows, kKeys, false), kPv = iqq::idesc_f16(kRows, D, true);
     const auto scores = [&](int t, int j) {
-        const uint32_t q = iqq::smem_u32(S.q[t]), k = iqq::smem_u32(S.k[j % kStages]);
+        const uint32_t q = iqq::desc_lo(iqq::smem_u32(S.q[t]), 16), k = iqq::desc_lo(iqq::smem_u32(S.k[j % kStages]), 16);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-            const uint32_t at = (i >> 2) * 16384 + (i & 3) * 32;
-            iqq::mma_f16(tmem + t * kKeys, iqq::desc_k128(q + at), iqq::desc_k128(k + at), kQk, i > 0);
+            const uint32_t at = ((i >> 2) * 16384 + (i & 3) * 32) >> 4;
+            iqq::mma_f16(tmem + t * kKeys, q + at, k + at, kQk, i > 0);
         }
         iqq::tc_commit<1>(iqq::smem_u32(&S.sfull[t]));
     };
@@ -257,19 +261,21 @@ __device__ __forceinline__ bool multiply(Smem<D>& S, const Work& W, uint32_t tme
         if (!iqq::bar_wait(iqq::smem_u32(&S.qfull[t]), 0)) return false;
     }
     for (int j = -1; j < n; ++j) {
+#pragma unroll 1
         for (int t = 0; t < kTiles; ++t) {
-            if (j >= 0 && j < W.tiles[t]) {
+            const int mine = t == 0 ? W.tiles[0] : W.tiles[1];
+            if (j >= 0 && j < mine) {
                 if (!iqq::bar_wait(iqq::smem_u32(&S.pfull[t]), j & 1)) return false;
                 if (!iqq::bar_wait(iqq::smem_u32(&S.vfull[j % kStages]), (j / kStages) & 1)) return false;
                 iqq::tc_fence_after();
-                const uint32_t v = iqq::smem_u32(S.v[j % kStages]), p = tmem + t * kKeys, o = tmem + kTiles * kKeys + t * 128;
+                const uint32_t v = iqq::desc_lo(iqq::smem_u32(S.v[j % kStages]), 16384), p = tmem + t * kKeys, o = tmem + kTiles * kKeys + t * 128;
 #pragma unroll
                 for (int i = 0; i < kKeys / 16; ++i)
-                    iqq::mma_f16_t(o, p + 8 * i, iqq::desc_n128(v + i * 2048, 16384), kPv, j > 0 || i > 0);
-                if (j + 1 == W.tiles[t]) iqq::tc_commit<1>(iqq::smem_u32(&S.ofull[t]));
+                    iqq::mma_f16_t(o, p + 8 * i, v + i * 128, kPv, j > 0 || i > 0);
+                if (j + 1 == mine) iqq::tc_commit<1>(iqq::smem_u32(&S.ofull[t]));
             }
             // the next scores overwrite this tile's weights: the products run in order
-            if (j + 1 < W.tiles[t]) {
+            if (j + 1 < mine) {
                 if (!iqq::bar_wait(iqq::smem_u32(&S.kfull[(j + 1) % kStages]), ((j + 1) / kStages) & 1)) return false;
                 iqq::tc_fence_after();
                 scores(t, j + 1);
@@ -352,6 +358,71 @@ __device__ __forceinline__ float row_weights(uint32_t s_at, const float* ks, con
     return l;
 }
 
+// A row is D/8 units of 16 bytes, in q and in the output: as many lanes take a row of global memory,
+// so a warp's access is whole rows (a thread for each row took 7 us for q and 2 us for the output).
+template <int D>
+struct Rows {
+    static constexpr int kUnits = D / 8, kAtOnce = 32 / kUnits;
+    // where the lane's unit of the i-th access lies: the row within the warp's 32, and the unit
+    __device__ __forceinline__ static int row(int i) { return kAtOnce * i + static_cast<int>(threadIdx.x & 31) / kUnits; }
+    __device__ __forceinline__ static int unit_of() { return static_cast<int>(threadIdx.x & 31) % kUnits; }
+    // ... and in the tile's operand
+    __device__ __forceinline__ static uint32_t at(int r, int u) { return static_cast<uint32_t>(u >> 3) * 16384 + unit(r, u & 7); }
+};
+
+// This warp's 32 rows of q on their way into the operand's place, as they are.
+template <class T, int D>
+__device__ __forceinline__ void fetch_q(Smem<D>& S, const Attend& A, const Work& W, int t)
+{
+    using R = Rows<D>;
+    const int r0 = static_cast<int>(threadIdx.x & 96), row = W.row0 + t * kRows + r0 + static_cast<int>(threadIdx.x & 31);
+    const int token = row / A.group;
+    const int64_t from = row < W.rows ? (W.first + token) * A.q_token_stride +
+                                            (W.head * A.group + row - token * A.group) * A.q_head_stride
+                                      : -1;
+#pragma unroll
+    for (int i = 0; i < R::kUnits; ++i) {
+        const int r = R::row(i), u = R::unit_of();
+        const int64_t at = __shfl_sync(0xffffffffu, from, r);
+        iqq::async_load16(iqq::smem_u32(S.q[t] + R::at(r0 + r, u)), static_cast<const T*>(A.q) + (at < 0 ? 0 : at + u * 8),
+                          at < 0 ? 0u : 16u);
+    }
+}
+
+// This warp's 32 rows of sums times `by`, out: staged in q's place, which no product reads any more.
+// `to` is this thread's row (null: none).
+template <class V, int D>
+__device__ __forceinline__ void put_rows(Smem<D>& S, int t, uint32_t o_at, float by, bool none, V* to)
+{
+    using R = Rows<D>;
+    constexpr int kRound = R::kUnits * 16 / static_cast<int>(sizeof(V)), kPer = 16 / static_cast<int>(sizeof(V));
+    const int r = static_cast<int>(threadIdx.x & 127), r0 = r & 96;
+#pragma unroll
+    for (int d = 0; d < D; d += kRound) {
+#pragma unroll
+        for (int i = 0; i < kRound; i += 32) {
+            uint32_t x[32];
+            iqq::tmem_ld32(o_at + d + i, x);
+            iqq::tmem_wait_ld(x);
+            __align__(16) V v[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = iqq::from_f32<V>(none ? 0.0f : __uint_as_float(x[e]) * by);
+#pragma unroll
+            for (int e = 0; e < 32 / kPer; ++e)
+                *reinterpret_cast<uint4*>(S.q[t] + R::at(r, i / kPer + e)) = reinterpret_cast<const uint4*>(v)[e];
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < R::kUnits; ++i) {
+            const int row = R::row(i), u = R::unit_of();
+            V* out = reinterpret_cast<V*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), row));
+            const uint4 w = *reinterpret_cast<const uint4*>(S.q[t] + R::at(r0 + row, u));
+            if (out != nullptr) reinterpret_cast<uint4*>(out + d)[u] = w;
+        }
+        __syncwarp();
+    }
+}
+
 template <class T, int D>
 __device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& W, uint32_t tmem, int t)
 {
@@ -359,7 +430,7 @@ __device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& 
     const bool real = row < W.rows;
     const int token = row / A.group;
     const int64_t at = static_cast<int64_t>(W.first + token) * A.heads + W.head * A.group + row - token * A.group;
-    const int n = W.tiles[t];
+    const int n = t == 0 ? W.tiles[0] : W.tiles[1];
     const int64_t part = W.part + t * kRows + r;
     if (n == 0) {  // nothing to see: zeros
         if (real && A.splits > 1) {
@@ -371,14 +442,15 @@ __device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& 
         }
         return true;
     }
-    // the row of q: all of it in flight at once, then its largest value, then the operand
+    // the row of q that fetch_q brought: its largest value, then the operand
     float unscale;
+    iqq::async_wait_all();
+    __syncwarp();
     {
-        const T* q = static_cast<const T*>(A.q) + (W.first + token) * A.q_token_stride +
-                     (W.head * A.group + row - token * A.group) * A.q_head_stride;
+        const T* q = nullptr;  // (of its type)
         uint4 raw[D / 8];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) raw[i] = real ? __ldg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < D / 8; ++i) raw[i] = *reinterpret_cast<const uint4*>(S.q[t] + Rows<D>::at(r, i));
         float top = 0.0f, v[8];
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
@@ -393,7 +465,7 @@ __device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& 
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
             iqq::widen8(q, raw[i], v);
-            *reinterpret_cast<uint4*>(S.q[t] + (i >> 3) * 16384 + unit(r, i & 7)) =
+            *reinterpret_cast<uint4*>(S.q[t] + Rows<D>::at(r, i)) =
                 make_uint4(pack_h2(v[0] * down, v[1] * down), pack_h2(v[2] * down, v[3] * down),
                            pack_h2(v[4] * down, v[5] * down), pack_h2(v[6] * down, v[7] * down));
         }
@@ -455,26 +527,8 @@ __device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& 
     iqq::tc_fence_after();
     const bool none = m == kNone && l == 0.0f;
     const float inv = none ? 0.0f : __fdiv_rn(1.0f, l);
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-        uint32_t x[32];
-        iqq::tmem_ld32(o_at + 32 * i, x);
-        iqq::tmem_wait_ld(x);
-        if (real && A.splits > 1) {
-            float4* out = reinterpret_cast<float4*>(A.part + part * D + 32 * i);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                out[e] = make_float4(__uint_as_float(x[4 * e]) * inv, __uint_as_float(x[4 * e + 1]) * inv,
-                                     __uint_as_float(x[4 * e + 2]) * inv, __uint_as_float(x[4 * e + 3]) * inv);
-        } else if (real) {
-            __align__(16) T v[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = iqq::from_f32<T>(none ? 0.0f : __uint_as_float(x[e]) * inv);
-            uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(A.out) + at * D + 32 * i);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) out[e] = reinterpret_cast<const uint4*>(v)[e];
-        }
-    }
+    if (A.splits > 1) put_rows<float, D>(S, t, o_at, inv, none, real ? A.part + part * D : nullptr);
+    else put_rows<T, D>(S, t, o_at, inv, none, real ? static_cast<T*>(A.out) + at * D : nullptr);
     const float lse = none ? -INFINITY : m + log2f(l);
     if (real && A.splits > 1) A.part_lse[part] = lse;
     else if (real && A.lse != nullptr) A.lse[at] = lse / kLog2e;
@@ -500,7 +554,7 @@ prompt_kernel(const Kv8 C, const Attend A, uint32_t* __restrict__ flags)
     const Span s = iqq::span_of(C, W.b);
     const int64_t row0 = (slot - iqq::slot_base(C, W.b, A.group, kTiles * kRows, 1)) * (kTiles * kRows);
     W.rows = s.n * A.group;  // 0 for a bad span
-    if (row0 < 0 || row0 >= W.rows) return;  // (a slot before the first sequence's, where cu begins above 0)
+    if (row0 < 0 || row0 >= W.rows) return;  // (below 0: before the first sequence's, where cu begins above 0)
     W.row0 = static_cast<int32_t>(row0);
     W.first = s.first;
     W.start = s.start;
@@ -520,7 +574,7 @@ prompt_kernel(const Kv8 C, const Attend A, uint32_t* __restrict__ flags)
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) W.tiles[t] = max(0, min(W.tiles[t], to) - W.tile0);
     }
-
+    if (warp < kMakers && (warp < 4 ? W.tiles[0] : W.tiles[1]) > 0) fetch_q<T, D>(S, A, W, warp >> 2);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             iqq::bar_init(iqq::smem_u32(&S.kfull[i]), 4);

@@ -168,6 +168,12 @@ __device__ __forceinline__ void async_load4(uint32_t dst, const void* src)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
+// 16 bytes, of which `real` (16 or 0) are read and the rest are zeros.
+__device__ __forceinline__ void async_load16(uint32_t dst, const void* src, uint32_t real)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real) : "memory");
+}
+__device__ __forceinline__ void async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Arrives on the barrier when this thread's async_load4 so far are done.
 __device__ __forceinline__ void async_arrive(uint32_t bar)
 {
@@ -230,32 +236,32 @@ __host__ __device__ constexpr uint32_t idesc_i8(int m, int n)
     return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// The same for a product with N contiguous in memory (rows of k, 64 values of n = 128 bytes each,
-// 128-byte swizzle): groups of eight k are 1024 bytes apart, blocks of 64 n `block` bytes.
-__device__ __forceinline__ uint64_t desc_n128(uint32_t addr, uint32_t block)
-{
-    return (static_cast<uint64_t>((addr & 0x3ffff) >> 4)) | (static_cast<uint64_t>(block >> 4) << 16) | (64ULL << 32) |
-           (1ULL << 46) | (2ULL << 61);
-}
+// Binary16 products take the low word of a descriptor alone, the high one being the same for all: rows
+// of 128 bytes, 128-byte swizzle, groups of eight rows 1024 bytes apart.  K-major operands (`block` 16,
+// not looked at), or N contiguous in memory (rows of k, 64 values of n = 128 bytes each, blocks of 64 n
+// `block` bytes apart).
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t block) { return (addr & 0x3ffff) >> 4 | (block >> 4) << 16; }
+constexpr uint32_t kDescHi = 64u | 1u << 14 | 2u << 29;
 
 // binary16 operands, binary32 sums; A from shared memory, or from tensor memory (two values a column).
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+__device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(kDescHi), "r"(idesc),
         "r"(static_cast<uint32_t>(add))
         : "memory");
 }
-__device__ __forceinline__ void mma_f16_t(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+__device__ __forceinline__ void mma_f16_t(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(kDescHi), "r"(idesc),
         "r"(static_cast<uint32_t>(add))
         : "memory");
 }
-// b_rows_of_k: B has N contiguous (desc_n128), else K (desc_k128).
+// b_rows_of_k: B has N contiguous, else K.
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool b_rows_of_k)
 {
     return (1u << 4) | (b_rows_of_k ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
