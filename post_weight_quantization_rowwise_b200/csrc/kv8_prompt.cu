@@ -33,7 +33,7 @@ using iqq::pack_h2;
 using iqq::Span;
 using iqq::sub_h2;
 
-constexpr int kRows = 128, kTiles = 2, kKeys = 128, kStages = 2, kScales = 4;
+constexpr int kRows = 128, kTiles = 2, kKeys = 128, kStages = 2 /* a power of two */, kScales = 4;
 constexpr int kMakers = 8, kMma = 12, kLoader = 13;  // first warp that makes operands; the ones that multiply and load
 constexpr int kThreads = 32 * 16;
 // Registers a thread of the softmax, the makers and the rest (the launch's are shared out anew); where
@@ -237,52 +237,57 @@ __device__ __forceinline__ bool make_operands(Smem<D>& S, int n)
     return true;
 }
 
-// ---- the warp that multiplies (one thread) ----
+// ---- the warp that multiplies ----
 // Its path from a tile's weights to the next products is every step's: it is one loop, not unrolled
 // over the tiles, within its registers, and descriptors are a 32-bit sum (8192 tokens of 32 heads
-// over 8: 590 us before, 541 us so).
+// over 8: 590 us before, 541 us so).  All lanes run it, on values that are the same in all, and one
+// issues, so the operands stay in uniform registers; the weights are waited for last (514 us).
 
 template <int D>
-__device__ __forceinline__ bool multiply(Smem<D>& S, const Work& W, uint32_t tmem)
+__device__ __forceinline__ bool multiply(Smem<D>& S, const Work& W, uint32_t base)
 {
+    const uint32_t tmem = __shfl_sync(0xffffffffu, base, 0);
+    const int tiles0 = __shfl_sync(0xffffffffu, W.tiles[0], 0), tiles1 = __shfl_sync(0xffffffffu, W.tiles[1], 0);
     constexpr uint32_t kQk = iqq::idesc_f16(kRows, kKeys, false), kPv = iqq::idesc_f16(kRows, D, true);
-    const auto scores = [&](int t, int j) {
-        const uint32_t q = iqq::desc_lo(iqq::smem_u32(S.q[t]), 16), k = iqq::desc_lo(iqq::smem_u32(S.k[j % kStages]), 16);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            const uint32_t at = ((i >> 2) * 16384 + (i & 3) * 32) >> 4;
-            iqq::mma_f16(tmem + t * kKeys, q + at, k + at, kQk, i > 0);
-        }
-        iqq::tc_commit<1>(iqq::smem_u32(&S.sfull[t]));
-    };
-    const int n = W.key_tiles();
-    for (int t = 0; t < kTiles; ++t) {
-        if (W.tiles[t] == 0) continue;
-        if (!iqq::bar_wait(iqq::smem_u32(&S.qfull[t]), 0)) return false;
-    }
+    const int n = max(tiles0, tiles1);
+    bool late = false;
+    for (int t = 0; t < kTiles; ++t)
+        if ((t == 0 ? tiles0 : tiles1) > 0) late |= !iqq::bar_wait(iqq::smem_u32(&S.qfull[t]), 0);
     for (int j = -1; j < n; ++j) {
+        const int sv = j & (kStages - 1), sk = (j + 1) & (kStages - 1);
 #pragma unroll 1
         for (int t = 0; t < kTiles; ++t) {
-            const int mine = t == 0 ? W.tiles[0] : W.tiles[1];
-            if (j >= 0 && j < mine) {
-                if (!iqq::bar_wait(iqq::smem_u32(&S.pfull[t]), j & 1)) return false;
-                if (!iqq::bar_wait(iqq::smem_u32(&S.vfull[j % kStages]), (j / kStages) & 1)) return false;
-                iqq::tc_fence_after();
-                const uint32_t v = iqq::desc_lo(iqq::smem_u32(S.v[j % kStages]), 16384), p = tmem + t * kKeys, o = tmem + kTiles * kKeys + t * 128;
+            const int mine = t == 0 ? tiles0 : tiles1;
+            const bool weigh = j >= 0 && j < mine, score = j + 1 < mine;
+            // the operands first, which are ready early: then nothing but the weights is waited for
+            if (weigh) late |= !iqq::bar_wait(iqq::smem_u32(&S.vfull[sv]), (j / kStages) & 1);
+            if (score) late |= !iqq::bar_wait(iqq::smem_u32(&S.kfull[sk]), ((j + 1) / kStages) & 1);
+            if (weigh) late |= !iqq::bar_wait(iqq::smem_u32(&S.pfull[t]), j & 1);
+            if (__any_sync(0xffffffffu, late)) return false;
+            iqq::tc_fence_after();
+            const uint32_t s = tmem + t * kKeys, o = tmem + kTiles * kKeys + t * 128;
+            const uint32_t q = iqq::desc_lo(iqq::smem_u32(S.q[t]), 16), k = iqq::desc_lo(iqq::smem_u32(S.k[sk]), 16);
+            const uint32_t v = iqq::desc_lo(iqq::smem_u32(S.v[sv]), 16384);
+            if (iqq::elect()) {
+                if (weigh) {
 #pragma unroll
-                for (int i = 0; i < kKeys / 16; ++i)
-                    iqq::mma_f16_t(o, p + 8 * i, v + i * 128, kPv, j > 0 || i > 0);
-                if (j + 1 == mine) iqq::tc_commit<1>(iqq::smem_u32(&S.ofull[t]));
-            }
-            // the next scores overwrite this tile's weights: the products run in order
-            if (j + 1 < mine) {
-                if (!iqq::bar_wait(iqq::smem_u32(&S.kfull[(j + 1) % kStages]), ((j + 1) / kStages) & 1)) return false;
-                iqq::tc_fence_after();
-                scores(t, j + 1);
+                    for (int i = 0; i < kKeys / 16; ++i) iqq::mma_f16_t(o, s + 8 * i, v + i * 128, kPv, j > 0 || i > 0);
+                    if (j + 1 == mine) iqq::tc_commit<1>(iqq::smem_u32(&S.ofull[t]));
+                }
+                if (score) {  // (over this tile's weights: the products run in order)
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint32_t at = ((i >> 2) * 16384 + (i & 3) * 32) >> 4;
+                        iqq::mma_f16(s, q + at, k + at, kQk, i > 0);
+                    }
+                    iqq::tc_commit<1>(iqq::smem_u32(&S.sfull[t]));
+                }
             }
         }
-        if (j + 1 < n) iqq::tc_commit<1>(iqq::smem_u32(&S.kempty[(j + 1) % kStages]));
-        if (j >= 0) iqq::tc_commit<1>(iqq::smem_u32(&S.vempty[j % kStages]));
+        if (iqq::elect()) {
+            if (j + 1 < n) iqq::tc_commit<1>(iqq::smem_u32(&S.kempty[sk]));
+            if (j >= 0) iqq::tc_commit<1>(iqq::smem_u32(&S.vempty[sv]));
+        }
     }
     return true;
 }
@@ -614,10 +619,10 @@ prompt_kernel(const Kv8 C, const Attend A, uint32_t* __restrict__ flags)
         fewer_registers<kOtherRegs>();
         if (warp == kLoader) {
             ok = load<D>(S, C, W, W.key_tiles(), end, flags);
-        } else if (threadIdx.x == 32 * kMma) {
+        } else if (warp == kMma) {
             ok = multiply<D>(S, W, tmem);
             // nothing is left running when the tensor memory goes
-            iqq::tc_commit<1>(iqq::smem_u32(&S.done));
+            if (iqq::elect()) iqq::tc_commit<1>(iqq::smem_u32(&S.done));
             ok &= iqq::bar_wait(iqq::smem_u32(&S.done), 0);
         }
     }

@@ -105,6 +105,15 @@ __device__ __forceinline__ bool bar_wait_long(uint32_t bar, uint32_t parity)
     return true;
 }
 
+// One lane of a whole warp, the same one every time (products and the commit that follows them are
+// one thread's).
+__device__ __forceinline__ bool elect()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // ---- clusters ----
 
 __device__ __forceinline__ uint32_t cluster_rank()
