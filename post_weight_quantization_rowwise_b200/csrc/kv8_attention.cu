@@ -886,6 +886,8 @@ extern "C" iqq_status iqq_kv8_attention(const iqq_kv8_cache* cache, const iqq_kv
     if (n_heads < 1 || n_heads % C.heads != 0 || n_heads > 65535 || q_token_stride < 0 || q_head_stride < 0 ||
         n_tokens * n_heads > 0x7fffffffLL)
         return IQQ_ERR_SHAPE;
+    // (a tile's row is 32 bits; more than 274 GB of codes are refused)
+    if (cache->n_pages * cache->n_kv_heads > 0x7fffffffLL * 128 / (cache->page_size * cache->head_dim)) return IQQ_ERR_SHAPE;
     if (n_tokens == 0 || C.n_seqs == 0) return IQQ_OK;
     const Plan p = plan_of(cache, seqs, n_heads, n_tokens);
     const size_t need = iqq_kv8_attention_workspace_bytes(cache, seqs, n_heads, n_tokens);

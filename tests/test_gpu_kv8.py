@@ -468,3 +468,69 @@ def test_attention_on_two_streams_at_once(iqq):
         y = iqq.kv8_attention(b.cache, qb, *args_b, stream=s2)
         torch.cuda.synchronize()
         assert torch.equal(x, alone[0]) and torch.equal(y, alone[1])
+
+
+def test_attention_prompts_beside_single_tokens(iqq):
+    """One call that holds whole prompts, chunks, drafts, single tokens and idle sequences."""
+    lens = [700, 33, 2000, 1, 260, 0, 90, 5000]
+    for new in ([700, 1, 1, 1, 4, 0, 0, 130], [1, 1, 1, 1, 3, 0, 2, 1], [40, 1, 300, 1, 1, 0, 90, 1]):
+        c = Case(iqq, lens, 2, 128, 32, 61)
+        _check_attention(iqq, c, new, 8, BF16, pad=2)
+
+
+@pytest.mark.parametrize("count", [33, 200, 1100])
+def test_many_sequences(iqq, count):
+    """More sequences than a warp's lanes, its square and a launch's CTAs; append, gather, attention."""
+    rng = random.Random(count)
+    lens = [rng.choice([0, 1, 5, 16, 17, 40]) for _ in range(count)]
+    new = [min(m, rng.choice([0, 1, 1, 2])) for m in lens]
+    c = Case(iqq, lens, 1, 64, 16, 63)
+    k = c.randn(sum(new), 1, 64)
+    want = [t.cpu().clone() for t in (c.cache.k_codes, c.cache.k_scales)]
+    at = 0
+    for b, n in enumerate(new):
+        _append64(want[0], want[1], k[at:at + n].cpu(), c.tables[b].tolist(), lens[b] - n, n, 16)
+        at += n
+    iqq.iqq_kv8_append(c.cache, k, k, c.tables, _i32(lens), _cu(new))
+    assert torch.equal(c.cache.k_codes.cpu(), want[0]) and torch.equal(c.cache.k_scales.cpu(), want[1])
+    ko, vo = iqq.kv8_gather(c.cache, c.tables, _i32(lens), _cu(new), sum(new), dtype=F32)
+    at = 0
+    for b, n in enumerate(new):
+        assert torch.equal(ko[at:at + n, 0], c.values(b, 0, 0)[lens[b] - n:].float())
+        assert torch.equal(vo[at:at + n, 0], c.values(b, 1, 0)[lens[b] - n:].float())
+        at += n
+    _check_attention(iqq, c, new, 2, F16)
+
+
+@pytest.mark.parametrize("kv,group,new", [(1, 64, [1, 2]), (1, 71, [1, 1]), (2, 33, [9, 1]), (1, 300, [2, 3])])
+def test_attention_large_groups(iqq, kv, group, new):
+    c = Case(iqq, [150, 77], kv, 64, 16, 67)
+    _check_attention(iqq, c, new, kv * group, BF16)
+
+
+def test_attention_shared_pages_and_lowest_codes(iqq):
+    """Two sequences whose first pages are the same, and codes of -128."""
+    c = Case(iqq, [300, 290], 1, 128, 16, 71)
+    c.tables[1, :12] = c.tables[0, :12]
+    c.cache.k_codes[c.tables[0, 3].long(), :, 5] = -128
+    c.cache.v_codes[c.tables[0, 7].long(), :, :, ::3] = -128
+    for new in ([1, 1], [200, 280]):
+        _check_attention(iqq, c, new, 4, BF16)
+
+
+def test_captured_prompts_with_split_keys(iqq):
+    """A long chunk whose keys are split, captured and replayed on new q, lengths and pages."""
+    c = Case(iqq, [9000], 1, 128, 64, 73)
+    q, lens, cu = torch.zeros(100, 8, 128, dtype=BF16, device="cuda"), _i32([9000]), _i32([0, 100])
+    assert iqq.kv8_attention_workspace_bytes(c.cache, 1, c.tables.shape[1], 8, 100) > 0
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = iqq.kv8_attention(c.cache, q, c.tables, lens, cu)
+    for m in (9000, 100, 4321):
+        q.copy_(c.randn(100, 8, 128))
+        lens.fill_(m)
+        c.tables[0, :140] = c.tables[0, torch.randperm(140, device="cuda")]
+        c.lens = [m]
+        graph.replay()
+        assert torch.equal(out, _check_attention(iqq, c, [100], 8, BF16, q=q))

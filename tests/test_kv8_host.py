@@ -79,6 +79,8 @@ def test_attention_refusals():
     assert _attend(_3=None) == 1 and _attend(_8=None) == 1
     assert _attend(_3=V(8)) == 3 and _attend(_8=V(8)) == 3 and _attend(_4=260) == 3 and _attend(_5=68) == 3
     assert _attend(_9=V(2)) == 3 and _attend(_11=V(8)) == 3 and _attend(_13=V(2)) == 3
+    for kw in (dict(n_pages=1 << 30, n_kv_heads=8), dict(n_pages=1 << 24, n_kv_heads=1, page_size=128, head_dim=128)):
+        assert _attend(cache=_cache(**kw), _6=8) == 2, kw  # 2^31 rows of 128 bytes and more
     W = m._lib.iqq_kv8_attention_workspace_bytes
     long = _seqs(n_seqs=1, table_width=1 << 14, table_stride=1 << 14)
     need = W(ctypes.byref(_cache()), ctypes.byref(long), 4, 1)
