@@ -776,11 +776,11 @@ combine_kernel(const Args A, const int ctas)
     if (A.lse != nullptr && d == 0) A.lse[at] = none ? -INFINITY : (top + log2f(sum)) / kLog2e;
 }
 
-// Rows a sequence (its share of the tokens, times the group) from which the prompt kernel is taken.
-// 24 sequences up to 5000, 128 dimensions: 32 rows 81 us against 121, 48 rows 117 against 121, 62 rows
-// 148 against 119; 64 sequences of 2000: 48 rows 201 against 182; 64 dimensions: 48 rows 124 against 149,
-// 62 rows 158 against 150.
-constexpr int64_t kPromptRows = 49;
+// Rows a sequence (its share of the tokens, times the group) from which the prompt kernel is taken: it
+// makes 256 rows' operands for any number, this one 16 rows' at a time.  Decode and prompt kernel, us:
+//   128 dimensions  24 sequences up to 5000: 32 rows 82, 101; 40 rows 110, 102.  64 of 2000: 32 rows 144, 155; 40 rows 200, 156
+//    64 dimensions  24 sequences up to 5000: 48 rows 76, 83; 62 rows 97, 82.     64 of 2000: 48 rows 124, 127; 62 rows 158, 127
+constexpr int64_t prompt_rows(int64_t head_dim) { return head_dim == 128 ? 33 : 49; }
 
 struct Plan {
     bool prompt;
@@ -798,7 +798,7 @@ Plan plan_of(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int64_t n_hea
     Plan p = {};
     const int64_t group = n_heads / cache->n_kv_heads;
     const int64_t each = (n_tokens + seqs->n_seqs - 1) / seqs->n_seqs * group;
-    p.prompt = each >= kPromptRows;
+    p.prompt = each >= prompt_rows(cache->head_dim);
     if (p.prompt) {
         p.splits = iqq::prompt_splits(cache, seqs, n_heads, n_tokens);
         p.part = iqq::prompt_part_bytes(cache, seqs, n_heads, n_tokens, p.splits, &p.lse);
