@@ -1,4 +1,5 @@
-"""imatrix-weighted Q4_0 and Q8_K_128 quantization on B200 (sm_100a).
+"""imatrix-weighted Q4_0 and Q8_K_128 quantization on B200 (sm_100a), int8 matrix products and
+attention over an int8 key/value cache.
 
 Thin Python binding over the C ABI in ``include/iqq.h`` (``libiqq.so`` in this
 package).  The functions have the ABI's names; they only check and marshal
@@ -13,6 +14,10 @@ first call raises ImportError if ``libiqq.so`` is missing or fails to load.
 Block formats (little endian):
   Q4_0      18 bytes per 32 values: binary16 d | qs[16], qs[i] = (l[i]+8) | (l[i+16]+8) << 4
   Q8_K_128  140 bytes per 128 values: float d | int8 qs[128] | int16 bsums[4]
+
+The int8 operators keep codes and scales in tensors of their own: a scale a row for
+quantize_i8_rows and gemm_i8, a scale for each page and head in a Kv8Cache, which
+iqq_kv8_append writes, kv8_gather reads back and kv8_attention attends over.
 """
 from __future__ import annotations
 

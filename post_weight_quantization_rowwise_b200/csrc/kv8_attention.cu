@@ -7,7 +7,7 @@
 // r % group of the group), so a page is read once for all of them.
 //
 // decode kernel (few rows a sequence).  Bound by the cache's bytes.  One warp streams the pages'
-// tiles into a ring of stages (cp.async.bulk, the scales beside them by cp.async); four warps
+// tiles into a ring of stages (TMA, the scales beside them by cp.async); four warps
 // take 32 keys of a stage each, straight into the operand registers of mma.m16n8k16:
 //     S^T = K Q^T (16 keys x 8 rows),  O^T = V^T P^T (16 dimensions x 8 rows).
 // The order of the dimensions in a dot product, and of the rows of V^T, is free, so each lane
@@ -27,6 +27,10 @@
 // machine evenly.  A tile that lies in one share is finished there; of the others each share
 // leaves a part, normalized and with its log-sum, in the workspace (two a CTA at most: where its
 // share begins and where it ends), and combine_kernel joins them.
+//
+// Measured with inputs larger than L2: 32 sequences of 4096 tokens, 32 heads over 32 of 128 dimensions
+// 169 us (6.3 TB/s of 6.55); 64 up to 8000, 32 over 8: 97 us (5.4); one of 131000, 32 over 4: 37 us
+// (3.6; the scan, the ring's filling and the joining launch are 10 us of any call).
 #include <math.h>
 
 #include <algorithm>
