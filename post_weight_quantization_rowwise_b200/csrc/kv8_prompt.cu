@@ -44,7 +44,7 @@ constexpr int kThreads = 32 * 16;
 constexpr int kSoftmaxRegs = 192, kMakerRegs = 72, kOtherRegs = 56;
 constexpr int kRegs = 128 * (2 * kSoftmaxRegs + kMakerRegs + kOtherRegs);
 
-constexpr float kTinyScale = 7.888609052210118e-31f;  // 2^-100: a value scale below it counts as 0
+constexpr float kTinyScale = 8.077935669463161e-28f;  // 2^-90: a value scale below it counts as 0, so sums of P / vs stay finite
 
 // Operands in rows of 64 dimensions (128 bytes), 128-byte swizzle: block b of 64 dimensions of a
 // tile is 128 rows at b * 16384.

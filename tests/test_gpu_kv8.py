@@ -534,3 +534,12 @@ def test_captured_prompts_with_split_keys(iqq):
         c.lens = [m]
         graph.replay()
         assert torch.equal(out, _check_attention(iqq, c, [100], 8, BF16, q=q))
+
+
+def test_attention_smallest_and_largest_value_scales(iqq):
+    """Pages whose value scales are all near 2^-87, or near 2^93: denominators and outputs stay finite."""
+    for size in (2.0 ** -80, 2.0 ** 100):
+        for new in ([1, 3], [300, 64]):
+            c = Case(iqq, [3000, 500], 1, 64, 64, 79)
+            c.cache.v_scales.mul_(size)
+            _check_attention(iqq, c, new, 4, BF16, scale=1.0)
