@@ -26,7 +26,8 @@
 // lengths by one scan.  So a ragged batch, one long sequence and many short ones all fill the
 // machine evenly.  A tile that lies in one share is finished there; of the others each share
 // leaves a part, normalized and with its log-sum, in the workspace (two a CTA at most: where its
-// share begins and where it ends), and combine_kernel joins them.
+// share begins and where it ends), and combine_kernel joins them.  Where the tables are short and the
+// tiles few, each CTA takes a whole tile instead: no parts, no workspace, one launch.
 //
 // Measured with inputs larger than L2: 32 sequences of 4096 tokens, 32 heads over 32 of 128 dimensions
 // 169 us (6.3 TB/s of 6.55); 64 up to 8000, 32 over 8: 97 us (5.4); one of 131000, 32 over 4: 37 us
@@ -54,7 +55,8 @@ constexpr int kKeys = 128;                  // keys of a stage: 32 a warp
 constexpr int kMaxCtas = 1024;
 
 struct Args : iqq::Attend {
-    struct Mark* marks;  // [gridDim.x]; parts are [gridDim.x][2][row tile][head_dim], log-sums [..][2][row tile]
+    // [gridDim.x]; parts are [gridDim.x][2][row tile][head_dim], log-sums [..][2][row tile].  Null: a tile a CTA.
+    struct Mark* marks;
 };
 
 // The launch's stages in equal shares: `each`, and one more for the first `more` CTAs.
@@ -145,7 +147,7 @@ struct Smem {
     float ks[kStages][kKeys / 16], vs[kStages][kKeys / 16];
     int live[kStages];              // which 16 keys have a page, a bit each
     uint64_t full[kStages], empty[kStages];
-    int64_t scan[kWarps + 1], offset;
+    int64_t scan[kWarps + 1], offset, left;
     int first, abort;
 };
 
@@ -285,15 +287,18 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // Where this CTA's share begins: a scan over the sequences, a run of them a thread.
+    // Where this CTA's share begins: a scan over the sequences, a run of them a thread, in stages (or in
+    // tiles, where a CTA takes one).
     Walk<kRows> walk;
     {
+        const bool whole = A.marks == nullptr;
+        const auto parts_of = [&](const Seq<kRows>& q) { return whole ? static_cast<int64_t>(q.tiles) * C.heads : q.all; };
         const int run = (C.n_seqs + kThreads + 31) / (kThreads + 32), b0 = min(C.n_seqs, tid * run), b1 = min(C.n_seqs, b0 + run);
         int64_t sum = 0;
         bool bad = false;
         for (int b = b0; b < b1; ++b) {
             const Seq<kRows> q(C, b, A.group);
-            sum += q.all;
+            sum += parts_of(q);
             bad |= !q.s.ok || q.s.len > C.capacity;
         }
         if (bad && blockIdx.x == 0) iqq::raise_flags(flags, IQQ_FLAG_BAD_INDEX);
@@ -313,34 +318,37 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
         before -= sum;
         const Shares shares(total, gridDim.x);
-        const int64_t start = shares.start(blockIdx.x), end = shares.start(blockIdx.x + 1);
+        const int64_t start = whole ? blockIdx.x : shares.start(blockIdx.x);
         if (start >= before && start < before + sum) {
             int64_t at = start - before;
             int b = b0;
             Seq<kRows> q(C, b, A.group);
-            while (at >= q.all) {
-                at -= q.all;
+            while (at >= parts_of(q)) {
+                at -= parts_of(q);
                 q = Seq<kRows>(C, ++b, A.group);
             }
             S.first = b;
-            S.offset = at;
-            Mark M;
-            int32_t stage, row_tile;
-            q.place(at, M.head, row_tile, stage);
-            M.t0 = start - stage;
-            M.t1 = M.t0 + q.stages;
-            M.shares = shares;
-            M.token = q.s.first;
-            M.row0 = row_tile * kRows;
-            M.rows = min(kRows, q.rows - M.row0);
-            A.marks[blockIdx.x] = M;
-        } else if (start >= total && tid == 0) {  // more CTAs than stages: an empty share at the end
+            S.offset = whole ? at * q.stages : at;
+            S.left = whole ? q.stages : shares.start(blockIdx.x + 1) - start;
+            if (!whole) {
+                Mark M;
+                int32_t stage, row_tile;
+                q.place(at, M.head, row_tile, stage);
+                M.t0 = start - stage;
+                M.t1 = M.t0 + q.stages;
+                M.shares = shares;
+                M.token = q.s.first;
+                M.row0 = row_tile * kRows;
+                M.rows = min(kRows, q.rows - M.row0);
+                A.marks[blockIdx.x] = M;
+            }
+        } else if (!whole && start >= total && tid == 0) {  // more CTAs than stages: an empty share at the end
             A.marks[blockIdx.x].t0 = A.marks[blockIdx.x].t1 = start;
         }
         __syncthreads();
         walk.b = S.first;
         walk.at = S.offset;
-        walk.left = walk.b < 0 ? 0 : end - start;
+        walk.left = walk.b < 0 ? 0 : S.left;
     }
 
     Piece P;
@@ -786,8 +794,14 @@ combine_kernel(const Args A, const int ctas)
 //    64 dimensions  24 sequences up to 5000: 48 rows 76, 83; 62 rows 97, 82.     64 of 2000: 48 rows 124, 127; 62 rows 158, 127
 constexpr int64_t prompt_rows(int64_t head_dim) { return head_dim == 128 ? 33 : 49; }
 
+// Tables up to this many keys, and tiles that fit the machine at once: a CTA takes a whole tile.  Shares
+// and whole tiles, us on the device: 32 heads over 32, one sequence: 100 keys 8.9, 5.7; 600 keys 10.0, 10.0;
+// 1000 keys 11.2, 12.9 (and 15.0, 14.5 for 8 sequences over 8 heads; a call's host part is 4 us less).
+constexpr int64_t kWholeKeys = 1024;
+
 struct Plan {
     bool prompt;
+    bool whole;       // a tile a CTA
     int splits;       // of the prompt kernel
     int row_tile;     // rows a CTA
     int64_t ctas;     // shares
@@ -812,6 +826,11 @@ Plan plan_of(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int64_t n_hea
     const int64_t tiles = (n_tokens * group / p.row_tile + seqs->n_seqs) * cache->n_kv_heads;
     const int64_t stages = 1 + (seqs->table_width * cache->page_size + kKeys - 1) / kKeys;
     const int64_t most = std::min<int64_t>(kMaxCtas, (p.row_tile == 8 ? 3 : 2) * iqq::sm_count());
+    p.whole = tiles <= most && seqs->table_width * cache->page_size <= kWholeKeys;
+    if (p.whole) {
+        p.ctas = tiles;
+        return p;
+    }
     p.ctas = tiles >= most ? most : std::min<int64_t>(most, tiles * std::min<int64_t>(stages, most));
     p.marks = (static_cast<size_t>(p.ctas) * sizeof(Mark) + 15) / 16 * 16;
     p.part = static_cast<size_t>(p.ctas) * 2 * p.row_tile * cache->head_dim * sizeof(float);
@@ -852,7 +871,7 @@ iqq_status launch(const Kv8& C, const Args& A, const Plan& p, cudaStream_t st, u
         if (s != IQQ_OK) return s;
     }
     s = start(decode_kernel<T, D, NT>, dim3(static_cast<unsigned>(p.ctas)), kThreads + 32, smem, st, maps[0], maps[1], C, A, flags);
-    if (s != IQQ_OK || p.ctas == 1) return s;
+    if (s != IQQ_OK || p.whole || p.ctas == 1) return s;
     return start(combine_kernel<T, D, 8 * NT>, dim3(static_cast<unsigned>(p.ctas - 1), 4 * NT), 256, 0, st, A,
                  static_cast<int>(p.ctas));
 }
@@ -911,7 +930,7 @@ extern "C" iqq_status iqq_kv8_attention(const iqq_kv8_cache* cache, const iqq_kv
     A.scale = scale;
     char* ws = static_cast<char*>(workspace);
     A.splits = p.splits;
-    A.marks = reinterpret_cast<Mark*>(ws);
+    A.marks = p.whole ? nullptr : reinterpret_cast<Mark*>(ws);
     A.part = reinterpret_cast<float*>(ws + p.marks);
     A.part_lse = reinterpret_cast<float*>(ws + p.marks + p.part);
     cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -543,3 +543,28 @@ def test_attention_smallest_and_largest_value_scales(iqq):
             c = Case(iqq, [3000, 500], 1, 64, 64, 79)
             c.cache.v_scales.mul_(size)
             _check_attention(iqq, c, new, 4, BF16, scale=1.0)
+
+
+def test_captured_tokens_over_long_and_short_tables(iqq):
+    """Single tokens, captured over tables wider than the lengths (shares of stages) and as narrow as
+    they (a tile a CTA), replayed on new q and lengths: the same values as uncaptured, within the
+    bounds both ways."""
+    c = Case(iqq, [4000, 900, 1000], 2, 128, 64, 83)
+    q, lens, cu = torch.zeros(3, 8, 128, dtype=F16, device="cuda"), _i32(c.lens), _cu([1, 1, 1])
+    short = c.tables[:, :16]
+    assert iqq.kv8_attention_workspace_bytes(c.cache, 3, c.tables.shape[1], 8, 3) > 0
+    assert iqq.kv8_attention_workspace_bytes(c.cache, 3, 16, 8, 3) == 0
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        wide = iqq.kv8_attention(c.cache, q, c.tables, lens, cu)
+        narrow = iqq.kv8_attention(c.cache, q, short, lens, cu)
+    full = c.tables
+    for m in ([1000, 900, 1000], [1, 0, 130], [1024, 63, 64]):
+        q.copy_(c.randn(3, 8, 128))
+        lens.copy_(_i32(m))
+        graph.replay()
+        c.lens = m
+        for tables, out in ((full, wide), (short, narrow)):
+            c.tables = tables
+            assert torch.equal(out, _check_attention(iqq, c, [1, 1, 1], 8, F16, q=q))
