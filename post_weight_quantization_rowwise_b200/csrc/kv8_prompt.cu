@@ -16,8 +16,8 @@
 // finer), and the denominator as sum P / vs in binary32.  m moves only when a P passes 2^15, and only
 // then O is rescaled.  Bound by the tensor cores and, as nearly, by the exponentials (16 an SM and clock).
 // Measured: 8192 tokens, 32 heads over 8 of 128 dimensions 514 us (1069 TFLOP/s of 1650); chunks of 2000
-// and 1700 tokens after 3000 and 6300: 347 us (950); 16 prompts of 1000: 263 us (500: a CTA's first
-// loads and its output are a third of its time there).
+// and 1700 tokens after 3000 and 6300: 347 us (950); 16 prompts of 1000: 263 us (500: a CTA's
+// lookups, first loads and output are half of its time there).
 #include <math.h>
 
 #include <algorithm>
