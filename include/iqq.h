@@ -478,7 +478,7 @@ iqq_status iqq_quantize_i8_rows(int dtype, const void* x, int64_t ldx, int8_t* c
  *  y          [n_tok] rows of n_out values, ldy values apart (ldy >= n_out; ignored for one
  *             row), aligned to its type; must not overlap an input.  Values between the rows
  *             are left as they are.
- *  k          0 .. IQQ_GEMM_I8_MAX_K; k == 0 is the empty sum.
+ *  k          0 .. IQQ_GEMM_I8_MAX_K; k == 0 is the empty sum (a, w, lda and ldw are not looked at).
  *  d_flags    optional; receives IQQ_FLAG_WAIT_TIMEOUT.
  */
 #define IQQ_GEMM_I8_MAX_K 131071
