@@ -108,9 +108,10 @@ def _lengths(case):
 
 
 def _quantize(x):
-    """The rows' codes (in binary64: a quotient next to a half decides a code) and scales."""
+    """The rows' codes (in binary64: a quotient next to a half decides a code) and scales (one rounding
+    of amax/127: in binary32 a device tensor over a number is a product with fl32(1/127), often an ulp off)."""
     amax = x.abs().amax(-1).float()
-    d = torch.where(amax < TINY, torch.zeros_like(amax), amax / 127.0)
+    d = torch.where(amax < TINY, torch.zeros_like(amax), (amax.double() / 127.0).float())
     q = torch.round(x.double() / torch.where(d > 0, d, torch.ones_like(d)).double()[..., None])
     return torch.where((d > 0)[..., None], q, torch.zeros_like(q)), d
 
@@ -204,7 +205,7 @@ def _plain_append(s, name):
     seq, pos = _spans(s["cu"], s["lens"], s["total"])
     where = s["tables"].long()[seq, pos // page]
     amax = x.abs().amax(-1)
-    need = torch.where(amax < TINY, torch.zeros_like(amax), amax / 127.0)
+    need = torch.where(amax < TINY, torch.zeros_like(amax), (amax.double() / 127.0).float())
     # only the first page that a sequence's new tokens reach can hold older ones
     start = s["lens"].long() - (s["cu"][1:] - s["cu"][:-1]).long()
     first = s["tables"].long().gather(1, (start // page).clamp(max=s["width"] - 1)[:, None])[:, 0]
