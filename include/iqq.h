@@ -571,7 +571,8 @@ iqq_status iqq_kv8_gather(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, 
  *     out = sum_j p_j v_j,  p = softmax_j(scale * q . k_j),  j <= seq_lens[b] - n_b + i,
  * where k_j and v_j are the cache's values (scale * code).  One token a sequence is a decoding
  * step; many are a prompt's chunk or drafted tokens.  A row that sees no token (n_b >
- * seq_lens[b]) gives out = 0 and lse = -Inf.
+ * seq_lens[b]) gives out = 0 and lse = -Inf.  A row that sees tokens, but whose scores are all
+ * -Inf in binary32 (an infinity in q, products beyond its range), is NaN, its lse too.
  *
  *  dtype       IQQ_BF16 or IQQ_F16: the type of q and out.
  *  q           [n_tokens][n_heads][head_dim], strides as for k of iqq_kv8_append.

@@ -82,6 +82,16 @@ __device__ __forceinline__ int page_at(const Kv8& C, int b, int64_t index)
     return p >= 0 && p < C.n_pages ? p : -1;
 }
 
+// Whether one of the keys j0 .. j1-1 of sequence b (j1 within its table) has a page.  Asked where a row's
+// sum of weights is 0 or NaN: its scores may all be -Inf (an infinity in q, products beyond binary32),
+// whose softmax is NaN, or it saw no key.
+__device__ __forceinline__ bool any_page(const Kv8& C, int b, int64_t j0, int64_t j1)
+{
+    for (int64_t index = j0 >> C.page_log2; (index << C.page_log2) < j1; ++index)
+        if (page_at(C, b, index) >= 0) return true;
+    return false;
+}
+
 // What both attention kernels take: q, the outputs, and n_heads = group * key/value heads.
 struct Attend {
     const void* q;
@@ -97,7 +107,10 @@ struct Attend {
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNone = -3.4028234663852886e38f;  // the maximum of no score: below every finite one
+// The maximum of no score: below every finite one.  As a part's log-sum it says that the part's scores are
+// all -Inf: it has no weight beside a part with finite ones, and where all parts say so the row is NaN
+// (a part that saw no key says -Inf).
+constexpr float kNone = -3.4028234663852886e38f;
 
 // The weights 2^(y - m) go to the products in binary16, where a value below 2^-14 rounds by an
 // absolute 2^-25.  So the reference m is kept kLift below the largest y when it moves, and moves

@@ -430,6 +430,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const int clear = static_cast<int>(max(int64_t{0}, min(clear64, int64_t{0x7fffffff})));
 
     float m[NT][2], l[NT][2], o[NT][kM][4], vref = 0.0f, vinv = 1.0f;
+    uint32_t sees = 0;  // rows that had a key here, a bit each
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -501,7 +502,10 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (dead || key0 + 16 * u + g + (e & 2) * 4 >= limit[n][e & 1]) x[u][n][e] = -INFINITY;
+                        else sees |= 1u << (2 * n + (e & 1));
             }
+        } else {
+            sees = ~0u;
         }
         bool moved = false;
         float top[NT][2];
@@ -606,6 +610,9 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+            // Keys without a weight: next to nothing, lost in any other sum.  Where all scores of a row are
+            // -Inf it stays the sum, with m still kNone.
+            if (l[n][h] == 0.0f && (sees >> (2 * n + h) & 1)) l[n][h] = 0x1p-126f;
             l[n][h] += __shfl_xor_sync(0xffffffffu, l[n][h], 4);
             l[n][h] += __shfl_xor_sync(0xffffffffu, l[n][h], 8);
             l[n][h] += __shfl_xor_sync(0xffffffffu, l[n][h], 16);
@@ -667,9 +674,9 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             for (int h = 0; h < 2; ++h) {
                 const int32_t r = 8 * n + 2 * t + h, row = first_row + r;
                 if (row >= rows) continue;
-                const bool none = m[n][h] == kNone && l[n][h] == 0.0f;
-                const float inv = none ? 0.0f : __fdiv_rn(1.0f, l[n][h]);
-                const float lse = none ? -INFINITY : m[n][h] + log2f(l[n][h]);
+                const bool none = l[n][h] == 0.0f, flat = whole && m[n][h] == kNone;
+                const float inv = none ? 0.0f : (flat ? NAN : __fdiv_rn(1.0f, l[n][h]));
+                const float lse = none ? -INFINITY : (flat ? NAN : m[n][h] + log2f(l[n][h]));
                 const int32_t token = row / A.group;
                 const int64_t at = static_cast<int64_t>(s.first + token) * A.heads + kvh * A.group + row - token * A.group;
                 if (whole) {
@@ -782,6 +789,7 @@ combine_kernel(const Args A, const int ctas)
         acc = fmaf(s_o[half][w][d], f, acc);
     }
     const bool none = top == kNone && sum == 0.0f;
+    if (top == kNone && !none) sum = NAN;  // parts whose scores are all -Inf
     const int32_t row = M.row0 + r, token = row / A.group;
     const int64_t at = static_cast<int64_t>(M.token + token) * A.heads + M.head * A.group + row - token * A.group;
     static_cast<T*>(A.out)[at * D + d] = iqq::from_f32<T>(none ? 0.0f : __fdiv_rn(acc, sum));

@@ -432,7 +432,7 @@ __device__ __forceinline__ void put_rows(Smem<D>& S, int t, uint32_t o_at, float
 }
 
 template <class T, int D>
-__device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& W, uint32_t tmem, int t)
+__device__ __forceinline__ bool attend(Smem<D>& S, const Kv8& C, const Attend& A, const Work& W, uint32_t tmem, int t)
 {
     const int r = threadIdx.x & 127, row = W.row0 + t * kRows + r;
     const bool real = row < W.rows;
@@ -533,11 +533,19 @@ __device__ __forceinline__ bool attend(Smem<D>& S, const Attend& A, const Work& 
     const bool late = !iqq::bar_wait(iqq::smem_u32(&S.ofull[t]), 0);
     if (__any_sync(0xffffffffu, late)) return false;
     iqq::tc_fence_after();
-    const bool none = m == kNone && l == 0.0f;
-    const float inv = none ? 0.0f : __fdiv_rn(1.0f, l);
+    float inv = __fdiv_rn(1.0f, l), lse = m + log2f(l);
+    bool none = false;
+    if (real && !(l > 0.0f)) {  // (a NaN may come of q alone, where no key has a page)
+        const int64_t first_key = static_cast<int64_t>(W.tile0) * kKeys;
+        const bool sees = iqq::any_page(C, W.b, first_key, min(limit64, first_key + static_cast<int64_t>(n) * kKeys));
+        if (!sees || l == 0.0f) {
+            none = !sees || A.splits > 1;
+            inv = NAN;
+            lse = !sees ? -INFINITY : (A.splits > 1 ? kNone : NAN);
+        }
+    }
     if (A.splits > 1) put_rows<float, D>(S, t, o_at, inv, none, real ? A.part + part * D : nullptr);
     else put_rows<T, D>(S, t, o_at, inv, none, real ? static_cast<T*>(A.out) + at * D : nullptr);
-    const float lse = none ? -INFINITY : m + log2f(l);
     if (real && A.splits > 1) A.part_lse[part] = lse;
     else if (real && A.lse != nullptr) A.lse[at] = lse / kLog2e;
     return true;
@@ -614,7 +622,7 @@ prompt_kernel(const Kv8 C, const Attend A, uint32_t* __restrict__ flags)
     bool ok = true;
     if (warp < kMakers) {
         more_registers<kSoftmaxRegs>();
-        ok = attend<T, D>(S, A, W, tmem, warp >> 2);
+        ok = attend<T, D>(S, C, A, W, tmem, warp >> 2);
     } else if (warp < kMma) {
         fewer_registers<kMakerRegs>();
         ok = make_operands<D>(S, W.key_tiles());
@@ -670,6 +678,7 @@ join_kernel(const Kv8 C, const Attend A)
         for (int e = 0; e < kE; ++e) o[e] = fmaf(o[e], keep, w * v[e]);
     }
     const bool none = m == kNone && l == 0.0f;
+    if (m == kNone && !none) l = NAN;  // parts whose scores are all -Inf
     const int64_t token = row / A.group, at = (s.first + token) * A.heads + head * A.group + row - token * A.group;
 #pragma unroll
     for (int e = 0; e < kE; ++e)

@@ -568,3 +568,41 @@ def test_captured_tokens_over_long_and_short_tables(iqq):
         for tables, out in ((full, wide), (short, narrow)):
             c.tables = tables
             assert torch.equal(out, _check_attention(iqq, c, [1, 1, 1], 8, F16, q=q))
+
+
+@pytest.mark.parametrize("lens,new", [([1], [1]), ([200, 90, 1], [1, 1, 1]), ([5000], [1]), ([300, 4], [3, 2]),
+                                      ([260, 1], [260, 1]), ([9000], [100])])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attention_rows_whose_scores_are_all_minus_infinity(iqq, lens, new, dim):
+    """Keys of one sign, so that an infinity in q, or products beyond binary32, give every visible score
+    the value -Inf: the softmax of such a row is NaN, and so is its log-sum; zeros and -Inf belong to
+    rows that see nothing.  Every form of the launch: whole tiles, shares, prompts, split keys."""
+    c = Case(iqq, lens, 1, dim, 64, 91)
+    c.cache.k_codes.clamp_(min=1)
+    q = c.randn(sum(new), 4, dim, dtype=BF16)
+    q[:, 1, 5] = -math.inf
+    q[:, 2] = -3.0e38
+    c.cache.k_scales.mul_(64.0)
+    out = torch.full_like(q, 7.0)
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    need = iqq.kv8_attention_workspace_bytes(c.cache, len(new), c.tables.shape[1], 4, sum(new))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    iqq.iqq_kv8_attention(c.cache, q, c.tables, _i32(lens), _cu(new), out, lse=lse, workspace=ws, scale=4.0)
+    assert out[:, 1:3].isnan().all() and lse[:, 1:3].isnan().all()
+    assert torch.isfinite(out[:, ::3]).all() and torch.isfinite(lse[:, ::3]).all()
+
+
+def test_attention_rows_that_see_nothing_with_infinities(iqq):
+    """More rows than tokens, q infinite: the rows that see no token give zeros and -Inf all the same,
+    and so do rows whose only pages have no place."""
+    for lens, new in (([2, 70], [4, 3]), ([30, 40], [90, 200])):
+        c = Case(iqq, lens, 1, 64, 16, 93)
+        c.cache.k_codes.clamp_(min=1)
+        q = torch.full((sum(new), 2, 64), -math.inf, device="cuda").to(BF16)
+        lse = torch.zeros(sum(new), 2, device="cuda")
+        out = iqq.kv8_attention(c.cache, q, c.tables, _i32(lens), _cu(new), lse=lse)
+        pos = torch.cat([torch.arange(n, device="cuda") + m - n for m, n in zip(lens, new)])
+        assert (out[pos < 0] == 0).all() and (lse[pos < 0] == -math.inf).all()
+        assert out[pos >= 0].isnan().all() and lse[pos >= 0].isnan().all()
+        out = iqq.kv8_attention(c.cache, q, torch.full_like(c.tables, -1), _i32(lens), _cu(new), lse=lse)
+        assert (out == 0).all() and (lse == -math.inf).all()
