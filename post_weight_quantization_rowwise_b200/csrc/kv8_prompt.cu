@@ -37,7 +37,8 @@ using iqq::Span;
 using iqq::sub_h2;
 
 constexpr int kRows = 128, kTiles = 2, kKeys = 128, kStages = 2 /* a power of two */, kScales = 4;
-constexpr int kMakers = 8, kMma = 12, kLoader = 13;  // first warp that makes operands; the ones that multiply and load
+// First warp that makes operands; the ones that multiply, load and turn the pages' scales into factors.
+constexpr int kMakers = 8, kMma = 12, kLoader = 13, kScaler = 14;
 constexpr int kThreads = 32 * 16;
 // Registers a thread of the softmax, the makers and the rest (the launch's are shared out anew); where
 // the rest spill, so does the time (8192 tokens of 32 heads over 8: 650 us with 40 for them).
@@ -170,6 +171,49 @@ __device__ __forceinline__ bool load(Smem<D>& S, const Kv8& C, const Work& W, in
     return ok;
 }
 
+// ---- the warp that makes the scales' factors ----
+
+// Codes of a value scale that counts as 0 are made 0, so any scale does in their weights, if it neither
+// moves m above what other pages need (as low as 2^-40, or as the lowest seen) nor takes the weights out
+// of binary32 beside the largest (2^-100 of it).
+template <int D>
+__device__ __forceinline__ bool make_scales(Smem<D>& S, int n)
+{
+    const int lane = threadIdx.x & 31;
+    float lo = -40.0f, hi = -40.0f;  // log2 of the smallest and the largest value scale so far
+    for (int j = 0; j < n; ++j) {
+        const int c = j % kScales;  // (its last reader is four tiles back: that tile's weights met their values before this one was loaded)
+        const bool late = !iqq::bar_wait(iqq::smem_u32(&S.rfull[0]), j & 1);
+        if (__any_sync(0xffffffffu, late)) return false;
+        const bool has = lane < kKeys / 16 && (S.live[0] >> lane & 1);
+        const float vs = has ? S.rawvs[lane] : 0.0f, ks = has ? S.rawks[lane] : 0.0f;
+        __syncwarp();
+        if (lane == 0) iqq::bar_arrive(iqq::smem_u32(&S.rempty[0]));
+        float here = vs;
+        if (vs >= kTinyScale) {
+            here = log2f(vs);
+            lo = fminf(lo, here);
+            hi = fmaxf(hi, here);
+        }
+        if (__any_sync(0xffffffffu, has && vs < kTinyScale)) {
+#pragma unroll
+            for (int o = 1; o < kKeys / 16; o *= 2) {
+                lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+                hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+            }
+            if (vs < kTinyScale) here = fmaxf(lo, hi - 100.0f);
+        }
+        if (lane < kKeys / 16) {
+            S.ks[c][lane] = ks;
+            S.lv[c][lane] = has ? here : -INFINITY;                       // no page: hidden
+            S.rv[c][lane] = has ? (vs == vs ? ex2(-here) : 1.0f) : 0.0f;  // (0 weights of NaN pages stay 0)
+        }
+        __syncwarp();
+        if (lane == 0) iqq::bar_arrive(iqq::smem_u32(&S.scaled[c]));
+    }
+    return true;
+}
+
 // ---- the warps that make the operands ----
 
 // This thread's pieces of a raw tile, to binary16, swizzled.
@@ -195,9 +239,8 @@ __device__ __forceinline__ bool make_operands(Smem<D>& S, int n)
 {
     constexpr int kChunks = D / 16;  // 16-byte pieces of a token, and a thread's of a tile
     const int tid = threadIdx.x - 32 * kMakers, lane = tid & 31;
-    float lv = 0.0f;  // log2 of the last value scale that was not 0
     for (int j = 0; j < n; ++j) {
-        const int s = j % kStages, c = j % kScales;
+        const int s = j % kStages;
         const uint32_t ph = (j / kStages) & 1;
         uint32_t zero = 0;  // the 16 keys whose value scale is 0
 #pragma unroll 1  // (the code of all roles together has to stay in the instruction caches)
@@ -207,17 +250,6 @@ __device__ __forceinline__ bool make_operands(Smem<D>& S, int n)
             uint32_t live = S.live[which];
             if (which == 0) {
                 zero = __ballot_sync(0xffffffffu, lane < kKeys / 16 && S.rawvs[lane & 7] < kTinyScale);
-                if (tid < kKeys / 16) {
-                    const bool has = live >> tid & 1;
-                    const float vs = has ? S.rawvs[tid] : 0.0f;
-                    if (vs >= kTinyScale) lv = log2f(vs);  // (below, the codes count as 0: any scale will do in the weights)
-                    const float here = vs == vs ? lv : vs;
-                    S.ks[c][tid] = has ? S.rawks[tid] : 0.0f;
-                    S.lv[c][tid] = has ? here : -INFINITY;  // no page: hidden
-                    S.rv[c][tid] = has ? (vs == vs ? ex2(-here) : 1.0f) : 0.0f;  // (0 weights of NaN pages stay 0)
-                }
-                __syncwarp();
-                if (tid == 0) iqq::bar_arrive(iqq::smem_u32(&S.scaled[c]));
             } else {
                 live &= ~zero;
             }
@@ -504,8 +536,9 @@ __device__ __forceinline__ bool attend(Smem<D>& S, const Kv8& C, const Attend& A
                 if (!__any_sync(0xffffffffu, over)) break;
                 const float top = masked ? row_top<true>(s_at, ks, lv, unscale, limit) : row_top<false>(s_at, ks, lv, unscale, limit);
                 const float to = top - iqq::kLift, next = over || to > m + iqq::kMove ? fmaxf(m, to) : m, f = ex2(m - next);
+                const float root = ex2(0.5f * (m - next));  // (f may be below binary32, where zero pages made l large)
                 m = next;
-                l *= f;
+                l = l * root * root;
                 if (j > 0) {
 #pragma unroll
                     for (int i = 0; i < D / 32; ++i) {
@@ -600,7 +633,7 @@ prompt_kernel(const Kv8 C, const Attend A, uint32_t* __restrict__ flags)
         }
         for (int i = 0; i < 2; ++i) {
             iqq::bar_init(iqq::smem_u32(&S.rfull[i]), 33);  // expect_tx, and the lanes' scales
-            iqq::bar_init(iqq::smem_u32(&S.rempty[i]), 4);
+            iqq::bar_init(iqq::smem_u32(&S.rempty[i]), i == 0 ? 5 : 4);  // the makers; of the keys the scales' warp, too
         }
         for (int i = 0; i < kScales; ++i) iqq::bar_init(iqq::smem_u32(&S.scaled[i]), 1);
         for (int i = 0; i < kTiles; ++i) {
@@ -630,6 +663,8 @@ prompt_kernel(const Kv8 C, const Attend A, uint32_t* __restrict__ flags)
         fewer_registers<kOtherRegs>();
         if (warp == kLoader) {
             ok = load<D>(S, C, W, W.key_tiles(), end, flags);
+        } else if (warp == kScaler) {
+            ok = make_scales<D>(S, W.key_tiles());
         } else if (warp == kMma) {
             ok = multiply<D>(S, W, tmem);
             // nothing is left running when the tensor memory goes

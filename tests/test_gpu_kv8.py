@@ -606,3 +606,65 @@ def test_attention_rows_that_see_nothing_with_infinities(iqq):
         assert out[pos >= 0].isnan().all() and lse[pos >= 0].isnan().all()
         out = iqq.kv8_attention(c.cache, q, torch.full_like(c.tables, -1), _i32(lens), _cu(new), lse=lse)
         assert (out == 0).all() and (lse == -math.inf).all()
+
+
+def _check_scales(iqq, c, new, heads, dtype, q):
+    """Attention where value scales lie far apart.  The weights p_j times their page's value scale are
+    rounded to binary16, 2^-11 of each or 2^-31 of the row's largest such product (a page of zeros counts
+    as the scale 2^-40 there, or 2^-100 of the largest): a code of 127 in each of the keys."""
+    out = iqq.kv8_attention(c.cache, q, c.tables, _i32(c.lens), _cu(new))
+    u, at = torch.finfo(dtype).eps / 2, 0
+    for b, n in enumerate(new):
+        for h in range(heads):
+            k, v = c.values(b, 0, h // (heads // c.kv)), c.values(b, 1, h // (heads // c.kv))
+            cells = c.tables[b, :-(-c.lens[b] // c.page)].long()
+            vs = c.cache.v_scales[cells, h // (heads // c.kv)].double().repeat_interleave(c.page)[:c.lens[b]]
+            seen = torch.arange(c.lens[b], device="cuda")[None] <= c.lens[b] - n + torch.arange(n, device="cuda")[:, None]
+            qh = q[at:at + n, h].double()
+            s = (qh @ k.t() * c.dim ** -0.5).masked_fill(~seen, -math.inf)
+            big = (qh.abs() @ k.abs().t() * c.dim ** -0.5).amax(1)
+            p = torch.softmax(s, 1)
+            ref, mass = p @ v, p @ v.abs()
+            as_if = torch.where(vs > 0, vs, max(2.0 ** -40, 2.0 ** -100 * float(vs.max())))
+            bound = mass * (u + 2 * (c.dim + 8) * 2.0 ** -24 * big[:, None] + (c.lens[b] + 64) * 2.0 ** -24)
+            bound = bound + c.lens[b] * 127 * 2.0 ** -31 * (p * as_if).amax(1)[:, None] + u * ref.abs() * (1 + u) + STEP[dtype]
+            off = (out[at:at + n, h].double() - ref).abs()
+            assert (off <= bound).all(), (b, h, float((off / bound).max()))
+        at += n
+
+
+def _zero_pages_before_small_values(iqq, new, small):
+    """Pages of zeros (scale 0), then values whose scales are near 2^small, which bfloat16 holds; one of
+    the sequences begins with such zeros, the other has them behind a page of the scale 1 that gets
+    next to no weight."""
+    c = Case(iqq, [640, 500], 1, 64, 64, 97)
+    c.cache.v_scales.mul_(100.0 * 2.0 ** small)
+    c.cache.v_scales[c.tables[0, :5].long()] = 0.0
+    c.cache.v_scales[c.tables[1, 1:3].long()] = 0.0
+    c.cache.v_scales[c.tables[1, 0].long()] = 1.0
+    c.cache.k_codes[c.tables[1, 0].long()] = -127
+    q = c.randn(sum(new), 2, 64, dtype=BF16)
+    at = sum(new[:1])
+    q[at:] = q[at:].abs() + 6.0
+    c.cache.k_codes[c.tables[1, 1:].long()] = c.cache.k_codes[c.tables[1, 1:].long()] // 16
+    c.cache.k_scales.fill_(0.02)
+    _check_scales(iqq, c, new, 2, BF16, q)
+
+
+def _zero_pages_beside_the_largest_values(iqq, new):
+    """Pages of zeros before, between and behind pages of scales near 2^93: they keep their share of the
+    weights."""
+    c = Case(iqq, [900], 1, 64, 64, 103)
+    c.cache.v_scales.mul_(2.0 ** 100)
+    c.cache.v_scales[c.tables[0, [0, 1, 6, 14]].long()] = 0.0
+    q = c.randn(new[0], 2, 64, dtype=BF16)
+    _check_scales(iqq, c, new, 2, BF16, q)
+
+
+@pytest.mark.parametrize("small", [-21, -32, -45, -70])
+def test_prompts_with_zero_pages_before_small_values(iqq, small):
+    _zero_pages_before_small_values(iqq, [300, 200], small)
+
+
+def test_prompts_with_zero_pages_beside_the_largest_values(iqq):
+    _zero_pages_beside_the_largest_values(iqq, [150])
