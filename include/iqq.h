@@ -586,9 +586,11 @@ iqq_status iqq_kv8_gather(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, 
  *  d_flags     optional; IQQ_FLAG_BAD_INDEX (a page without a place, and tokens beyond
  *              table_width * page_size, are not attended to; the rows of a bad span are left as
  *              they are), IQQ_FLAG_WAIT_TIMEOUT.
- * Scores, sums and the softmax's maximum are binary32; the weights p_j meet the codes in binary16
- * (2^-11 of each, or 2^-31 of the largest), whatever the dtype.  A page whose scale is NaN makes
- * the rows that see it NaN, and no others; a value scale below 2^-90 may count as 0.
+ * Scores, sums and the softmax's maximum are binary32; the weights p_j, times their page's value
+ * scale, meet the codes in binary16, whatever the dtype: 2^-11 of each such product, or 2^-31 of the
+ * row's largest (where a page of the value scale 0 counts as 2^-40, or 2^-100 of the largest scale).
+ * A page whose scale is NaN makes the rows that see it NaN, and no others; a value scale below 2^-90
+ * may count as 0.
  * The launch is laid out for the average number of tokens a sequence: a batch of single tokens or
  * drafts beside prompts is right in one call, but faster in two.  A narrower view of the block
  * tables (table_width) bounds the lengths that are looked at, and the workspace.

@@ -112,6 +112,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // (a part that saw no key says -Inf).
 constexpr float kNone = -3.4028234663852886e38f;
 
+constexpr float kTinyScale = 8.077935669463161e-28f;  // 2^-90: a value scale below it counts as 0, so denominators stay finite
+
 // The weights 2^(y - m) go to the products in binary16, where a value below 2^-14 rounds by an
 // absolute 2^-25.  So the reference m is kept kLift below the largest y when it moves, and moves
 // only when a y comes kMove further: the largest weight is 2^7 to 2^15 (of 65504), and a weight

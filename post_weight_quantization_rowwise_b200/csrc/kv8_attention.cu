@@ -16,10 +16,11 @@
 // byte b of a code c, in the low byte of 0x6400, is the binary16 1152 + c after b ^= 0x80, and
 // 1152 is subtracted.  Rows of q become binary16 exactly as well, by a power of two for each row
 // that brings its largest value near 2^14 (values below 2^-38 of it round, which is beyond the
-// binary32 sums).  The weights p_j are rounded to binary16, times the page's value scale over a
-// power of two that follows the largest such scale: 2^-11 each, as fine as the output's type or
-// finer.  m is the running maximum less 7 (see kLift) and moves only when a weight passes 2^15, so
-// a block costs one vote.
+// binary32 sums).  With vs = f 2^v the page's value scale, f from 1/2 to 1, the weights that meet the
+// codes are f 2^(y - m), y = s log2(e) + v, rounded to binary16: 2^-11 of each, as fine as the output's
+// type or finer.  m is the running maximum of y less 7 (see kLift), so large values without weight cost
+// the others no bits; it moves only when a weight passes 2^15, so a block costs one vote.  The
+// denominator is the sum of 2^(y - m) 2^-v, in binary32.
 //
 // Every launch is one wave of CTAs, and each takes an equal share of the work: the stages of all
 // sequences, heads and row tiles laid end to end, in an order that every CTA works out from the
@@ -429,8 +430,9 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const int64_t clear64 = min(len, s.start + first_row / A.group + 1) - j0;
     const int clear = static_cast<int>(max(int64_t{0}, min(clear64, int64_t{0x7fffffff})));
 
-    float m[NT][2], l[NT][2], o[NT][kM][4], vref = 0.0f, vinv = 1.0f;
+    float m[NT][2], l[NT][2], o[NT][kM][4];
     uint32_t sees = 0;  // rows that had a key here, a bit each
+    int hi = 86;  // biased exponent of the largest value scale so far
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -455,7 +457,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         const uint8_t* kp = &S.stage[st][32 * warp * D];
         const uint8_t* vp = kp + Sm::kHalf;
         // scores: x[u][n] of keys 16u + g and 16u + g + 8 (elements 0, 1 and 2, 3), rows 2t, 2t+1
-        float x[2][NT][4], vs[2];
+        const int live = S.live[st] >> (2 * warp);
+        float x[2][NT][4], vf[2], rv[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
 #pragma unroll
@@ -483,20 +486,30 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                     for (int n = 0; n < NT; ++n) mma(x[u][n], a0, a1, a2, a3, bq[n][4 * h + c][0], bq[n][4 * h + c][1]);
                 }
             }
-            const float ks = S.ks[st][2 * warp + u];
-            vs[u] = S.vs[st][2 * warp + u];
+            const float ks = S.ks[st][2 * warp + u], vs = live >> u & 1 ? S.vs[st][2 * warp + u] : 1.0f;
+            int exp = static_cast<int>(__float_as_uint(vs) >> 23);  // of vs = vf 2^(exp - 126)
+            vf[u] = __uint_as_float((__float_as_uint(vs) & 0x007fffffu) | 0x3f000000u);
+            if (vs >= iqq::kTinyScale) {  // (all of this is the same in all lanes)
+                hi = max(hi, exp);
+            } else {
+                // Codes of a scale that counts as 0 have no part in the sums, so any scale does in their
+                // weights, if it neither moves m above what other pages need (2^-40) nor takes the weights
+                // out of binary32 beside the largest scale (2^-100 of it).
+                exp = max(86, hi - 100);
+                vf[u] = 0.0f;
+            }
+            rv[u] = __uint_as_float(static_cast<uint32_t>(253 - exp) << 23);
+            const float v = vs == vs ? static_cast<float>(exp - 126) : vs;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[u][n][e] *= unscale[n][e & 1] * ks;
+                for (int e = 0; e < 4; ++e) x[u][n][e] = fmaf(x[u][n][e], unscale[n][e & 1] * ks, v);
         }
-        const int live = S.live[st] >> (2 * warp);
         const bool masked = key0 + 32 > clear || (live & 3) != 3;
         if (masked) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const bool dead = !(live >> u & 1);
-                if (dead) vs[u] = 0.0f;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -525,9 +538,9 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                    const float f = ex2(m[n][h] - v);
+                    const float root = ex2(0.5f * (m[n][h] - v)), f = root * root;
                     m[n][h] = v;
-                    l[n][h] *= f;
+                    l[n][h] = l[n][h] * root * root;  // (f may be below binary32, where zero pages made l large)
 #pragma unroll
                     for (int d = 0; d < kM; ++d) {
                         o[n][d][h] *= f;
@@ -535,36 +548,18 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                     }
                 }
         }
-        if (vs[0] > vref || vs[1] > vref) {  // (uniform) the next power of two above the larger
-            const uint32_t up = (__float_as_uint(fmaxf(vs[0], vs[1])) & 0x7f800000u) + 0x00800000u;
-            const float f = vref * __uint_as_float(0x7f000000u - up);  // over a power of two: exact
-            vref = __uint_as_float(up);
-            vinv = __uint_as_float(0x7f000000u - up);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int d = 0; d < kM; ++d)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[n][d][e] *= f;
-        }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const float vf = vs[u] * vinv;
             uint32_t bp[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float p[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) p[e] = ex2(x[u][n][e] - m[n][e & 1]);
-                l[n][0] += p[0] + p[2];
-                l[n][1] += p[1] + p[3];
+                l[n][0] = fmaf(p[0] + p[2], rv[u], l[n][0]);
+                l[n][1] = fmaf(p[1] + p[3], rv[u], l[n][1]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] *= vf;
-                if (masked) {  // (a hidden key's page may have the scale NaN)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (x[u][n][e] == -INFINITY) p[e] = 0.0f;
-                }
+                for (int e = 0; e < 4; ++e) p[e] *= vf[u];
                 bp[n][0] = transpose8(pack_h2(p[0], p[1]));
                 bp[n][1] = transpose8(pack_h2(p[2], p[3]));
             }
@@ -612,7 +607,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         for (int h = 0; h < 2; ++h) {
             // Keys without a weight: next to nothing, lost in any other sum.  Where all scores of a row are
             // -Inf it stays the sum, with m still kNone.
-            if (l[n][h] == 0.0f && (sees >> (2 * n + h) & 1)) l[n][h] = 0x1p-126f;
+            if (l[n][h] == 0.0f && (sees >> (2 * n + h) & 1)) l[n][h] = 0x1p-149f;
             l[n][h] += __shfl_xor_sync(0xffffffffu, l[n][h], 4);
             l[n][h] += __shfl_xor_sync(0xffffffffu, l[n][h], 8);
             l[n][h] += __shfl_xor_sync(0xffffffffu, l[n][h], 16);
@@ -630,7 +625,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                     }
 #pragma unroll
                 for (int d = 0; d < kM; ++d)
-                    S.o[warp - step][n * kM + d][lane] = make_float4(o[n][d][0] * vref, o[n][d][1] * vref, o[n][d][2] * vref, o[n][d][3] * vref);
+                    S.o[warp - step][n * kM + d][lane] = make_float4(o[n][d][0], o[n][d][1], o[n][d][2], o[n][d][3]);
             }
         }
         meet();
@@ -642,11 +637,11 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float mo = S.m[warp][8 * n + 2 * t + h], v = fmaxf(m[n][h], mo);
-                    own[h] = ex2(m[n][h] - v);
-                    other[h] = ex2(mo - v);
-                    l[n][h] = fmaf(l[n][h], own[h], S.l[warp][8 * n + 2 * t + h] * other[h]);
+                    const float r = ex2(0.5f * (m[n][h] - v)), ro = ex2(0.5f * (mo - v));
+                    l[n][h] = l[n][h] * r * r + S.l[warp][8 * n + 2 * t + h] * ro * ro;
                     m[n][h] = v;
-                    own[h] *= vref;
+                    own[h] = r * r;
+                    other[h] = ro * ro;
                 }
 #pragma unroll
                 for (int d = 0; d < kM; ++d) {
@@ -657,7 +652,6 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                     o[n][d][3] = fmaf(o[n][d][3], own[1], v.w * other[1]);
                 }
             }
-            vref = 1.0f;
         }
         meet();
     }
@@ -674,9 +668,9 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             for (int h = 0; h < 2; ++h) {
                 const int32_t r = 8 * n + 2 * t + h, row = first_row + r;
                 if (row >= rows) continue;
-                const bool none = l[n][h] == 0.0f, flat = whole && m[n][h] == kNone;
-                const float inv = none ? 0.0f : (flat ? NAN : __fdiv_rn(1.0f, l[n][h]));
-                const float lse = none ? -INFINITY : (flat ? NAN : m[n][h] + log2f(l[n][h]));
+                const bool none = l[n][h] == 0.0f, flat = m[n][h] == kNone;
+                const float inv = none || (flat && !whole) ? 0.0f : (flat ? NAN : __fdiv_rn(1.0f, l[n][h]));
+                const float lse = none ? -INFINITY : (flat && whole ? NAN : m[n][h] + log2f(l[n][h]));
                 const int32_t token = row / A.group;
                 const int64_t at = static_cast<int64_t>(s.first + token) * A.heads + kvh * A.group + row - token * A.group;
                 if (whole) {

@@ -31,6 +31,7 @@ using iqq::Attend;
 using iqq::ex2;
 using iqq::kLog2e;
 using iqq::kNone;
+using iqq::kTinyScale;
 using iqq::Kv8;
 using iqq::pack_h2;
 using iqq::Span;
@@ -44,8 +45,6 @@ constexpr int kThreads = 32 * 16;
 // the rest spill, so does the time (8192 tokens of 32 heads over 8: 650 us with 40 for them).
 constexpr int kSoftmaxRegs = 192, kMakerRegs = 72, kOtherRegs = 56;
 constexpr int kRegs = 128 * (2 * kSoftmaxRegs + kMakerRegs + kOtherRegs);
-
-constexpr float kTinyScale = 8.077935669463161e-28f;  // 2^-90: a value scale below it counts as 0, so sums of P / vs stay finite
 
 // Operands in rows of 64 dimensions (128 bytes), 128-byte swizzle: block b of 64 dimensions of a
 // tile is 128 rows at b * 16384.

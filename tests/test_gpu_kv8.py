@@ -668,3 +668,29 @@ def test_prompts_with_zero_pages_before_small_values(iqq, small):
 
 def test_prompts_with_zero_pages_beside_the_largest_values(iqq):
     _zero_pages_beside_the_largest_values(iqq, [150])
+
+
+@pytest.mark.parametrize("new", [[1, 1], [3, 4]])
+@pytest.mark.parametrize("small", [-21, -32, -45, -70])
+def test_tokens_with_zero_pages_before_small_values(iqq, new, small):
+    _zero_pages_before_small_values(iqq, new, small)
+
+
+def test_tokens_with_zero_pages_beside_the_largest_values(iqq):
+    _zero_pages_beside_the_largest_values(iqq, [1])
+
+
+@pytest.mark.parametrize("new", [[1], [4], [200]])
+@pytest.mark.parametrize("lens", [[700], [5000]])
+@pytest.mark.parametrize("apart", [20, 26, 34, 60])
+def test_attention_negligible_page_of_large_values(iqq, new, lens, apart):
+    """A page whose value scale is 2^apart times the others' and whose keys get next to no weight: the
+    others' weights keep their bits, wherever the page lies."""
+    for where in (0, 1, 9):
+        c = Case(iqq, lens, 1, 128, 64, 101)
+        c.cache.k_scales.fill_(0.02)
+        c.cache.k_codes[:] = c.cache.k_codes // 16
+        c.cache.k_codes[c.tables[0, where].long()] = -127
+        c.cache.v_scales[c.tables[0, where].long()] *= 2.0 ** apart
+        q = c.randn(new[0], 2, 128, dtype=BF16).abs() + 5.0
+        _check_scales(iqq, c, new, 2, BF16, q)
