@@ -12,6 +12,28 @@ namespace iqq {
 constexpr uint32_t kInfBits = 0x7f800000u;
 constexpr uint32_t kTinyBits = 0x04000000u;  // 2^-119: amax below it gives the scale 0
 
+// A load of what an earlier launch may have written.  The kernels here begin while the launch before
+// them still runs and wait for it inside (programmatic serialization), so nothing that it writes is
+// constant for their lifetime, as the read-only path (__ldg, const __restrict__) would have it.
+template <class T>
+__device__ __forceinline__ T ld(const T* p)
+{
+    return *p;
+}
+// (16 bytes as written, in order: left to the compiler it spilled, and 12 prompts' append took 32.4 us for 30.9.)
+__device__ __forceinline__ uint4 ld(const uint4* p)
+{
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float4 ld(const float4* p)
+{
+    float4 v;
+    asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+    return v;
+}
+
 // The scale of values whose largest magnitude has these bits (a NaN's magnitude orders above
 // Inf, so one unsigned maximum finds both): NaN when not finite.  amax >= 2^-119 keeps the
 // scale and its reciprocal normal.
@@ -43,14 +65,14 @@ __device__ __forceinline__ void widen8(const __half*, uint4 a, float (&v)[8])
 // Eight values from a 16-byte boundary.
 __device__ __forceinline__ void load8(const float* p, float (&v)[8])
 {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    const float4 a = ld(reinterpret_cast<const float4*>(p)), b = ld(reinterpret_cast<const float4*>(p) + 1);
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 template <class T>
 __device__ __forceinline__ void load8(const T* p, float (&v)[8])
 {
-    widen8(p, __ldg(reinterpret_cast<const uint4*>(p)), v);
+    widen8(p, ld(reinterpret_cast<const uint4*>(p)), v);
 }
 
 // rint(num * mul / d), decided exactly: 2 |num mul| is compared with (2m+1) d in binary64, where both
@@ -119,10 +141,10 @@ template <> struct Raw<float> { using type = Wide; };
 
 __device__ __forceinline__ void fetch(const float* p, Wide& r)
 {
-    r.a = __ldg(reinterpret_cast<const float4*>(p));
-    r.b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    r.a = ld(reinterpret_cast<const float4*>(p));
+    r.b = ld(reinterpret_cast<const float4*>(p) + 1);
 }
-template <class T> __device__ __forceinline__ void fetch(const T* p, uint4& r) { r = __ldg(reinterpret_cast<const uint4*>(p)); }
+template <class T> __device__ __forceinline__ void fetch(const T* p, uint4& r) { r = ld(reinterpret_cast<const uint4*>(p)); }
 
 __device__ __forceinline__ void widen(const float*, const Wide& r, float (&v)[8])
 {

@@ -95,7 +95,7 @@ __device__ __forceinline__ void put(const Args& P, uint32_t at, int64_t t0, int 
     uint32_t v0[32], v1[32];
     iqq::tmem_ld32(at, v0);
     __syncwarp();
-    for (int c = lane; c < cols; c += 32) da[c] = __ldg(P.as + t0 + c);
+    for (int c = lane; c < cols; c += 32) da[c] = iqq::ld(P.as + t0 + c);
     __syncwarp();
     for (int c = 0; c < cols; c += 64) {
         iqq::tmem_wait_ld(v0);
@@ -113,7 +113,7 @@ __device__ __forceinline__ void put(const Args& P, uint32_t at, int64_t t0, int 
 // (0 + bias and no bias differ for no value but -0, which the product of a zero sum may have)
 __device__ __forceinline__ float bias_of(const Args& P, int64_t r)
 {
-    return P.bias != nullptr && r < P.n_out ? __ldg(P.bias + r) : 0.0f;
+    return P.bias != nullptr && r < P.n_out ? iqq::ld(P.bias + r) : 0.0f;
 }
 
 template <class T>
@@ -212,7 +212,7 @@ pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CU
         for (int64_t i = pair; i < tiles; i += pairs, ++turn) {
             const int buf = turn & 1;
             const int64_t r = (i / P.t_tiles) * 2 * kRows + rank * kRows + quad * 32 + lane, t0 = (i % P.t_tiles) * P.tn;
-            const float dw = r < P.n_out ? __ldg(P.ws + r) : 0.0f, bias = bias_of(P, r);
+            const float dw = r < P.n_out ? iqq::ld(P.ws + r) : 0.0f, bias = bias_of(P, r);
             late = !iqq::bar_wait_long<true>(iqq::smem_u32(&S.done[buf]), static_cast<uint32_t>(turn >> 1) & 1u);
             if (__any_sync(0xffffffffu, late)) break;
             iqq::tc_fence_after();
@@ -333,7 +333,7 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
         if (warp >= 2) {
             float* scales = reinterpret_cast<float*>(raw + (base - iqq::smem_u32(raw))) + (warp - 2) * 256;  // (the stages are free)
             const int64_t r = m0 + row;
-            const float dw = r < P.n_out ? __ldg(P.ws + r) : 0.0f, bias = bias_of(P, r);
+            const float dw = r < P.n_out ? iqq::ld(P.ws + r) : 0.0f, bias = bias_of(P, r);
             put<T>(P, lanes, t0, cols, r, dw, bias, scales);
         }
     } else {
@@ -372,13 +372,13 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
             }
             const int64_t t = t0 + 4 * (first + i / kRows), r = m0 + i % kRows;
             if (r >= P.n_out) continue;
-            const float dw = __ldg(P.ws + r), bias = bias_of(P, r);
+            const float dw = iqq::ld(P.ws + r), bias = bias_of(P, r);
             T* y = static_cast<T*>(P.y) + t * P.ldy + r;
             const uint32_t each[4] = {sum.x, sum.y, sum.z, sum.w};
 #pragma unroll
             for (int u = 0; u < 4; ++u)
                 if (t + u < P.n_tok)
-                    y[u * P.ldy] = iqq::from_f32<T>(finish(static_cast<int>(each[u]), __ldg(P.as + t + u), dw, bias));
+                    y[u * P.ldy] = iqq::from_f32<T>(finish(static_cast<int>(each[u]), iqq::ld(P.as + t + u), dw, bias));
         }
     }
     if (late) iqq::raise_flags(P.flags, IQQ_FLAG_WAIT_TIMEOUT);

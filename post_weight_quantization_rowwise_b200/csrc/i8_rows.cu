@@ -20,8 +20,8 @@ constexpr int kMaxWarps = 32;
 // Rows of whole units of eight values on 16-byte boundaries.
 template <class T, int NV>
 __global__ void __launch_bounds__(1024)
-i8_rows_kernel(const T* __restrict__ x, int64_t ldx, int8_t* __restrict__ codes, int64_t ldc,
-               float* __restrict__ scales, int64_t nrows, int64_t n, uint32_t* __restrict__ flags)
+i8_rows_kernel(const T* x, int64_t ldx, int8_t* codes, int64_t ldc,
+               float* scales, int64_t nrows, int64_t n, uint32_t* flags)
 {
     __shared__ uint32_t part[2][kMaxWarps];
     const int tid = threadIdx.x, lane = tid & 31, warps = blockDim.x >> 5;
@@ -80,8 +80,8 @@ i8_rows_kernel(const T* __restrict__ x, int64_t ldx, int8_t* __restrict__ codes,
 // Any rows, a value at a time; the second pass reads them again.
 template <class T>
 __global__ void __launch_bounds__(1024)
-i8_rows_any_kernel(const T* __restrict__ x, int64_t ldx, int8_t* __restrict__ codes, int64_t ldc,
-                   float* __restrict__ scales, int64_t nrows, int64_t n, uint32_t* __restrict__ flags)
+i8_rows_any_kernel(const T* x, int64_t ldx, int8_t* codes, int64_t ldc,
+                   float* scales, int64_t nrows, int64_t n, uint32_t* flags)
 {
     __shared__ uint32_t part[2][kMaxWarps];
     const int tid = threadIdx.x, lane = tid & 31, warps = blockDim.x >> 5;

@@ -28,7 +28,7 @@ struct Span {
 __device__ __forceinline__ Span span_of(const Kv8& C, int b)
 {
     Span s;
-    const int32_t c0 = __ldg(C.cu + b), c1 = __ldg(C.cu + b + 1), len = __ldg(C.lens + b);
+    const int32_t c0 = ld(C.cu + b), c1 = ld(C.cu + b + 1), len = ld(C.lens + b);
     s.ok = c0 >= 0 && c1 >= c0 && c1 <= C.n_tokens && len >= 0;
     s.first = c0;
     s.n = s.ok ? c1 - c0 : 0;
@@ -57,7 +57,7 @@ __device__ __forceinline__ void check_spans(const Kv8& C, bool places, uint32_t*
 // clamped, so arrays that are not monotone give some sequence in range, which span_of checks.)
 __device__ __forceinline__ int64_t slot_base(const Kv8& C, int b, int per, int unit, int extra)
 {
-    const int32_t c = max(0, min(__ldg(C.cu + b), C.n_tokens));
+    const int32_t c = max(0, min(ld(C.cu + b), C.n_tokens));
     return static_cast<int64_t>(c) * per / unit + static_cast<int64_t>(extra) * b;
 }
 
@@ -78,7 +78,7 @@ __device__ __forceinline__ int seq_of_slot(const Kv8& C, int64_t slot, int per, 
 // The page of tokens pos >> page_log2 of sequence b, or -1 when the table's entry is no page.
 __device__ __forceinline__ int page_at(const Kv8& C, int b, int64_t index)
 {
-    const int p = __ldg(C.tables + b * C.table_stride + index);
+    const int p = ld(C.tables + b * C.table_stride + index);
     return p >= 0 && p < C.n_pages ? p : -1;
 }
 

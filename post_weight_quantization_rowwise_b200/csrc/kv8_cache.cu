@@ -145,7 +145,7 @@ template <class T, int D>
 __global__ void __launch_bounds__(kThreads)
 gather_kernel(const Kv8 C, T* __restrict__ ko, T* __restrict__ vo, uint32_t* __restrict__ flags)
 {
-    constexpr int kRow = D / 8;
+    constexpr int kRow = D / 8, kFlight = 4;
     const int lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -164,20 +164,30 @@ gather_kernel(const Kv8 C, T* __restrict__ ko, T* __restrict__ vo, uint32_t* __r
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         T* out = (which == 0 ? ko : vo) + row * units * 8;
-#pragma unroll 4
-        for (int u = lane; u < units; u += 32) {
-            const int h = u / kRow;
-            float t[8] = {};
-            if (p >= 0) {
-                const int64_t cell = static_cast<int64_t>(p) * C.heads + h;
-                const float d = __ldg(C.scales[which] + cell);
-                const uint2 w = __ldg(reinterpret_cast<const uint2*>(
-                    C.codes[which] + ((cell << C.page_log2) + off) * D + (u % kRow) * 8));
+        // four units' loads before their stores (which may not pass one another)
+        for (int u0 = lane; u0 < units; u0 += 32 * kFlight) {
+            float d[kFlight];
+            uint2 w[kFlight];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    t[i] = __fmul_rn(d, static_cast<float>(static_cast<int8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3)))));
+            for (int i = 0; i < kFlight; ++i) {
+                const int u = u0 + 32 * i;
+                d[i] = 0.0f;
+                w[i] = make_uint2(0u, 0u);
+                if (p >= 0 && u < units) {
+                    const int64_t cell = static_cast<int64_t>(p) * C.heads + u / kRow;
+                    d[i] = iqq::ld(C.scales[which] + cell);
+                    w[i] = iqq::ld(reinterpret_cast<const uint2*>(C.codes[which] + ((cell << C.page_log2) + off) * D + (u % kRow) * 8));
+                }
             }
-            put8(out + u * 8, t);
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                if (u0 + 32 * i >= units) break;
+                float t[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    t[e] = __fmul_rn(d[i], static_cast<float>(static_cast<int8_t>((e < 4 ? w[i].x : w[i].y) >> (8 * (e & 3)))));
+                put8(out + (u0 + 32 * i) * 8, t);
+            }
         }
     }
 }

@@ -209,3 +209,19 @@ def test_linear_on_a_side_stream_and_in_a_graph(iqq):
         graph.replay()
         q0, d0 = _rows64(x)
         _check(y2, q0, d0, wc, dw, None)
+
+
+def test_calls_in_turn_on_the_same_buffers(iqq):
+    """Rows and product over and over into the same codes, scales and y with other data, and nothing that
+    waits for the device between the calls: every call sees what the one before wrote."""
+    xs = [_rand((40, 1000), F32, i) * 2.0 ** (i % 5 - 2) for i in range(24)]
+    w, dw = iqq.quantize_i8_rows(_rand((300, 1000), F32, 99))
+    codes, scales = torch.zeros(40, 1008, dtype=torch.int8, device="cuda")[:, :1000], torch.zeros(40, device="cuda")
+    ys = [torch.zeros(40, 300, device="cuda") for _ in xs]
+    torch.cuda.synchronize()
+    for x, y in zip(xs, ys):
+        iqq.iqq_quantize_i8_rows(x, codes, scales)
+        iqq.iqq_gemm_i8(codes, scales, w, dw, y)
+    for x, y in zip(xs, ys):
+        q0, d0 = _rows64(x)
+        _check(y, q0, d0, w, dw, None)

@@ -694,3 +694,29 @@ def test_attention_negligible_page_of_large_values(iqq, new, lens, apart):
         c.cache.v_scales[c.tables[0, where].long()] *= 2.0 ** apart
         q = c.randn(new[0], 2, 128, dtype=BF16).abs() + 5.0
         _check_scales(iqq, c, new, 2, BF16, q)
+
+
+def test_calls_in_turn_on_the_same_buffers(iqq):
+    """Append and gather, and append and attention, over and over on the same pages with other data, and
+    nothing that waits for the device between the calls: every call sees what the one before wrote."""
+    lens = [130, 64, 1, 40]
+    c = Case(iqq, lens, 4, 128, 64, 109)
+    args, total = (c.tables, _i32(lens), _cu(lens)), sum(lens)
+    data = [c.randn(total, 4, 128, dtype=BF16) * 2.0 ** (i % 5 - 2) for i in range(24)]
+    q, last = c.randn(4, 8, 128, dtype=BF16), _i32([0, 1, 2, 3, 4])
+    alone = []
+    for x in data:
+        iqq.iqq_kv8_append(c.cache, x, -x, *args)
+        torch.cuda.synchronize()
+        k, v = iqq.kv8_gather(c.cache, *args, total, dtype=BF16)
+        torch.cuda.synchronize()
+        alone.append((k, v, iqq.kv8_attention(c.cache, q, c.tables, args[1], last)))
+        torch.cuda.synchronize()
+    got = []
+    for x in data:
+        iqq.iqq_kv8_append(c.cache, x, -x, *args)
+        k, v = iqq.kv8_gather(c.cache, *args, total, dtype=BF16)
+        got.append((k, v, iqq.kv8_attention(c.cache, q, c.tables, args[1], last)))
+    for a, b in zip(alone, got):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
