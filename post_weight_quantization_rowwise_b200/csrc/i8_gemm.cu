@@ -297,6 +297,7 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
         }
     } else if (warp == 1) {
         if (lane == 0) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");  // (its waits are limited, as the copies they wait for begin here)
             const uint32_t idesc = iqq::idesc_i8(kRows, P.tn);
             int s = 0;
             uint32_t ph = 0;
