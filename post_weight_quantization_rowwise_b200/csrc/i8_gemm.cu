@@ -174,10 +174,13 @@ pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CU
                 }
             }
         }
-        // every copy has landed (the products waited for them) unless a wait ran out
+        // every copy has landed (the products waited for them) unless a wait ran out: then the two CTAs may have
+        // stopped at different stages, whose barriers never complete, and the copies get 1 ms to land
         if (rank == 0)
-            for (int64_t i = issued > P.stages ? issued - P.stages : 0; i < issued; ++i)
-                late |= !iqq::bar_wait_long<true>(iqq::smem_u32(&S.full[i % P.stages]), static_cast<uint32_t>(i / P.stages) & 1u);
+            for (int64_t i = issued > P.stages ? issued - P.stages : 0; i < issued && !late; ++i)
+                late = !iqq::bar_drain<true>(iqq::smem_u32(&S.full[i % P.stages]), static_cast<uint32_t>(i / P.stages) & 1u);
+        if (late)
+            for (const long long t0 = clock64(); clock64() - t0 < 2000000LL;) {}
     } else if (warp == 1 && lane == 0 && rank == 0) {
         const uint32_t idesc = iqq::idesc_i8(2 * kRows, P.tn);
         int s = 0, turn = 0;
@@ -205,6 +208,8 @@ pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CU
             }
             iqq::tc_commit<2>(iqq::smem_u32(&S.done[buf]));
         }
+        // (the tensor memory goes after the last products, also where the epilogue gave up)
+        if (turn > 0) late |= !iqq::bar_drain<true>(iqq::smem_u32(&S.done[(turn - 1) & 1]), static_cast<uint32_t>((turn - 1) >> 1) & 1u);
     } else if (warp >= 2) {
         const int quad = warp & 3;
         float* scales = reinterpret_cast<float*>(raw + (base - iqq::smem_u32(raw)) + P.stages * stage_bytes) + (warp - 2) * 256;
@@ -293,7 +298,7 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
             }
             // every copy has landed (the products waited for them) unless a wait ran out
             for (int i = issued > P.stages ? issued - P.stages : 0; i < issued; ++i)
-                late |= !iqq::bar_wait_long(iqq::smem_u32(&S.full[i % P.stages]), static_cast<uint32_t>(i / P.stages) & 1u);
+                late |= !iqq::bar_drain(iqq::smem_u32(&S.full[i % P.stages]), static_cast<uint32_t>(i / P.stages) & 1u);
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -323,7 +328,7 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
     }
     __syncwarp();
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    late |= !iqq::bar_wait_long(iqq::smem_u32(&S.done[0]), 0);
+    late |= !iqq::bar_drain(iqq::smem_u32(&S.done[0]), 0);
     __syncwarp();
     iqq::tc_fence_after();
 

@@ -11,7 +11,14 @@
 
 namespace iqq {
 
-constexpr long long kWaitClocks = 4000000000LL;  // about 2 s at the maximum SM clock
+// Limits of the waits on barriers: about 2 s at the maximum SM clock.  A build may set another for the
+// waits of a kernel's work (0: they ask once, to see what happens when they run out); those for what a CTA
+// has under way itself when it ends (kDrainClocks: copies into its shared memory, products in its tensor
+// memory) keep theirs.
+#ifndef IQQ_WAIT_CLOCKS
+#define IQQ_WAIT_CLOCKS 4000000000LL
+#endif
+constexpr long long kWaitClocks = IQQ_WAIT_CLOCKS, kDrainClocks = 4000000000LL;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p)
 {
@@ -85,24 +92,45 @@ __device__ __forceinline__ bool bar_try_long(uint32_t bar, uint32_t parity)
             : "memory");
     return ok != 0u;
 }
-// Waits for the phase of this parity, at most about 2 s; false when it did not complete.
+// Whether the phase is complete, without a wait.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0u;
+}
+// Waits for the phase of this parity, for a limited time; false when it did not complete.  (Only after
+// griddepcontrol.wait: the time that the launch before takes is not this one's.)
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity)
 {
+    if constexpr (kWaitClocks == 0) return bar_test(bar, parity);
     if (bar_try<CLUSTER>(bar, parity)) return true;
     const long long t0 = clock64();
     while (!bar_try<CLUSTER>(bar, parity))
         if (clock64() - t0 > kWaitClocks) return false;
     return true;
 }
-template <bool CLUSTER = false>
+template <bool CLUSTER = false, long long LIMIT = kWaitClocks>
 __device__ __forceinline__ bool bar_wait_long(uint32_t bar, uint32_t parity)
 {
+    if constexpr (LIMIT == 0) return bar_test(bar, parity);
     if (bar_try_long<CLUSTER>(bar, parity)) return true;
     const long long t0 = clock64();
     while (!bar_try_long<CLUSTER>(bar, parity))
-        if (clock64() - t0 > kWaitClocks) return false;
+        if (clock64() - t0 > LIMIT) return false;
     return true;
+}
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool bar_drain(uint32_t bar, uint32_t parity)
+{
+    return bar_wait_long<CLUSTER, kDrainClocks>(bar, parity);
 }
 
 // One lane of a whole warp, the same one every time (products and the commit that follows them are
