@@ -123,7 +123,7 @@ __device__ __forceinline__ bool load(Smem<D>& S, const Kv8& C, const Work& W, in
         return key < end ? iqq::page_at(C, W.b, key >> C.page_log2) : -2;
     };
     bool ok = true;
-    int page = page_of(0), j = 0;
+    int page = page_of(0), j = 0, sent[2] = {0, 0};
     for (int j0 = 0; j0 < n && ok; j0 += batch) {
         const int here = page;
         if (j0 + batch < n) page = page_of(j0 + batch);
@@ -161,12 +161,14 @@ __device__ __forceinline__ bool load(Smem<D>& S, const Kv8& C, const Work& W, in
                         }
                 }
                 iqq::async_arrive(bar);
+                ++sent[which];
             }
         }
     }
     // every copy has landed (the makers waited for it) unless a wait ran out
+#pragma unroll
     for (int which = 0; which < 2; ++which)
-        if (j > 0) ok &= iqq::bar_wait(iqq::smem_u32(&S.rfull[which]), (j - 1) & 1);
+        if (sent[which] > 0) ok &= iqq::bar_drain(iqq::smem_u32(&S.rfull[which]), (sent[which] - 1) & 1);
     return ok;
 }
 
@@ -668,7 +670,7 @@ prompt_kernel(const Kv8 C, const Attend A, uint32_t* __restrict__ flags)
             ok = multiply<D>(S, W, tmem);
             // nothing is left running when the tensor memory goes
             if (iqq::elect()) iqq::tc_commit<1>(iqq::smem_u32(&S.done));
-            ok &= iqq::bar_wait(iqq::smem_u32(&S.done), 0);
+            ok &= iqq::bar_drain(iqq::smem_u32(&S.done), 0);
         }
     }
     if (!ok) iqq::raise_flags(flags, IQQ_FLAG_WAIT_TIMEOUT);

@@ -71,3 +71,27 @@ def test_product(iqq, both, n_tok, n_out, k):
     da, dw = torch.ones(n_tok, device="cuda"), torch.ones(n_out, device="cuda")
     y = both(lambda flags: iqq.gemm_i8(a, da, w, dw, flags=flags))
     assert torch.equal(y, (a.double() @ w.double().t()).float())
+
+
+def _attention(iqq, both, dim, lens, new, heads):
+    page, n = 64, sum(-(-m // 64) for m in lens)
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    codes = [torch.randint(-127, 128, (n, 1, page, dim), generator=g, device="cuda").to(torch.int8) for _ in range(2)]
+    scales = [torch.rand(n, 1, generator=g, device="cuda") * 0.02 for _ in range(2)]
+    cache = iqq.Kv8Cache(*codes, *scales)
+    width, at, rows = max(-(-m // page) for m in lens), 0, []
+    for m in lens:
+        rows.append([at + i if i < -(-m // page) else 0 for i in range(width)])
+        at += -(-m // page)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    args = (i32(rows), i32(lens), i32([sum(new[:b]) for b in range(len(new) + 1)]))
+    q = torch.randn(sum(new), heads, dim, generator=g, device="cuda").to(torch.bfloat16)
+    want = iqq.kv8_attention(cache, q, *args)
+    out = both(lambda flags: iqq.kv8_attention(cache, q, *args, flags=flags))
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens,new,heads", [([300], [300], 2), ([9000], [100], 4), ([700] * 12, [600] * 12, 8)])
+def test_prompts(iqq, both, dim, lens, new, heads):
+    _attention(iqq, both, dim, lens, new, heads)
