@@ -256,7 +256,7 @@ struct Feed {
     {
         bool ok = true;
         for (int64_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-            ok &= iqq::bar_wait(iqq::smem_u32(&S.full[i % kStages]), static_cast<uint32_t>(i / kStages) & 1u);
+            ok &= iqq::bar_drain(iqq::smem_u32(&S.full[i % kStages]), static_cast<uint32_t>(i / kStages) & 1u);
         return ok;
     }
 };
@@ -612,6 +612,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             l[n][h] += __shfl_xor_sync(0xffffffffu, l[n][h], 8);
             l[n][h] += __shfl_xor_sync(0xffffffffu, l[n][h], 16);
         }
+    bool stop = false;
 #pragma unroll
     for (int step = 2; step > 0; step /= 2) {
         if (warp >= step && warp < 2 * step) {
@@ -629,7 +630,10 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             }
         }
         meet();
-        if (step == 2 && S.abort) break;  // (all four warps together)
+        // All four warps stop together: what they set before this barrier they see here, and none gets past the
+        // next one to set it for another piece before all have looked.
+        if (step == 2) stop = S.abort != 0;
+        if (stop) break;
         if (warp < step) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -655,7 +659,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
         meet();
     }
-    if (S.abort) {
+    if (stop) {
         iqq::raise_flags(flags, IQQ_FLAG_WAIT_TIMEOUT);
         break;
     }

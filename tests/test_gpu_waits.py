@@ -95,3 +95,10 @@ def _attention(iqq, both, dim, lens, new, heads):
 @pytest.mark.parametrize("lens,new,heads", [([300], [300], 2), ([9000], [100], 4), ([700] * 12, [600] * 12, 8)])
 def test_prompts(iqq, both, dim, lens, new, heads):
     _attention(iqq, both, dim, lens, new, heads)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens,new,heads", [([40], [1], 1), ([600, 30], [1, 1], 4), ([9000, 200], [1, 1], 8),
+                                            ([3000] * 40, [3] * 40, 4)])
+def test_tokens(iqq, both, dim, lens, new, heads):
+    _attention(iqq, both, dim, lens, new, heads)
