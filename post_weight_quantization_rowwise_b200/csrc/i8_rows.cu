@@ -162,10 +162,17 @@ int iqq::sm_count()
 {
     static std::atomic<int> known[64];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();  // (not the next launch's)
+        return 148;
+    }
+    if (dev < 0 || dev >= 64) return 148;
     int n = known[dev].load(std::memory_order_relaxed);
     if (n == 0) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+            cudaGetLastError();
+            return 148;
+        }
         known[dev].store(n, std::memory_order_relaxed);
     }
     return n;

@@ -750,10 +750,14 @@ iqq_status launch(const Kv8& C, const Attend& A, uint32_t* flags, cudaStream_t s
     iqq_status s = iqq::opt_in_smem(reinterpret_cast<const void*>(prompt_kernel<T, D>), smem, done);
     if (s != IQQ_OK) return s;
     // The warps' shares have to fit what the launch gives, or they would wait for registers for good.
-    static const int regs = [] {
+    static std::atomic<int> known{0};  // registers a thread, once they could be asked for
+    int regs = known.load(std::memory_order_relaxed);
+    if (regs == 0) {
         cudaFuncAttributes at = {};
-        return cudaFuncGetAttributes(&at, prompt_kernel<T, D>) == cudaSuccess ? at.numRegs : 0;
-    }();
+        if (cudaFuncGetAttributes(&at, prompt_kernel<T, D>) != cudaSuccess) return iqq::launch_status();
+        regs = at.numRegs;
+        known.store(regs, std::memory_order_relaxed);
+    }
     if (regs * kThreads < kRegs) {
         iqq::set_last_cuda_error(cudaErrorLaunchOutOfResources);
         return IQQ_ERR_CUDA;

@@ -60,3 +60,12 @@ def test_binding_refusals():
     with pytest.raises(ValueError):
         m.gemm_i8(torch.zeros(2, 64, dtype=torch.int8), torch.ones(2), torch.zeros(3, 64, dtype=torch.int8), torch.ones(3))
     assert "gemm_i8" in m.__all__ and "quantize_i8_rows" in m.__all__
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="what calls say without a device")
+def test_without_a_device_every_call_says_why():
+    """The CUDA error of the call itself (no device, or no driver for it), each time."""
+    G, W = m._lib.iqq_gemm_i8, m._lib.iqq_last_cuda_error
+    for n_tok, n_out, k in ((1, 8, 64), (4, 8, 64), (4000, 4000, 640), (4, 8, 64)):
+        assert G(V(16), 640, V(16), V(16), 640, V(16), None, 0, V(16), n_out, n_tok, n_out, k, None, None) == 4
+        assert W() in (35, 100), W()

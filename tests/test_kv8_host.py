@@ -94,3 +94,13 @@ def test_binding_refusals():
         m.Kv8Cache(z(2, 1, 16, 64, dtype=torch.int8), z(2, 1, 16, 64, dtype=torch.int8), z(2, 1), z(2, 1))
     for n in ("Kv8Cache", "kv8_cache", "kv8_gather", "kv8_attention", "iqq_kv8_append", "iqq_kv8_gather", "iqq_kv8_attention"):
         assert n in m.__all__
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="what calls say without a device")
+def test_without_a_device_every_call_says_why():
+    """The CUDA error of the call itself (no device, or no driver for it), each time; for tokens, prompts
+    and the cache."""
+    W = m._lib.iqq_last_cuda_error
+    for _ in range(2):
+        for call in (_append, _gather, _attend, lambda: _attend(_7=5000)):
+            assert call() == 4 and W() in (35, 100), W()
