@@ -800,10 +800,15 @@ combine_kernel(const Args A, const int ctas)
 //    64 dimensions  24 sequences up to 5000: 48 rows 76, 83; 62 rows 97, 82.     64 of 2000: 48 rows 124, 127; 62 rows 158, 127
 constexpr int64_t prompt_rows(int64_t head_dim) { return head_dim == 128 ? 33 : 49; }
 
-// Tables up to this many keys, and tiles that fit the machine at once: a CTA takes a whole tile.  Shares
-// and whole tiles, us on the device: 32 heads over 32, one sequence: 100 keys 8.9, 5.7; 600 keys 10.0, 10.0;
-// 1000 keys 11.2, 12.9 (and 15.0, 14.5 for 8 sequences over 8 heads; a call's host part is 4 us less).
-constexpr int64_t kWholeKeys = 1024;
+// Tables up to this many keys, and tiles that fit the machine at once: a CTA takes a whole tile; of one
+// sequence whose tiles are less than a quarter of the SMs, up to kFewKeys.  Shares and whole tiles, us on
+// the device (128 dimensions), by keys:
+//   1 sequence    1 tile 512: 8.3, 8.0; 768: 8.6, 9.8    8 tiles 640: 9.5, 9.1; 704: 9.6, 10.0; 1024: 10.1, 11.7
+//                32 tiles 640: 10.2, 9.9; 1024: 11.5, 12.6    64 tiles 1024: 13.7, 12.9
+//   sequences x heads   2 x 32 1024: 13.8, 12.9   8 x 8 1024: 15.2, 13.7; 1536: 17.0, 17.8   32 x 8 1024: 24.9, 22.6
+// Few sequences of few tiles lose on the device between the two limits (3 x 2 heads 1024: 9.8, 11.7) and
+// win in a call that the host makes each time, where the second launch and the workspace take 4 us.
+constexpr int64_t kWholeKeys = 1024, kFewKeys = 704;
 
 struct Plan {
     bool prompt;
@@ -832,7 +837,8 @@ Plan plan_of(const iqq_kv8_cache* cache, const iqq_kv8_seqs* seqs, int64_t n_hea
     const int64_t tiles = (n_tokens * group / p.row_tile + seqs->n_seqs) * cache->n_kv_heads;
     const int64_t stages = 1 + (seqs->table_width * cache->page_size + kKeys - 1) / kKeys;
     const int64_t most = std::min<int64_t>(kMaxCtas, (p.row_tile == 8 ? 3 : 2) * iqq::sm_count());
-    p.whole = tiles <= most && seqs->table_width * cache->page_size <= kWholeKeys;
+    const bool few = seqs->n_seqs == 1 && tiles < iqq::sm_count() / 4;
+    p.whole = tiles <= most && seqs->table_width * cache->page_size <= (few ? kFewKeys : kWholeKeys);
     if (p.whole) {
         p.ctas = tiles;
         return p;

@@ -104,3 +104,22 @@ def test_without_a_device_every_call_says_why():
     for _ in range(2):
         for call in (_append, _gather, _attend, lambda: _attend(_7=5000)):
             assert call() == 4 and W() in (35, 100), W()
+
+
+def test_workspace_of_short_tables():
+    """One sequence of few tiles: a CTA takes a tile up to 704 keys, beyond them the keys are shared out;
+    more tiles or sequences up to 1024 keys.  A workspace that is too small, or none, is refused."""
+    W = m._lib.iqq_kv8_attention_workspace_bytes
+
+    def need(n_seqs, width, kv, heads):
+        seqs = _seqs(n_seqs=n_seqs, table_width=width, table_stride=width)
+        return W(ctypes.byref(_cache(n_kv_heads=kv, page_size=64, head_dim=128)), ctypes.byref(seqs), heads, n_seqs)
+
+    for kv, heads in ((1, 8), (8, 32), (32, 32)):
+        assert need(1, 11, kv, heads) == 0 and need(1, 12, kv, heads) > 0 and need(1, 16, kv, heads) > 0
+    assert need(1, 16, 64, 64) == 0 and need(1, 17, 64, 64) > 0
+    assert need(8, 16, 8, 32) == 0 and need(8, 17, 8, 32) > 0
+    long = _seqs(n_seqs=1, table_width=1 << 14, table_stride=1 << 14)
+    size = W(ctypes.byref(_cache()), ctypes.byref(long), 4, 1)
+    assert size > 0
+    assert _attend(seqs=long, _7=1, _12=size - 1) == 2 and _attend(seqs=long, _7=1, _11=None) == 1
