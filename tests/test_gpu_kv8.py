@@ -720,3 +720,43 @@ def test_calls_in_turn_on_the_same_buffers(iqq):
     for a, b in zip(alone, got):
         for x, y in zip(a, b):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("lens,new,heads", [([100, 80, 50], [2, 1, 2], 2), ([9000, 700, 300], [1, 2, 1], 4),
+                                            ([700, 650, 900], [300, 200, 400], 4), ([20000, 9000, 900], [40, 60, 50], 8)])
+def test_attention_bad_spans_leave_their_rows(iqq, lens, new, heads):
+    """A span below 0, beyond the rows, of negative length, and a negative length of the sequence: its
+    rows and their log-sums stay as they were, and the other sequences' rows are what a good call
+    gives.  Whole tiles, shares joined, the prompt kernel, and its keys split."""
+    c = Case(iqq, lens, 1, 64, 16, 107)
+    total, n = sum(new), len(lens)
+    q = c.randn(total, heads, 64, dtype=BF16)
+    need = iqq.kv8_attention_workspace_bytes(c.cache, n, c.tables.shape[1], heads, total)
+    assert (need > 0) == (max(lens) > 5000)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call(m, cu):
+        out, lse = torch.full_like(q, 7.0), torch.full((total, heads), 7.0, device="cuda")
+        flags.zero_()
+        iqq.iqq_kv8_attention(c.cache, q, c.tables, _i32(m), _i32(cu), out, lse=lse, workspace=ws, flags=flags)
+        return out, lse, int(flags.item())
+
+    cu = _cu(new).tolist()
+    good, good_lse, f = call(lens, cu)
+    assert f == 0
+    for m, at, bad in ((lens, [-4] + cu[1:], [0]), (lens, cu[:-1] + [total + 9], [2]),
+                       ([lens[0], -3, lens[2]], cu, [1]), ([-1, lens[1], lens[2]], cu, [0]),
+                       (lens, [cu[0], cu[2], cu[1], cu[1]], [1]), (lens, [-2, -1, total + 1, 2 ** 31 - 1], [0, 1, 2])):
+        out, lse, f = call(m, at)
+        assert f == iqq.FLAG_BAD_INDEX, (m, at)
+        written = torch.zeros(total, dtype=torch.bool, device="cuda")
+        for b in range(n):
+            if b not in bad:
+                written[at[b]:at[b + 1]] = True
+        assert (out[~written] == 7.0).all() and (lse[~written] == 7.0).all(), (m, at)
+        for b in range(n):
+            if b not in bad and (at[b], at[b + 1]) == (cu[b], cu[b + 1]):
+                torch.testing.assert_close(out[cu[b]:cu[b + 1]].float(), good[cu[b]:cu[b + 1]].float(),
+                                           rtol=2.0 ** -7, atol=2e-3)
+                torch.testing.assert_close(lse[cu[b]:cu[b + 1]], good_lse[cu[b]:cu[b + 1]], rtol=1e-5, atol=1e-5)
