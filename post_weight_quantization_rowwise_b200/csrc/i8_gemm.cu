@@ -371,20 +371,22 @@ split_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
         const int first = static_cast<int>(rank) * per, mine = min(per, groups - first);
         const uint4* part = reinterpret_cast<const uint4*>(raw + (base - iqq::smem_u32(raw)));
         for (int i = threadIdx.x; i < mine * kRows; i += kThreads) {
+            const int64_t t = t0 + 4 * (first + i / kRows), r = m0 + i % kRows;
+            if (r >= P.n_out) continue;
+            const float dw = iqq::ld(P.ws + r), bias = bias_of(P, r);
+            float da[4];  // (before the stores, which loads may not pass)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) da[u] = t + u < P.n_tok ? iqq::ld(P.as + t + u) : 0.0f;
             uint4 sum = make_uint4(0, 0, 0, 0);
             for (int src = 0; src < P.split; ++src) {
                 const uint4 v = part[src * per * kRows + i];
                 sum = make_uint4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
             }
-            const int64_t t = t0 + 4 * (first + i / kRows), r = m0 + i % kRows;
-            if (r >= P.n_out) continue;
-            const float dw = iqq::ld(P.ws + r), bias = bias_of(P, r);
             T* y = static_cast<T*>(P.y) + t * P.ldy + r;
             const uint32_t each[4] = {sum.x, sum.y, sum.z, sum.w};
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                if (t + u < P.n_tok)
-                    y[u * P.ldy] = iqq::from_f32<T>(finish(static_cast<int>(each[u]), iqq::ld(P.as + t + u), dw, bias));
+                if (t + u < P.n_tok) y[u * P.ldy] = iqq::from_f32<T>(finish(static_cast<int>(each[u]), da[u], dw, bias));
         }
     }
     if (late) iqq::raise_flags(P.flags, IQQ_FLAG_WAIT_TIMEOUT);
