@@ -30,11 +30,5 @@ __device__ __forceinline__ uint32_t max_h2(uint32_t a, uint32_t b)
     asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-__device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 
 }  // namespace iqq

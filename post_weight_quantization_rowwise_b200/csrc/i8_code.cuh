@@ -62,13 +62,7 @@ __device__ __forceinline__ void widen8(const __half*, uint4 a, float (&v)[8])
         v[2 * i + 1] = __half2float(__ushort_as_half(static_cast<unsigned short>(w[i] >> 16)));
     }
 }
-// Eight values from a 16-byte boundary.
-__device__ __forceinline__ void load8(const float* p, float (&v)[8])
-{
-    const float4 a = ld(reinterpret_cast<const float4*>(p)), b = ld(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
+// Eight 16-bit values from a 16-byte boundary.
 template <class T>
 __device__ __forceinline__ void load8(const T* p, float (&v)[8])
 {
