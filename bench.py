@@ -779,11 +779,23 @@ def main_reference(args):
 
 def profile_case(name: str):
     """Fixed cases for ncu captures (one GPU, a few launches): gemv_11008x4096 (25 MB of
-    blocks), gemv_16384x53248 (490 MB, the large matrix of the GEMV phase) and
-    moe_experts_4 (the first 4 MoE experts' gate, up and down tensors quantized once each,
-    12 launches in expert order, 704 MB of x)."""
+    blocks), gemv_16384x53248 (490 MB, the large matrix of the GEMV phase), moe_experts_4
+    (the first 4 MoE experts' gate, up and down tensors quantized once each, 12 launches in
+    expert order, 704 MB of x) and int8_operators (the listed cases of perf/operators.py, one
+    pass each, less than 2 GB held)."""
     import torch
     import post_weight_quantization_rowwise_b200 as iqq
+    if name == "int8_operators":
+        from perf import operators
+        operators.own = True
+        for case in operators.listed():
+            state = operators.prepare(case, 1)
+            out = operators.run(state)
+            torch.cuda.synchronize()
+            print("ok", case["name"], len(out))
+            del state, out
+            torch.cuda.empty_cache()
+        return
     if name == "moe_experts_4":
         from post_weight_quantization_rowwise_b200 import synth
         ts = synth.moe_experts(4)
