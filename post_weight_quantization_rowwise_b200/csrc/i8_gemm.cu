@@ -17,8 +17,8 @@
 //                to 8 CTAs whose partial sums meet in shared memory: when tokens are few, the
 //                weights' bytes bound the product and every SM has to read its share of them.
 //
-// Measured with weights larger than L2 in turn (tokens x channels x k): 4096 x 11008 x 4096 116 us
-// (3180 TOPS; twice the bfloat16 rate would be 3299), 777 x 4099 x 11000 30 us (2320 TOPS), 192 x 4096
+// Measured with weights larger than L2 in turn (tokens x channels x k): 4096 x 11008 x 4096 117 us
+// (3170 TOPS; twice the bfloat16 rate would be 3299), 777 x 4099 x 11000 30 us (2340 TOPS), 192 x 4096
 // x 14336 21 us, 16 x 11008 x 4096 11.2 us (4.1 TB/s of weights), 1 x 4096 x 4096 6.5 us.
 #include <math.h>
 

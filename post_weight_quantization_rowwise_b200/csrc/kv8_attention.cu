@@ -31,7 +31,7 @@
 // tiles few, each CTA takes a whole tile instead: no parts, no workspace, one launch.
 //
 // Measured with inputs larger than L2: 32 sequences of 4096 tokens, 32 heads over 32 of 128 dimensions
-// 169 us (6.3 TB/s of 6.55); 64 up to 8000, 32 over 8: 97 us (5.4); one of 131000, 32 over 4: 37 us
+// 168 us (6.4 TB/s of 6.55); 64 up to 8000, 32 over 8: 97 us (5.5); one of 131000, 32 over 4: 37 us
 // (3.6; the scan, the ring's filling and the joining launch are 10 us of any call).
 #include <math.h>
 

@@ -8,11 +8,11 @@
 // value); a decoding step is one token and, when the scale grows, the page's old codes, and takes the
 // five dependent reads (cu, the span, the table, the scale, the codes) that lead to its store.
 //
-// Measured: 12 prompts of up to 1500 tokens, 8 heads of 128 dimensions, bfloat16: 20.6 us (2.3 TB/s);
-// 96 sequences of one token: 4.5 us.
+// Measured: 12 prompts of up to 1500 tokens, 8 heads of 128 dimensions, bfloat16: 21.8 us (2.2 TB/s);
+// 96 sequences of one token: 4.8 us.
 //
 // Gather.  One warp a packed row: fl32(d * q) of all heads, 8 codes in and 16 or 32 B out a lane.
-// The same prompts back: 10.3 us (4.8 TB/s).
+// The same prompts back: 9.1 us (5.5 TB/s).
 #include "kv8.cuh"
 
 namespace {

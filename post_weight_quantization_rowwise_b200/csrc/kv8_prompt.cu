@@ -5,18 +5,19 @@
 // running maximum m.  A CTA takes 256 rows of one sequence and key/value head (row r is token
 // r / group, head r % group of the group) as two tiles of 128, over 128 keys at a time:
 //     S = Q K^T and O += P V on tcgen05 (binary16 operands, binary32 sums in tensor memory).
-// While one tile's scores go through the softmax, the other's products run.  Four warps make the
-// operands: codes become binary16 exactly (the byte b of a code c, in the low byte of 0x6400, is
-// the binary16 1152 + c after b ^= 0x80), rows of q by a power of two for each row.  Four warps a
-// tile do the softmax, a thread a row, so maximum and sum need no other thread.
+// While one tile's scores go through the softmax, the other's products run.  One warp loads, one turns
+// the pages' scales into factors.  Four warps make the operands: codes become binary16 exactly (the
+// byte b of a code c, in the low byte of 0x6400, is the binary16 1152 + c after b ^= 0x80), rows of q
+// by a power of two for each row.  Four warps a tile do the softmax, a thread a row, so maximum and
+// sum need no other thread.
 //
 // The scales stay out of the operands: with f = (the row's and the page's key scale) and the page's
 // value scale vs, the thread computes y = s f + log2(vs) for 16 keys at a time, P = 2^(y - m) with
 // m the running maximum of y less 7 (see kLift), in binary16 (2^-11, as fine as the output's type or
 // finer), and the denominator as sum P / vs in binary32.  m moves only when a P passes 2^15, and only
 // then O is rescaled.  Bound by the tensor cores and, as nearly, by the exponentials (16 an SM and clock).
-// Measured: 8192 tokens, 32 heads over 8 of 128 dimensions 514 us (1069 TFLOP/s of 1650); chunks of 2000
-// and 1700 tokens after 3000 and 6300: 347 us (950); 16 prompts of 1000: 263 us (500: a CTA's
+// Measured: 8192 tokens, 32 heads over 8 of 128 dimensions 520 us (1057 TFLOP/s of 1650); chunks of 2000
+// and 1700 tokens after 3000 and 6300: 354 us (932); 16 prompts of 1000: 270 us (486: a CTA's
 // lookups, first loads and output are half of its time there).
 #include <math.h>
 
@@ -277,7 +278,7 @@ __device__ __forceinline__ bool make_operands(Smem<D>& S, int n)
 // Its path from a tile's weights to the next products is every step's: it is one loop, not unrolled
 // over the tiles, within its registers, and descriptors are a 32-bit sum (8192 tokens of 32 heads
 // over 8: 590 us before, 541 us so).  All lanes run it, on values that are the same in all, and one
-// issues, so the operands stay in uniform registers; the weights are waited for last (514 us).
+// issues, so the operands stay in uniform registers; the weights are waited for last (514 us then).
 
 template <int D>
 __device__ __forceinline__ bool multiply(Smem<D>& S, const Work& W, uint32_t base)
