@@ -760,3 +760,12 @@ def test_attention_bad_spans_leave_their_rows(iqq, lens, new, heads):
                 torch.testing.assert_close(out[cu[b]:cu[b + 1]].float(), good[cu[b]:cu[b + 1]].float(),
                                            rtol=2.0 ** -7, atol=2e-3)
                 torch.testing.assert_close(lse[cu[b]:cu[b + 1]], good_lse[cu[b]:cu[b + 1]], rtol=1e-5, atol=1e-5)
+
+
+@pytest.mark.parametrize("keys", [1, 63, 500, 640, 704, 705, 960, 1024, 1100])
+@pytest.mark.parametrize("kv,group,dim", [(1, 8, 128), (8, 4, 64), (40, 1, 128)])
+def test_attention_one_short_sequence(iqq, keys, kv, group, dim):
+    """One token over tables on both sides of the lengths up to which a CTA takes a whole tile."""
+    c = Case(iqq, [keys], kv, dim, 64, 113)
+    c.tables = c.tables[:, :-(-keys // 64)].contiguous()
+    _check_attention(iqq, c, [1], kv * group, F16)
